@@ -4,11 +4,14 @@
 // touches no device state.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -1081,6 +1084,347 @@ dc_status dc_stream_rows_shaped(const void* src, int64_t src_ld_vec, int32_t row
                                                   rows_written, nvec, group, cap,
                                                   static_cast<hipStream_t>(stream)),
                     "shaped stream rows launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxSide = (int64_t)1 << 28;      // of a product's matrices
+constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of one of them
+constexpr int64_t kMaxUpdated = (int64_t)1 << 34;   // of a dc_matrix
+
+// A [rows, ld] matrix of `cols` columns where a model keeps it.
+struct Rows {
+  const char* name;
+  const void* p;
+  int64_t rows, cols, ld;
+  int32_t bytes;  // of an element
+};
+
+dc_status check_rows(const Rows& m) {
+  if (m.rows > 0 && m.p == nullptr) return fail(DC_ERR_NULL, "%s is NULL", m.name);
+  if (m.ld > kMaxExtent) return fail(DC_ERR_SHAPE, "%s: ld=%lld exceeds 2^44", m.name, (long long)m.ld);
+  if (m.ld < m.cols)
+    return fail(DC_ERR_SHAPE, "%s: ld=%lld < %lld columns", m.name, (long long)m.ld, (long long)m.cols);
+  if (m.rows > 1 && m.ld > (((int64_t)1 << 60) / m.rows))
+    return fail(DC_ERR_SHAPE, "%s: %lld rows of ld=%lld", m.name, (long long)m.rows, (long long)m.ld);
+  if (reinterpret_cast<uintptr_t>(m.p) % m.bytes != 0)
+    return fail(DC_ERR_ALIGN, "%s is not aligned to its elements", m.name);
+  return DC_OK;
+}
+
+// Whether the matrices share an element.  Column ranges of rows with one
+// stride interleave without sharing any.
+bool share(const Rows& a, const Rows& b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows <= 0 || b.rows <= 0) return false;
+  const int64_t na = ((a.rows - 1) * a.ld + a.cols) * a.bytes, nb = ((b.rows - 1) * b.ld + b.cols) * b.bytes;
+  if (!overlaps(a.p, na, b.p, nb)) return false;
+  const uint64_t step = (uint64_t)a.ld * a.bytes;
+  if (step != (uint64_t)b.ld * b.bytes) return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t d = pb >= pa ? (pb - pa) % step : (step - (pa - pb) % step) % step;
+  return d < (uint64_t)a.cols * a.bytes || d + (uint64_t)b.cols * b.bytes > step;
+}
+
+bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld && a.bytes == b.bytes; }
+
+// Output `o` against the inputs (and earlier outputs) in `others`; `may`: the
+// one that it may be, in place.
+dc_status check_apart(const Rows& o, std::initializer_list<const Rows*> others, const Rows* may = nullptr) {
+  for (const Rows* m : others) {
+    if (m == may && same(o, *m)) continue;
+    if (share(o, *m)) return fail(DC_ERR_ARG, "%s and %s overlap", o.name, m->name);
+  }
+  return DC_OK;
+}
+
+dc_status check_sizes(int64_t T, int64_t N, int64_t K) {
+  if (T < 0) return fail(DC_ERR_ARG, "T=%lld < 0", (long long)T);
+  if (N < 1 || K < 1) return fail(DC_ERR_ARG, "N=%lld or K=%lld < 1", (long long)N, (long long)K);
+  if (T > kMaxSide || N > kMaxSide || K > kMaxSide)
+    return fail(DC_ERR_SHAPE, "T=%lld, N=%lld or K=%lld exceeds 2^28", (long long)T, (long long)N, (long long)K);
+  if (T * N > kMaxElements || T * K > kMaxElements || N * K > kMaxElements)
+    return fail(DC_ERR_SHAPE, "T=%lld, N=%lld, K=%lld: a matrix exceeds 2^36 elements", (long long)T, (long long)N,
+                (long long)K);
+  return DC_OK;
+}
+
+dc_status check_act(int32_t act) {
+  if (act < DC_ACT_NONE || act > DC_ACT_SILU) return fail(DC_ERR_ARG, "act=%d", act);
+  return DC_OK;
+}
+
+dc_status check_grad_dtype(int32_t dtype, int32_t grad_dtype) {
+  if (grad_dtype != DC_F32 && grad_dtype != dtype)
+    return fail(DC_ERR_DTYPE, "grad_dtype %d is neither DC_F32 nor dtype", grad_dtype);
+  return DC_OK;
+}
+
+dc_status check_workspace(const void* p, int64_t have, int64_t need) {
+  if (need == 0) return DC_OK;
+  if (have < need)
+    return fail(DC_ERR_SHAPE, "workspace_bytes=%lld, %lld are needed", (long long)have, (long long)need);
+  if (p == nullptr) return fail(DC_ERR_NULL, "workspace is NULL");
+  if (!aligned16(p)) return fail(DC_ERR_ALIGN, "workspace is not 16-byte aligned");
+  return DC_OK;
+}
+
+dc_status check_matrices(const dc_matrix* mats, int32_t num) {
+  if (num < 0 || num > 1 << 20) return fail(DC_ERR_ARG, "num=%d outside [0, 2^20]", num);
+  if (num > 0 && mats == nullptr) return fail(DC_ERR_NULL, "mats is NULL");
+  for (int32_t k = 0; k < num; ++k) {
+    const dc_matrix& m = mats[k];
+    if (m.rows < 1 || m.cols < 1) return fail(DC_ERR_ARG, "matrix %d: %d x %d", k, m.rows, m.cols);
+    if (m.rows > kMaxSide || m.cols > kMaxSide || (int64_t)m.rows * m.cols > kMaxUpdated)
+      return fail(DC_ERR_SHAPE, "matrix %d: %d x %d exceeds 2^28 a side or 2^34 elements", k, m.rows, m.cols);
+  }
+  return DC_OK;
+}
+
+dc_status check_steps(int32_t steps, const float* coeffs, float eps) {
+  if (steps < 1 || steps > DC_NS_MAX_STEPS)
+    return fail(DC_ERR_ARG, "steps=%d outside [1, %d]", steps, DC_NS_MAX_STEPS);
+  if (coeffs == nullptr) return fail(DC_ERR_NULL, "coeffs is NULL");
+  for (int32_t k = 0; k < 3 * steps; ++k)
+    if (!std::isfinite(coeffs[k])) return fail(DC_ERR_ARG, "coeffs[%d] is not finite", k);
+  if (!(eps >= 0) || !std::isfinite(eps)) return fail(DC_ERR_ARG, "eps=%g", (double)eps);
+  const double top = dc::ns_largest(steps, coeffs);
+  if (!(top < 64)) return fail(DC_ERR_ARG, "the steps diverge: a singular value may reach %g", top);
+  return DC_OK;
+}
+
+// Every written matrix against everything else that the list names.  Sorted
+// by address, only neighbours whose byte ranges meet are compared.
+struct Named {
+  Rows m;
+  int32_t matrix;
+  bool written;
+};
+
+dc_status check_disjoint(std::vector<Named>& all, bool in_place) {
+  auto from = [](const Named& x) { return reinterpret_cast<uintptr_t>(x.m.p); };
+  auto to = [&](const Named& x) {
+    return from(x) + (uint64_t)((x.m.rows - 1) * x.m.ld + x.m.cols) * x.m.bytes;
+  };
+  std::sort(all.begin(), all.end(), [&](const Named& x, const Named& y) { return from(x) < from(y); });
+  for (size_t i = 0; i < all.size(); ++i)
+    for (size_t j = i + 1; j < all.size() && from(all[j]) < to(all[i]); ++j) {
+      const Named &x = all[i], &y = all[j];
+      if (!x.written && !y.written) continue;
+      if (in_place && x.matrix == y.matrix && x.written != y.written && same(x.m, y.m)) continue;
+      if (share(x.m, y.m))
+        return fail(DC_ERR_ARG, "%s of matrix %d and %s of matrix %d overlap", x.m.name, x.matrix, y.m.name,
+                    y.matrix);
+    }
+  return DC_OK;
+}
+
+// The checks that both list operators share.
+dc_status check_list(int32_t dtype, int32_t out_dtype, const dc_matrix* mats, int32_t num, bool update) {
+  dc_status st;
+  if ((st = check_matrices(mats, num))) return st;
+  std::vector<Named> all;
+  try {
+    all.reserve((size_t)num * 3);
+  } catch (const std::bad_alloc&) {
+    return fail(DC_ERR_UNSUPPORTED, "no host memory to check %d matrices", num);
+  }
+  for (int32_t k = 0; k < num; ++k) {
+    const dc_matrix& m = mats[k];
+    const Rows g{"grad", m.grad, m.rows, m.cols, m.ld_grad, elem_bytes(dtype)};
+    const Rows o{"out", m.out, m.rows, m.cols, m.ld_out, elem_bytes(out_dtype)};
+    if ((st = check_rows(g)) || (st = check_rows(o))) {
+      g_last_error = "matrix " + std::to_string(k) + ": " + g_last_error;
+      return st;
+    }
+    all.push_back({g, k, false});
+    all.push_back({o, k, true});
+    if (update) {
+      const Rows mo{"momentum", m.momentum, m.rows, m.cols, m.cols, 4};
+      if ((st = check_rows(mo))) {
+        g_last_error = "matrix " + std::to_string(k) + ": " + g_last_error;
+        return st;
+      }
+      all.push_back({mo, k, true});
+    }
+  }
+  return check_disjoint(all, !update);
+}
+
+}  // namespace
+
+extern "C" {
+
+dc_status dc_linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t* bytes) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, K))) return st;
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::linear_workspace(dtype, T, N, K);
+  return ok();
+}
+
+dc_status dc_linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t* bytes) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, K))) return st;
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::linear_backward_workspace(dtype, T, N, K);
+  return ok();
+}
+
+dc_status dc_bias_act_workspace(int32_t dtype, int64_t T, int64_t N, int64_t* bytes) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, 1))) return st;
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::bias_act_workspace(dtype, T, N);
+  return ok();
+}
+
+dc_status dc_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x,
+                    const void* w, int64_t ld_w, const void* bias, const void* residual,
+                    int64_t ld_res, int32_t act, void* pre, int64_t ld_pre, void* y, int64_t ld_y,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, K)) || (st = check_act(act))) return st;
+  const int32_t e = elem_bytes(dtype);
+  const Rows mx{"x", x, T, K, ld_x, e}, mw{"w", w, N, K, ld_w, e}, mb{"bias", bias, 1, N, N, e},
+      mr{"residual", residual, T, N, ld_res, e}, mp{"pre", pre, T, N, ld_pre, e}, my{"y", y, T, N, ld_y, e};
+  if ((st = check_rows(mx)) || (st = check_rows(mw)) || (st = check_rows(my))) return st;
+  if ((bias && (st = check_rows(mb))) || (residual && (st = check_rows(mr))) || (pre && (st = check_rows(mp))))
+    return st;
+  if ((st = check_apart(my, {&mx, &mw, &mb, &mr}, &mr)) || (st = check_apart(mp, {&mx, &mw, &mb, &mr, &my})))
+    return st;
+  if ((st = check_workspace(workspace, workspace_bytes, dc::linear_workspace(dtype, T, N, K)))) return st;
+  const dc::LinearOut o{y, ld_y, bias, residual, ld_res, pre, ld_pre, act, 0};
+  return hip_status(dc::launch_linear(dtype, T, N, K, x, ld_x, w, ld_w, o, workspace,
+                                      static_cast<hipStream_t>(stream)),
+                    "linear launch");
+}
+
+dc_status dc_bias_act_backward(int32_t dtype, int64_t T, int64_t N, const void* dy, int64_t ld_dy,
+                               const void* pre, int64_t ld_pre, int32_t act, void* dz,
+                               int64_t ld_dz, int32_t grad_dtype, void* db, int32_t accumulate,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, 1)) || (st = check_act(act)) ||
+      (st = check_grad_dtype(dtype, grad_dtype)))
+    return st;
+  if (accumulate != 0 && accumulate != 1) return fail(DC_ERR_ARG, "accumulate=%d", accumulate);
+  if (dz == nullptr && db == nullptr) return fail(DC_ERR_NULL, "dz and db are both NULL");
+  const int32_t e = elem_bytes(dtype);
+  const Rows my{"dy", dy, T, N, ld_dy, e}, mp{"pre", pre, T, N, ld_pre, e}, mz{"dz", dz, T, N, ld_dz, e},
+      mb{"db", db, 1, N, N, elem_bytes(grad_dtype)};
+  if ((st = check_rows(my))) return st;
+  if (act != DC_ACT_NONE && (st = check_rows(mp))) return st;
+  if ((dz && (st = check_rows(mz))) || (db && (st = check_rows(mb)))) return st;
+  if (act == DC_ACT_NONE) pre = nullptr;
+  const Rows used{"pre", pre, T, N, ld_pre, e};
+  if ((st = check_apart(mz, {&my, &used}, &my)) || (st = check_apart(mb, {&my, &used, &mz}))) return st;
+  if (db && (st = check_workspace(workspace, workspace_bytes, dc::bias_act_workspace(dtype, T, N)))) return st;
+  return hip_status(dc::launch_bias_act(dtype, grad_dtype, T, N, dy, ld_dy, pre, ld_pre, act, dz, ld_dz, db,
+                                        accumulate, workspace, static_cast<hipStream_t>(stream)),
+                    "bias-act backward launch");
+}
+
+dc_status dc_linear_backward(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* dz,
+                             int64_t ld_dz, const void* w, int64_t ld_w, const void* x, int64_t ld_x,
+                             void* dx, int64_t ld_dx, int32_t grad_dtype, void* dw, int64_t ld_dw,
+                             int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                             void* stream) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, K)) || (st = check_grad_dtype(dtype, grad_dtype)))
+    return st;
+  if (accumulate != 0 && accumulate != 1) return fail(DC_ERR_ARG, "accumulate=%d", accumulate);
+  if (dx == nullptr && dw == nullptr) return fail(DC_ERR_NULL, "dx and dw are both NULL");
+  const int32_t e = elem_bytes(dtype);
+  const Rows mz{"dz", dz, T, N, ld_dz, e}, mw{"w", dx ? w : nullptr, N, K, ld_w, e},
+      mx{"x", dw ? x : nullptr, T, K, ld_x, e}, ox{"dx", dx, T, K, ld_dx, e},
+      ow{"dw", dw, N, K, ld_dw, elem_bytes(grad_dtype)};
+  if ((st = check_rows(mz))) return st;
+  if (dx && ((st = check_rows(mw)) || (st = check_rows(ox)))) return st;
+  if (dw && ((st = check_rows(mx)) || (st = check_rows(ow)))) return st;
+  if ((st = check_apart(ox, {&mz, &mw, &mx})) || (st = check_apart(ow, {&mz, &mw, &mx, &ox}))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, dc::linear_backward_workspace(dtype, T, N, K)))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dx) {
+    dc::LinearOut o{};
+    o.out = dx;
+    o.ld_out = ld_dx;
+    if ((st = hip_status(dc::launch_linear_dx(dtype, T, N, K, dz, ld_dz, w, ld_w, o, workspace, s), "dx launch")))
+      return st;
+  }
+  if (dw) {
+    dc::LinearOut o{};
+    o.out = dw;
+    o.ld_out = ld_dw;
+    o.accumulate = accumulate;
+    if ((st = hip_status(dc::launch_linear_dw(dtype, grad_dtype, T, N, K, dz, ld_dz, x, ld_x, o, workspace, s),
+                         "dw launch")))
+      return st;
+  }
+  return ok();
+}
+
+dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32_t num, int64_t* bytes) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_matrices(mats, num))) return st;
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::ns_workspace(dtype, mats, num);
+  return ok();
+}
+
+dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, int32_t steps,
+                           const float* coeffs, float eps, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_steps(steps, coeffs, eps)) ||
+      (st = check_list(dtype, dtype, mats, num, false)) ||
+      (st = check_workspace(workspace, workspace_bytes, dc::ns_workspace(dtype, mats, num))))
+    return st;
+  dc::NsLaunch a{};
+  a.dtype = a.out_dtype = dtype;
+  a.mats = mats;
+  a.num = num;
+  a.steps = steps;
+  a.coeffs = coeffs;
+  a.eps = eps;
+  a.workspace = workspace;
+  return hip_status(dc::launch_ns(a, static_cast<hipStream_t>(stream)), "orthogonalize launch");
+}
+
+dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, const dc_matrix* mats, int32_t num,
+                         float lr, const float* lr_scale, float mu, int32_t nesterov,
+                         float weight_decay, int32_t scale_mode, int32_t steps,
+                         const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_dtype(weight_dtype)) || (st = check_steps(steps, coeffs, eps)))
+    return st;
+  if (!std::isfinite(lr) || !std::isfinite(mu) || !std::isfinite(weight_decay))
+    return fail(DC_ERR_ARG, "lr=%g mu=%g weight_decay=%g", (double)lr, (double)mu, (double)weight_decay);
+  if (nesterov != 0 && nesterov != 1) return fail(DC_ERR_ARG, "nesterov=%d", nesterov);
+  if (scale_mode < DC_SCALE_NONE || scale_mode > DC_SCALE_RMS) return fail(DC_ERR_ARG, "scale_mode=%d", scale_mode);
+  if (reinterpret_cast<uintptr_t>(lr_scale) % 4 != 0) return fail(DC_ERR_ALIGN, "lr_scale is not aligned");
+  if ((st = check_list(dtype, weight_dtype, mats, num, true)) ||
+      (st = check_workspace(workspace, workspace_bytes, dc::ns_workspace(dtype, mats, num))))
+    return st;
+  dc::NsLaunch a{};
+  a.dtype = dtype;
+  a.out_dtype = weight_dtype;
+  a.update = true;
+  a.mats = mats;
+  a.num = num;
+  a.steps = steps;
+  a.coeffs = coeffs;
+  a.eps = eps;
+  a.mu = mu;
+  a.lr = lr;
+  a.weight_decay = weight_decay;
+  a.nesterov = nesterov;
+  a.scale_mode = scale_mode;
+  a.lr_scale = lr_scale;
+  a.workspace = workspace;
+  return hip_status(dc::launch_ns(a, static_cast<hipStream_t>(stream)), "update launch");
 }
 
 }  // extern "C"

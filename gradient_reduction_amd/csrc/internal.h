@@ -174,4 +174,61 @@ hipError_t launch_stream_rows_shaped(const void* src, int64_t src_ld_vec, int32_
                                      void* dst, int64_t dst_ld_vec, int32_t rows_written,
                                      int64_t nvec, int32_t group, int32_t cap, hipStream_t stream);
 
+// What a linear layer's product writes: y = act(v + bias) + residual and
+// pre = v + bias forward, out = (accumulate ? out : 0) + v backward.  NULL
+// pointers leave their part out.
+struct LinearOut {
+  void* out;
+  int64_t ld_out;
+  const void* bias;
+  const void* residual;
+  int64_t ld_res;
+  void* pre;
+  int64_t ld_pre;
+  int32_t act;
+  int32_t accumulate;
+};
+
+// Bytes of workspace that the launches below need (0: none).
+int64_t linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K);
+int64_t linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K);
+int64_t bias_act_workspace(int32_t dtype, int64_t T, int64_t N);
+
+hipError_t launch_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x, const void* w,
+                         int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream);
+
+hipError_t launch_linear_dx(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* dz, int64_t ld_dz,
+                            const void* w, int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream);
+
+hipError_t launch_linear_dw(int32_t dtype, int32_t grad_dtype, int64_t T, int64_t N, int64_t K, const void* dz,
+                            int64_t ld_dz, const void* x, int64_t ld_x, const LinearOut& o, void* workspace,
+                            hipStream_t stream);
+
+hipError_t launch_bias_act(int32_t dtype, int32_t grad_dtype, int64_t T, int64_t N, const void* dy, int64_t ld_dy,
+                           const void* pre, int64_t ld_pre, int act, void* dz, int64_t ld_dz, void* db,
+                           int accumulate, void* workspace, hipStream_t stream);
+
+// A list of matrices orthogonalised, into `out` (update false) or as the
+// momentum's update of the weights `out`.
+struct NsLaunch {
+  int32_t dtype;      // of the gradients, and of `out` when update is false
+  int32_t out_dtype;  // of the weights
+  bool update;
+  const dc_matrix* mats;  // host
+  int32_t num;
+  int32_t steps;
+  const float* coeffs;  // host [steps][3]
+  float eps;
+  float mu, lr, weight_decay;
+  int32_t nesterov, scale_mode;
+  const float* lr_scale;  // device, or NULL
+  void* workspace;
+};
+
+float ns_factor(int32_t scale_mode, int32_t rows, int32_t cols);
+// Upper bound of every singular value at any step.
+double ns_largest(int32_t steps, const float* coeffs);
+int64_t ns_workspace(int32_t dtype, const dc_matrix* mats, int32_t num);
+hipError_t launch_ns(const NsLaunch& a, hipStream_t stream);
+
 }  // namespace dc

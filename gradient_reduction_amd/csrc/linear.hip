@@ -1,0 +1,332 @@
+// The linear layer's kernels: forward product with bias, activation and
+// residual in its epilogue, the bias-and-activation backward, and the two
+// backward products.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "product.h"
+
+namespace dc {
+namespace {
+
+// act(v) and its slope, in fp32.  gelu is the exact one: v Phi(v), with
+// Phi(v) = erfc(-v / sqrt 2) / 2, which keeps its relative accuracy in the
+// lower tail.
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case DC_ACT_RELU: return v > 0.f || v != v ? v : 0.f;
+    case DC_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    case DC_ACT_SILU: return v / (1.f + expf(-v));
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float activation_slope(float v, int act) {
+  switch (act) {
+    case DC_ACT_RELU: return v > 0.f ? 1.f : 0.f;
+    case DC_ACT_GELU:
+      return 0.5f * erfcf(-0.70710678118654752f * v) + 0.39894228040143268f * v * expf(-0.5f * v * v);
+    case DC_ACT_SILU: {
+      const float p = 1.f / (1.f + expf(-v));
+      return p * (1.f + v * (1.f - p));
+    }
+    default: return 1.f;
+  }
+}
+
+// What happens to the sums of columns j .. j + 3 of row i.
+template <class T>
+struct LinearEpilogue {  // y = act(v + bias) + residual, pre = v + bias
+  LinearOut o;
+  int64_t n_cols;
+  __device__ void operator()(int64_t i, int64_t j, f32x4 v) const {
+    const int n = (int)(n_cols - j < 4 ? n_cols - j : 4);
+    if (o.bias) v += load4(static_cast<const T*>(o.bias) + j, n);
+    if (o.pre) store4(static_cast<T*>(o.pre) + i * o.ld_pre + j, v, n);
+    if (o.act != DC_ACT_NONE) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) v[t] = activate(v[t], o.act);
+    }
+    if (o.residual) v += load4(static_cast<const T*>(o.residual) + i * o.ld_res + j, n);
+    store4(static_cast<T*>(o.out) + i * o.ld_out + j, v, n);
+  }
+};
+
+template <class G>
+struct GradEpilogue {  // out = (accumulate ? out : 0) + v
+  LinearOut o;
+  int64_t n_cols;
+  __device__ void operator()(int64_t i, int64_t j, f32x4 v) const {
+    const int n = (int)(n_cols - j < 4 ? n_cols - j : 4);
+    G* p = static_cast<G*>(o.out) + i * o.ld_out + j;
+    if (o.accumulate) v += load4(p, n);
+    store4(p, v, n);
+  }
+};
+
+struct ProductArgs {
+  const void *a, *b;
+  int64_t ld_a, ld_b;
+  int64_t m, n, k;
+  int64_t tiles_m, tiles_n;
+  int32_t splits;
+  int64_t k_per_split;  // a multiple of the stage depth
+  float* partial;       // [splits][m][n rounded up to 4] when splits > 1
+  int64_t ld_partial;
+};
+
+template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, class Epi>
+__global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi) {
+  using P = TileProduct<T, BM, BN, WM, WN, KCA, KCB>;
+  __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+  const int64_t per = g.tiles_m * g.tiles_n;
+  const int64_t t = xcd_run(blockIdx.x, gridDim.x);
+  const int32_t split = (int32_t)(t / per);
+  int64_t ti, tj;
+  band_tile(t - split * per, g.tiles_m, g.tiles_n, 8, ti, tj);
+  const int64_t i0 = ti * BM, j0 = tj * BN;
+  Operand<T> a{static_cast<const T*>(g.a) + (KCA ? i0 * g.ld_a : i0), g.ld_a,
+               (int32_t)(g.m - i0 < BM ? g.m - i0 : BM)};
+  Operand<T> b{static_cast<const T*>(g.b) + (KCB ? j0 * g.ld_b : j0), g.ld_b,
+               (int32_t)(g.n - j0 < BN ? g.n - j0 : BN)};
+  const int64_t k0 = split * g.k_per_split;
+  const int64_t k1 = k0 + g.k_per_split < g.k ? k0 + g.k_per_split : g.k;
+  f32x4 acc[P::MI][P::NI] = {};
+  P::run(a, b, k0, k1, lds, acc);
+  if (g.splits > 1) {
+    float* out = g.partial + split * g.m * g.ld_partial;
+    P::each(acc, [&](int i, int j, f32x4 v) {
+      if (i < a.rows && j < b.rows) store4(out + (i0 + i) * g.ld_partial + j0 + j, v, 4);
+    });
+  } else {
+    P::each(acc, [&](int i, int j, f32x4 v) {
+      if (i < a.rows && j < b.rows) epi(i0 + i, j0 + j, v);
+    });
+  }
+}
+
+// The splits of a long k added in their order, then the epilogue.
+template <class Epi>
+__global__ void __launch_bounds__(256) k_product_join(const float* partial, int64_t ld, int32_t splits, int64_t m,
+                                                      int64_t n, Epi epi) {
+  const int64_t groups = (n + 3) / 4;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= m * groups) return;
+  const int64_t i = at / groups, j = (at - i * groups) * 4;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int32_t s = 0; s < splits; ++s)
+    v += *reinterpret_cast<const f32x4*>(partial + ((int64_t)s * m + i) * ld + j);
+  epi(i, j, v);
+}
+
+// How a product of m x n over k is cut: 128 x 128 tiles when those (with k
+// split at 16 stages or more) give every compute unit work, else 64 x 64.
+struct Cut {
+  int32_t tile, splits;
+  int64_t k_per_split, ld_partial;
+  int64_t partial_bytes(int64_t m) const { return splits > 1 ? splits * m * ld_partial * 4 : 0; }
+};
+
+Cut cut(int32_t dtype, int64_t m, int64_t n, int64_t k) {
+  constexpr int64_t kUnits = 256;  // compute units
+  const int64_t bk = dtype == DC_F32 ? 32 : 64;
+  const int64_t stages = std::max<int64_t>(1, (k + bk - 1) / bk);
+  Cut c;
+  auto tiles = [&](int64_t b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
+  const int64_t most = std::max<int64_t>(1, stages / 8);
+  c.tile = tiles(128) * most >= kUnits ? 128 : 64;
+  const int64_t t = std::max<int64_t>(1, tiles(c.tile));
+  int64_t s = t >= kUnits ? 1 : std::min<int64_t>(most, (kUnits + t - 1) / t);
+  const int64_t per = (stages + s - 1) / s;
+  c.splits = (int32_t)((stages + per - 1) / per);
+  c.k_per_split = per * bk;
+  c.ld_partial = (n + 3) / 4 * 4;
+  return c;
+}
+
+template <class T, bool KCA, bool KCB, class Epi>
+hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t m, int64_t n,
+                   int64_t k, float* partial, const Epi& epi, hipStream_t stream) {
+  const Cut c = cut(dtype, m, n, k);
+  ProductArgs g{a, b, ld_a, ld_b, m, n, k, (m + c.tile - 1) / c.tile, (n + c.tile - 1) / c.tile, c.splits,
+                c.k_per_split, partial, c.ld_partial};
+  const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n * c.splits));
+  if (c.tile == 128) k_product<T, 128, 128, 2, 2, KCA, KCB, Epi><<<grid, 256, 0, stream>>>(g, epi);
+  else k_product<T, 64, 64, 2, 2, KCA, KCB, Epi><<<grid, 256, 0, stream>>>(g, epi);
+  if (c.splits > 1) {
+    const int64_t groups = m * ((n + 3) / 4);
+    k_product_join<Epi><<<dim3((uint32_t)((groups + 255) / 256)), 256, 0, stream>>>(partial, c.ld_partial, c.splits,
+                                                                                  m, n, epi);
+  }
+  return hipGetLastError();
+}
+
+// dz = dy act'(pre) and the column sums of dz, in strips of `strip` rows: one
+// workgroup per 32 chunks of 16 bytes of columns and strip, eight rows at a
+// time.  The strips' sums go to partial[strip][n] and are added in order by
+// k_column_join, or straight to db when there is one strip.
+template <class T, class G>
+__global__ void __launch_bounds__(256) k_bias_act(int64_t rows, int64_t n, const T* dy, int64_t ld_dy, const T* pre,
+                                                  int64_t ld_pre, int act, T* dz, int64_t ld_dz, float* partial,
+                                                  G* db, int accumulate, int64_t strip) {
+  constexpr int V = 16 / sizeof(T);
+  __shared__ float sum[8][32][V + 1];
+  const int c = threadIdx.x & 31, l = threadIdx.x >> 5;
+  const int64_t j = ((int64_t)blockIdx.x * 32 + c) * V;
+  const int64_t i0 = (int64_t)blockIdx.y * strip, i1 = i0 + strip < rows ? i0 + strip : rows;
+  const int64_t left = n - j;
+  float s[V] = {};
+  if (left > 0) {
+    for (int64_t i = i0 + l; i < i1; i += 8) {
+      T d[V] = {}, z[V] = {};
+      if (left >= V) {
+        __builtin_memcpy(d, dy + i * ld_dy + j, 16);
+        if (pre) __builtin_memcpy(z, pre + i * ld_pre + j, 16);
+      } else {
+#pragma unroll
+        for (int t = 0; t < V; ++t)
+          if (t < left) {
+            d[t] = dy[i * ld_dy + j + t];
+            if (pre) z[t] = pre[i * ld_pre + j + t];
+          }
+      }
+      T o[V];
+#pragma unroll
+      for (int t = 0; t < V; ++t) {
+        float v = (float)d[t];
+        if (pre) v *= activation_slope((float)z[t], act);
+        s[t] += v;
+        o[t] = (T)v;
+      }
+      if (dz) {
+        if (left >= V) {
+          __builtin_memcpy(dz + i * ld_dz + j, o, 16);
+        } else {
+#pragma unroll
+          for (int t = 0; t < V; ++t)
+            if (t < left) dz[i * ld_dz + j + t] = o[t];
+        }
+      }
+    }
+  }
+  if (!db) return;
+#pragma unroll
+  for (int t = 0; t < V; ++t) sum[l][c][t] = s[t];
+  __syncthreads();
+  if (threadIdx.x < 32 * V) {
+    const int cc = threadIdx.x / V, t = threadIdx.x % V;
+    const int64_t jj = ((int64_t)blockIdx.x * 32 + cc) * V + t;
+    if (jj < n) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v += sum[w][cc][t];
+      if (gridDim.y > 1) partial[(int64_t)blockIdx.y * n + jj] = v;
+      else db[jj] = (G)(accumulate ? (float)db[jj] + v : v);
+    }
+  }
+}
+
+template <class G>
+__global__ void __launch_bounds__(256) k_column_join(const float* partial, int32_t strips, int64_t n, G* db,
+                                                     int accumulate) {
+  __shared__ float sum[8][32];
+  const int c = threadIdx.x & 31, l = threadIdx.x >> 5;
+  const int64_t j = (int64_t)blockIdx.x * 32 + c;
+  float v = 0.f;
+  if (j < n)
+    for (int32_t s = l; s < strips; s += 8) v += partial[(int64_t)s * n + j];
+  sum[l][c] = v;
+  __syncthreads();
+  if (l == 0 && j < n) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sum[w][c];
+    db[j] = (G)(accumulate ? (float)db[j] + t : t);
+  }
+}
+
+// Rows per strip: about 2048 workgroups over the chip, at least 32 rows each.
+int64_t strip_rows(int32_t dtype, int64_t rows, int64_t n) {
+  const int64_t per = dtype == DC_F32 ? 128 : 256;
+  const int64_t across = (n + per - 1) / per;
+  const int64_t strips = std::max<int64_t>(1, 2048 / across);
+  const int64_t r = std::max<int64_t>(32, (rows + strips - 1) / strips);
+  return (r + 7) / 8 * 8;
+}
+
+template <class T, class G>
+hipError_t bias_act(int32_t dtype, int64_t rows, int64_t n, const void* dy, int64_t ld_dy, const void* pre,
+                    int64_t ld_pre, int act, void* dz, int64_t ld_dz, void* db, int accumulate, float* partial,
+                    hipStream_t stream) {
+  const int64_t strip = strip_rows(dtype, rows, n);
+  const int64_t strips = std::max<int64_t>(1, (rows + strip - 1) / strip);
+  constexpr int64_t per = 32 * (16 / sizeof(T));
+  const dim3 grid((uint32_t)((n + per - 1) / per), (uint32_t)strips);
+  k_bias_act<T, G><<<grid, 256, 0, stream>>>(rows, n, static_cast<const T*>(dy), ld_dy, static_cast<const T*>(pre),
+                                             ld_pre, act, static_cast<T*>(dz), ld_dz, partial, static_cast<G*>(db),
+                                             accumulate, strip);
+  if (db && strips > 1)
+    k_column_join<G><<<dim3((uint32_t)((n + 31) / 32)), 256, 0, stream>>>(partial, (int32_t)strips, n,
+                                                                         static_cast<G*>(db), accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K) {
+  return cut(dtype, T, N, K).partial_bytes(T);
+}
+
+int64_t linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K) {
+  return std::max(cut(dtype, T, K, N).partial_bytes(T), cut(dtype, N, K, T).partial_bytes(N));
+}
+
+int64_t bias_act_workspace(int32_t dtype, int64_t T, int64_t N) {
+  const int64_t strip = strip_rows(dtype, T, N), strips = (T + strip - 1) / strip;
+  return strips > 1 ? strips * N * 4 : 0;
+}
+
+hipError_t launch_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x, const void* w,
+                         int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  float* ws = static_cast<float*>(workspace);
+  if (dtype == DC_BF16)
+    return product<__bf16, true, true>(dtype, x, ld_x, w, ld_w, T, N, K, ws, LinearEpilogue<__bf16>{o, N}, stream);
+  return product<float, true, true>(dtype, x, ld_x, w, ld_w, T, N, K, ws, LinearEpilogue<float>{o, N}, stream);
+}
+
+hipError_t launch_linear_dx(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* dz, int64_t ld_dz,
+                            const void* w, int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  float* ws = static_cast<float*>(workspace);
+  if (dtype == DC_BF16)
+    return product<__bf16, true, false>(dtype, dz, ld_dz, w, ld_w, T, K, N, ws, GradEpilogue<__bf16>{o, K}, stream);
+  return product<float, true, false>(dtype, dz, ld_dz, w, ld_w, T, K, N, ws, GradEpilogue<float>{o, K}, stream);
+}
+
+hipError_t launch_linear_dw(int32_t dtype, int32_t grad_dtype, int64_t T, int64_t N, int64_t K, const void* dz,
+                            int64_t ld_dz, const void* x, int64_t ld_x, const LinearOut& o, void* workspace,
+                            hipStream_t stream) {
+  if (T == 0 && o.accumulate) return hipSuccess;
+  float* ws = static_cast<float*>(workspace);
+  if (dtype == DC_F32)
+    return product<float, false, false>(dtype, dz, ld_dz, x, ld_x, N, K, T, ws, GradEpilogue<float>{o, K}, stream);
+  if (grad_dtype == DC_F32)
+    return product<__bf16, false, false>(dtype, dz, ld_dz, x, ld_x, N, K, T, ws, GradEpilogue<float>{o, K}, stream);
+  return product<__bf16, false, false>(dtype, dz, ld_dz, x, ld_x, N, K, T, ws, GradEpilogue<__bf16>{o, K}, stream);
+}
+
+hipError_t launch_bias_act(int32_t dtype, int32_t grad_dtype, int64_t T, int64_t N, const void* dy, int64_t ld_dy,
+                           const void* pre, int64_t ld_pre, int act, void* dz, int64_t ld_dz, void* db,
+                           int accumulate, void* workspace, hipStream_t stream) {
+  float* ws = static_cast<float*>(workspace);
+  if (dtype == DC_F32)
+    return bias_act<float, float>(dtype, T, N, dy, ld_dy, pre, ld_pre, act, dz, ld_dz, db, accumulate, ws, stream);
+  if (grad_dtype == DC_F32)
+    return bias_act<__bf16, float>(dtype, T, N, dy, ld_dy, pre, ld_pre, act, dz, ld_dz, db, accumulate, ws, stream);
+  return bias_act<__bf16, __bf16>(dtype, T, N, dy, ld_dy, pre, ld_pre, act, dz, ld_dz, db, accumulate, ws, stream);
+}
+
+}  // namespace dc

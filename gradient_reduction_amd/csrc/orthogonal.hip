@@ -1,0 +1,476 @@
+// Orthogonalising matrices by Newton-Schulz products, and the momentum update
+// that uses it.  For every matrix G (rows x cols; m = the smaller side, n the
+// larger, G transposed where rows > cols):
+//   X <- U / (|U|_F + eps)              U = G, or the momentum's look-ahead
+//   repeat: A = X XT; B = b A + c A A; X <- a X + B X
+//   O = X, or W <- (1 - lr wd) W - lr s X
+// Every step is one launch for a chunk of up to kNsChunk matrices: a workgroup
+// finds its matrix by its tile number.  A and B are symmetric, so only tiles
+// on and above their diagonal are computed and each is written twice.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "product.h"
+
+namespace dc {
+namespace {
+
+constexpr int kNsChunk = 40;          // matrices per launch: their table is a kernel argument
+constexpr int kNormParts = 256;       // partial sums of squares per matrix, at most
+constexpr int64_t kNormSpan = 16384;  // elements per partial sum, at least
+
+// One matrix of a chunk.  Its planes in the workspace, in values from the
+// planes' base: X [m][ldx], the next X [m][ldx], A [m][lda], B [m][lda].
+struct NsMatrix {
+  const void* grad;
+  void* out;
+  float* momentum;
+  int64_t ld_grad, ld_out;
+  int64_t base;
+  int32_t rows, cols;
+  float scale;  // lr times the shape's factor (update only)
+};
+
+struct NsTable {
+  int32_t count;
+  NsMatrix m[kNsChunk];
+};
+
+// First tile of every matrix of the chunk, and their number.
+struct NsTiles {
+  int32_t begin[kNsChunk + 1];
+};
+
+static_assert(sizeof(NsTable) + sizeof(NsTiles) + 128 <= 4096, "kernel arguments");
+
+__host__ __device__ inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+__host__ __device__ inline int64_t up128(int64_t v) { return (v + 127) / 128 * 128; }
+
+struct NsShape {
+  int64_t m, n, ldx, lda, x_size, a_size;
+  bool flip;  // X is G transposed
+  __host__ __device__ NsShape(int64_t rows, int64_t cols) {
+    flip = rows > cols;
+    m = flip ? cols : rows;
+    n = flip ? rows : cols;
+    ldx = up8(n);
+    lda = up8(m);
+    x_size = up128(m * ldx);
+    a_size = up128(m * lda);
+  }
+  __host__ __device__ int64_t values() const { return 2 * (x_size + a_size); }
+};
+
+__host__ __device__ inline int32_t norm_parts(int64_t rows, int64_t cols) {
+  const int64_t p = (rows * cols + kNormSpan - 1) / kNormSpan;
+  return (int32_t)(p < 1 ? 1 : p > kNormParts ? kNormParts : p);
+}
+
+// The matrix of tile t: the last one whose first tile is at or before t.
+__device__ __forceinline__ int find_matrix(const NsTiles& tiles, int count, int32_t t) {
+  int lo = 0, hi = count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tiles.begin[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+struct NsUpdate {
+  float mu, decay;   // decay = lr wd
+  int32_t nesterov;
+  const float* lr_scale;  // device, or null
+};
+
+// |U|_F^2 in parts, in fp64 (fp32 gradients of 1e-30 and 1e30 both have a
+// square there), and the momentum's step: m <- mu m + g.
+template <class G, bool MOM>
+__global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsUpdate up, double* parts) {
+  const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
+  const NsMatrix& x = tab.m[e];
+  const int part = (int)blockIdx.x - tiles.begin[e], np = tiles.begin[e + 1] - tiles.begin[e];
+  const int64_t per_row = (x.cols + 3) / 4, groups = x.rows * per_row;
+  const G* grad = static_cast<const G*>(x.grad);
+  double s = 0;
+  for (int64_t q = (int64_t)part * 256 + threadIdx.x; q < groups; q += (int64_t)np * 256) {
+    int64_t r, c;
+    if (groups < ((int64_t)1 << 31)) {
+      r = (uint32_t)q / (uint32_t)per_row;
+      c = ((uint32_t)q - (uint32_t)r * (uint32_t)per_row) * (int64_t)4;
+    } else {
+      r = q / per_row;
+      c = (q - r * per_row) * 4;
+    }
+    const int n = (int)(x.cols - c < 4 ? x.cols - c : 4);
+    f32x4 u = load4(grad + r * x.ld_grad + c, n);
+    if constexpr (MOM) {
+      float* mp = x.momentum + r * x.cols + c;
+      const f32x4 g = u;
+      u = load4(mp, n);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = fmaf(up.mu, u[t], g[t]);
+      store4(mp, u, n);
+      if (up.nesterov) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t] = fmaf(up.mu, u[t], g[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) s = fma((double)u[t], (double)u[t], s);
+  }
+  __shared__ double sum[4];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_down(s, d);
+  if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) parts[(int64_t)e * kNormParts + part] = sum[0] + sum[1] + sum[2] + sum[3];
+}
+
+// X = U scale / (|U|_F + eps), transposed where rows > cols, 64 x 64 at a
+// time; columns n .. ldx - 1 of X are zero.
+template <class T, class G, bool MOM>
+__global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsUpdate up, const double* parts,
+                                                 float eps, float scale, T* planes) {
+  const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
+  const NsMatrix& x = tab.m[e];
+  const NsShape sh(x.rows, x.cols);
+  __shared__ float tile[64][65];
+  __shared__ double total[4];
+  const int np = norm_parts(x.rows, x.cols);
+  double s = threadIdx.x < (unsigned)np ? parts[(int64_t)e * kNormParts + threadIdx.x] : 0.0;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_down(s, d);
+  if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = s;
+  __syncthreads();
+  // the factor and the product with it in fp64: neither leaves its range
+  const double f = (double)scale / (sqrt(total[0] + total[1] + total[2] + total[3]) + (double)eps);
+  const int32_t t = (int32_t)blockIdx.x - tiles.begin[e];
+  const int32_t across = (x.cols + 63) / 64;
+  const int64_t r0 = (int64_t)(t / across) * 64, c0 = (int64_t)(t % across) * 64;
+  const G* grad = static_cast<const G*>(x.grad);
+  const int c = (threadIdx.x & 15) * 4, l = threadIdx.x >> 4;
+  T* out = planes + x.base;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int rr = l + 16 * p;
+    const int64_t r = r0 + rr, col = c0 + c;
+    f32x4 u = {0.f, 0.f, 0.f, 0.f};
+    if (r < x.rows && col < x.cols) {
+      const int n = (int)(x.cols - col < 4 ? x.cols - col : 4);
+      u = load4(grad + r * x.ld_grad + col, n);
+      if constexpr (MOM) {
+        const f32x4 g = u;
+        u = load4(x.momentum + r * x.cols + col, n);
+        if (up.nesterov) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[k] = fmaf(up.mu, u[k], g[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = (float)((double)u[k] * f);
+    }
+    if (!sh.flip) {
+      if (r < sh.m && col < sh.ldx) store4(out + r * sh.ldx + col, u, 4);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tile[rr][c + k] = u[k];
+    }
+  }
+  if (sh.flip) {
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int64_t i = c0 + l + 16 * p, j = r0 + c;  // X[i][j ..] = U[j ..][i]
+      f32x4 u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = tile[c + k][l + 16 * p];
+      if (i < sh.m && j < sh.ldx) store4(out + i * sh.ldx + j, u, 4);
+    }
+  }
+}
+
+// Tile t of the upper triangle of an nt x nt grid, by rows.
+__device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti, int32_t& tj) {
+  int32_t row = 0, left = t;
+  while (left >= nt - row) {
+    left -= nt - row;
+    ++row;
+  }
+  ti = row;
+  tj = row + left;
+}
+
+// A = alpha X XT (POLY false: src = X, dst = A), or B = beta A + alpha A A
+// (POLY true: src = A, dst = B; A is its own transpose).
+template <class T, int BT, bool POLY>
+__global__ void __launch_bounds__(256) k_ns_symmetric(NsTable tab, NsTiles tiles, T* planes, int32_t next, float alpha,
+                                                      float beta) {
+  using P = TileProduct<T, BT, BT, 2, 2, true, true>;
+  __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+  const int32_t t = (int32_t)xcd_run(blockIdx.x, gridDim.x);
+  const int e = find_matrix(tiles, tab.count, t);
+  const NsShape sh(tab.m[e].rows, tab.m[e].cols);
+  T* x = planes + tab.m[e].base;
+  T* a_plane = x + 2 * sh.x_size;
+  const T* src = POLY ? a_plane : x + (next ? sh.x_size : 0);
+  T* dst = POLY ? a_plane + sh.a_size : a_plane;
+  const int64_t ld = POLY ? sh.lda : sh.ldx;
+  int32_t ti, tj;
+  triangle_tile(t - tiles.begin[e], (int32_t)((sh.m + BT - 1) / BT), ti, tj);
+  const int64_t i0 = (int64_t)ti * BT, j0 = (int64_t)tj * BT;
+  const Operand<T> a{src + i0 * ld, ld, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
+  const Operand<T> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
+  f32x4 acc[P::MI][P::NI] = {};
+  P::run(a, b, 0, ld, lds, acc);
+  P::each(acc, [&](int i, int j, f32x4 v) {
+    if (i >= a.rows || j0 + j >= sh.lda) return;
+    v *= alpha;
+    if constexpr (POLY) v += beta * load4(src + (i0 + i) * ld + j0 + j, 4);
+    store4(dst + (i0 + i) * sh.lda + j0 + j, v, 4);  // columns m .. lda - 1 get zeros
+    if (ti != tj) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k < b.rows) dst[(j0 + j + k) * sh.lda + i0 + i] = (T)v[k];
+    }
+  });
+}
+
+// X <- a X + beta B X into the other X plane, or out of it in the last step.
+enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
+
+template <class T, class O, int BT, int LAST>
+__global__ void __launch_bounds__(256) k_ns_step(NsTable tab, NsTiles tiles, T* planes, int32_t next, float a_coef,
+                                                 float beta, NsUpdate up) {
+  using P = TileProduct<T, BT, BT, 2, 2, true, false>;
+  __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+  const int32_t t = (int32_t)xcd_run(blockIdx.x, gridDim.x);
+  const int e = find_matrix(tiles, tab.count, t);
+  const NsMatrix& x = tab.m[e];
+  const NsShape sh(x.rows, x.cols);
+  const T* src = planes + x.base + (next ? sh.x_size : 0);
+  T* dst = planes + x.base + (next ? 0 : sh.x_size);
+  const T* poly = planes + x.base + 2 * sh.x_size + sh.a_size;
+  int64_t ti, tj;
+  band_tile(t - tiles.begin[e], (sh.m + BT - 1) / BT, (sh.n + BT - 1) / BT, 8, ti, tj);
+  const int64_t i0 = ti * BT, j0 = tj * BT;
+  const Operand<T> a{poly + i0 * sh.lda, sh.lda, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
+  const Operand<T> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
+  f32x4 acc[P::MI][P::NI] = {};
+  P::run(a, b, 0, sh.m, lds, acc);
+  const float scale = LAST == kNsWeight ? x.scale * (up.lr_scale ? *up.lr_scale : 1.f) : 1.f;
+  const float keep = LAST == kNsWeight ? 1.f - up.decay * (up.lr_scale ? *up.lr_scale : 1.f) : 1.f;
+  P::each(acc, [&](int i, int j, f32x4 v) {
+    if (i >= a.rows || j >= b.rows) return;
+    v = beta * v + a_coef * load4(src + (i0 + i) * sh.ldx + j0 + j, 4);
+    if constexpr (LAST == kNsNext) {
+      store4(dst + (i0 + i) * sh.ldx + j0 + j, v, 4);
+    } else {
+      const int64_t left = sh.n - (j0 + j);
+      if (left <= 0) return;
+      const int n = (int)(left < 4 ? left : 4);
+      O* out = static_cast<O*>(x.out);
+      if (!sh.flip) {
+        O* p = out + (i0 + i) * x.ld_out + j0 + j;
+        if constexpr (LAST == kNsWeight) v = keep * load4(p, n) - scale * v;
+        store4(p, v, n);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < n) {
+            O* p = out + (j0 + j + k) * x.ld_out + i0 + i;
+            if constexpr (LAST == kNsWeight) *p = (O)(keep * (float)*p - scale * v[k]);
+            else *p = (O)v[k];
+          }
+      }
+    }
+  });
+}
+
+// Largest |a x + b x^3 + c x^5| for 0 <= x <= top: at the ends or where the
+// slope a + 3 b t + 5 c t^2 (t = x^2) is zero.
+double step_top(const float* co, double top) {
+  const double a = co[0], b = co[1], c = co[2];
+  auto p = [&](double x) { return std::fabs(x * (a + x * x * (b + x * x * c))); };
+  double best = p(top);
+  double roots[2];
+  int n = 0;
+  if (c != 0) {
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0) {
+      roots[n++] = (-3 * b + std::sqrt(d)) / (10 * c);
+      roots[n++] = (-3 * b - std::sqrt(d)) / (10 * c);
+    }
+  } else if (b != 0) {
+    roots[n++] = -a / (3 * b);
+  }
+  for (int k = 0; k < n; ++k)
+    if (roots[k] > 0 && roots[k] < top * top) best = std::max(best, p(std::sqrt(roots[k])));
+  return best;
+}
+
+// The powers of two by which X, A and B are held.  The largest singular value
+// bounds every element: X0 has at most |X0|_F <= 1, each step's is bounded by
+// its polynomial (with a thousandth for what is held having been rounded),
+// |A| by the square, |B| by |b| A + |c| A A.  In fp16 the bound is held at
+// 2^13 to 2^14, a quarter of the type's largest value; values down to 2^-27 of
+// it keep all 11 bits.  In fp32 nothing is scaled.
+constexpr double kSlack = 1.001;
+
+struct NsScales {
+  float x = 1.f, a = 1.f;
+  float b[DC_NS_MAX_STEPS];
+};
+
+NsScales ns_scales(int32_t dtype, int32_t steps, const float* coeffs) {
+  NsScales s;
+  for (int k = 0; k < steps; ++k) s.b[k] = 1.f;
+  if (dtype == DC_F32) return s;
+  double top[DC_NS_MAX_STEPS + 1], most = kSlack;
+  top[0] = kSlack;
+  for (int k = 0; k < steps; ++k) {
+    top[k + 1] = kSlack * step_top(coeffs + 3 * k, top[k]);
+    most = std::max(most, top[k + 1]);
+  }
+  auto hold = [](double bound) { return (float)std::ldexp(1.0, 14 - std::max(-40, std::ilogb(bound) + 1)); };
+  s.x = hold(most);
+  s.a = hold(most * most);
+  for (int k = 0; k < steps; ++k) {
+    const double q = top[k] * top[k];
+    s.b[k] = hold(std::max(1e-6, std::fabs(coeffs[3 * k + 1]) * q + std::fabs(coeffs[3 * k + 2]) * q * q));
+  }
+  return s;
+}
+
+// The next chunk of matrices from `first`: kNsChunk of them at most, and of
+// 2^22 64 x 64 tiles together unless it is one matrix (a grid holds 2^24).
+int32_t chunk_end(const dc_matrix* mats, int32_t n, int32_t first) {
+  int64_t tiles = 0;
+  int32_t k = first;
+  for (; k < n && k < first + kNsChunk; ++k) {
+    tiles += ((int64_t)(mats[k].rows + 63) / 64) * ((mats[k].cols + 63) / 64);
+    if (k > first && tiles > ((int64_t)1 << 22)) break;
+  }
+  return k;
+}
+
+int64_t chunk_values(const dc_matrix* mats, int32_t first, int32_t last) {
+  int64_t v = 0;
+  for (int32_t k = first; k < last; ++k) v += NsShape(mats[k].rows, mats[k].cols).values();
+  return v;
+}
+
+constexpr int64_t kPartsBytes = (int64_t)kNsChunk * kNormParts * 8;
+
+template <class F>
+int32_t fill_tiles(NsTiles& tiles, const NsTable& tab, F&& count) {
+  int64_t t = 0;
+  for (int k = 0; k < tab.count; ++k) {
+    tiles.begin[k] = (int32_t)t;
+    t += count(NsShape(tab.m[k].rows, tab.m[k].cols), tab.m[k]);
+  }
+  for (int k = tab.count; k <= kNsChunk; ++k) tiles.begin[k] = (int32_t)t;
+  return (int32_t)t;
+}
+
+template <class T, class G, class O, bool MOM, int BT>
+void ns_chunk(const NsTable& tab, const NsLaunch& a, const NsScales& sc, const NsUpdate& up, double* parts,
+              T* planes, hipStream_t stream) {
+  NsTiles tiles;
+  int32_t n = fill_tiles(tiles, tab, [](const NsShape&, const NsMatrix& x) { return norm_parts(x.rows, x.cols); });
+  k_ns_norm<G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts);
+  n = fill_tiles(tiles, tab, [](const NsShape&, const NsMatrix& x) {
+    return (int64_t)((x.rows + 63) / 64) * ((x.cols + 63) / 64);
+  });
+  k_ns_load<T, G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts, a.eps, sc.x, planes);
+  NsTiles square, wide;
+  const int32_t n_square = fill_tiles(square, tab, [](const NsShape& s, const NsMatrix&) {
+    const int64_t nt = (s.m + BT - 1) / BT;
+    return nt * (nt + 1) / 2;
+  });
+  const int32_t n_wide = fill_tiles(wide, tab, [](const NsShape& s, const NsMatrix&) {
+    return ((s.m + BT - 1) / BT) * ((s.n + BT - 1) / BT);
+  });
+  for (int32_t k = 0; k < a.steps; ++k) {
+    const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
+    const int32_t next = k & 1;
+    k_ns_symmetric<T, BT, false><<<n_square, 256, 0, stream>>>(tab, square, planes, next, sc.a / (sc.x * sc.x), 0.f);
+    k_ns_symmetric<T, BT, true><<<n_square, 256, 0, stream>>>(tab, square, planes, next,
+                                                              cc * (sc.b[k] / (sc.a * sc.a)), cb * (sc.b[k] / sc.a));
+    if (k + 1 < a.steps) {
+      k_ns_step<T, O, BT, kNsNext><<<n_wide, 256, 0, stream>>>(tab, wide, planes, next, ca, 1.f / sc.b[k], up);
+    } else {
+      k_ns_step<T, O, BT, MOM ? kNsWeight : kNsOut><<<n_wide, 256, 0, stream>>>(
+          tab, wide, planes, next, ca / sc.x, 1.f / (sc.b[k] * sc.x), up);
+    }
+  }
+}
+
+template <class T, class G, class O, bool MOM>
+hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
+  const NsScales sc = ns_scales(a.dtype, a.steps, a.coeffs);
+  double* parts = static_cast<double*>(a.workspace);
+  T* planes = reinterpret_cast<T*>(static_cast<char*>(a.workspace) + kPartsBytes);
+  const NsUpdate up{a.mu, a.lr * a.weight_decay, a.nesterov, a.lr_scale};
+  for (int32_t first = 0, last; first < a.num; first = last) {
+    last = chunk_end(a.mats, a.num, first);
+    NsTable tab;
+    tab.count = last - first;
+    int64_t base = 0, tiles = 0;
+    for (int32_t k = first; k < last; ++k) {
+      const dc_matrix& d = a.mats[k];
+      const NsShape sh(d.rows, d.cols);
+      tab.m[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
+                                  a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
+      base += sh.values();
+      tiles += ((sh.m + 127) / 128) * ((sh.n + 127) / 128);
+    }
+    // 128 x 128 tiles once they give every compute unit one
+    if (tiles >= 256) ns_chunk<T, G, O, MOM, 128>(tab, a, sc, up, parts, planes, stream);
+    else ns_chunk<T, G, O, MOM, 64>(tab, a, sc, up, parts, planes, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+float ns_factor(int32_t scale_mode, int32_t rows, int32_t cols) {
+  if (scale_mode == DC_SCALE_ASPECT) return std::sqrt(std::max(1.f, (float)rows / (float)cols));
+  if (scale_mode == DC_SCALE_RMS) return 0.2f * std::sqrt((float)std::max(rows, cols));
+  return 1.f;
+}
+
+double ns_largest(int32_t steps, const float* coeffs) {
+  double top = kSlack, most = top;
+  for (int k = 0; k < steps; ++k) most = std::max(most, top = kSlack * step_top(coeffs + 3 * k, top));
+  return most;
+}
+
+int64_t ns_workspace(int32_t dtype, const dc_matrix* mats, int32_t num) {
+  int64_t most = 0;
+  for (int32_t first = 0, last; first < num; first = last) {
+    last = chunk_end(mats, num, first);
+    most = std::max(most, chunk_values(mats, first, last));
+  }
+  return num ? kPartsBytes + most * (dtype == DC_F32 ? 4 : 2) : 0;
+}
+
+hipError_t launch_ns(const NsLaunch& a, hipStream_t stream) {
+  if (a.num == 0) return hipSuccess;
+  if (!a.update) {
+    if (a.dtype == DC_F32) return ns_run<float, float, float, false>(a, stream);
+    return ns_run<_Float16, __bf16, __bf16, false>(a, stream);
+  }
+  if (a.dtype == DC_F32) {
+    if (a.out_dtype == DC_F32) return ns_run<float, float, float, true>(a, stream);
+    return ns_run<float, float, __bf16, true>(a, stream);
+  }
+  if (a.out_dtype == DC_F32) return ns_run<_Float16, __bf16, float, true>(a, stream);
+  return ns_run<_Float16, __bf16, __bf16, true>(a, stream);
+}
+
+}  // namespace dc

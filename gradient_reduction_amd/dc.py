@@ -23,11 +23,18 @@ DC_ORDER_RANK, DC_ORDER_RING = 0, 1
 DC_SCHED_RING, DC_SCHED_BIDIR, DC_SCHED_RD = 0, 1, 2
 DC_MAX_W, DC_MAX_GROUPS, DC_MAX_COMMS = 64, 64, 8
 
+DC_ACT_NONE, DC_ACT_RELU, DC_ACT_GELU, DC_ACT_SILU = 0, 1, 2, 3
+DC_SCALE_NONE, DC_SCALE_ASPECT, DC_SCALE_RMS = 0, 1, 2
+DC_NS_MAX_STEPS = 16
+
 TASK_DTYPE = np.dtype([("offset", "<i8"), ("numel", "<i8"), ("param", "<i4"),
                        ("comm", "<i4"), ("reserved", "<i8")])
 COMM_DTYPE = np.dtype([("size", "<i4"), ("stride", "<i4")])
 PIECE_DTYPE = np.dtype([("src", "<i8"), ("dst", "<i8"), ("len", "<i8"), ("reserved", "<i8")])
 TILE_DTYPE = np.dtype([("first", "<i4"), ("last", "<i4"), ("root", "<i4"), ("flags", "<i4")])
+
+MATRIX_DTYPE = np.dtype([("grad", "<u8"), ("out", "<u8"), ("momentum", "<u8"), ("ld_grad", "<i8"),
+                         ("ld_out", "<i8"), ("rows", "<i4"), ("cols", "<i4")])
 
 
 class dc_probe(ctypes.Structure):
@@ -45,7 +52,7 @@ class DCError(RuntimeError):
 
 
 _lib = None
-_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
 _SIGS = {
     "dc_version": ([], ctypes.c_char_p),
@@ -90,6 +97,19 @@ _SIGS = {
     "dc_deferred_reduce": ([_i32, _vp, _i64, _vp, _i64, _i64, _i32, _vp], _i32),
     "dc_accumulate_reduce": ([_i32, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _i32, _i64, _vp],
                              _i32),
+    "dc_linear_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
+    "dc_linear_backward_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
+    "dc_bias_act_workspace": ([_i32, _i64, _i64, _vp], _i32),
+    "dc_linear": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp,
+                   _i64, _vp, _i64, _vp], _i32),
+    "dc_bias_act_backward": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i32,
+                              _vp, _i64, _vp], _i32),
+    "dc_linear_backward": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                            _vp, _i64, _i32, _vp, _i64, _vp], _i32),
+    "dc_orthogonalize_workspace": ([_i32, _vp, _i32, _vp], _i32),
+    "dc_orthogonalize": ([_i32, _vp, _i32, _i32, _vp, _f32, _vp, _i64, _vp], _i32),
+    "dc_muon_update": ([_i32, _i32, _vp, _i32, _f32, _vp, _f32, _i32, _f32, _i32, _i32, _vp, _f32, _vp,
+                        _i64, _vp], _i32),
     "dc_round_bf16": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_copy": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_rows": ([_vp, _i64, _i32, _vp, _i64, _i32, _i64, _vp], _i32),
@@ -442,6 +462,77 @@ def dc_accumulate_reduce(W, x, ld_x, acc, ld_acc, init, keep_acc, out, ld_out, o
     _check("dc_accumulate_reduce", lib().dc_accumulate_reduce(
         W, _dev(x), ld_x, _dev(acc), ld_acc, init, keep_acc, _dev(out), ld_out, out_rows, M,
         _stream(stream)))
+
+
+def dc_linear_workspace(dtype, T, N, K):
+    """Host only; bytes of workspace."""
+    n = ctypes.c_int64(0)
+    _check("dc_linear_workspace", lib().dc_linear_workspace(dtype, T, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def dc_linear_backward_workspace(dtype, T, N, K):
+    """Host only; bytes of workspace."""
+    n = ctypes.c_int64(0)
+    _check("dc_linear_backward_workspace", lib().dc_linear_backward_workspace(dtype, T, N, K,
+                                                                              ctypes.byref(n)))
+    return n.value
+
+
+def dc_bias_act_workspace(dtype, T, N):
+    """Host only; bytes of workspace."""
+    n = ctypes.c_int64(0)
+    _check("dc_bias_act_workspace", lib().dc_bias_act_workspace(dtype, T, N, ctypes.byref(n)))
+    return n.value
+
+
+def dc_linear(dtype, T, N, K, x, ld_x, w, ld_w, bias, residual, ld_res, act, pre, ld_pre, y, ld_y,
+              workspace, workspace_bytes, stream=None):
+    _check("dc_linear", lib().dc_linear(
+        dtype, T, N, K, _dev(x), ld_x, _dev(w), ld_w, _dev(bias), _dev(residual), ld_res, act,
+        _dev(pre), ld_pre, _dev(y), ld_y, _dev(workspace), workspace_bytes, _stream(stream)))
+
+
+def dc_bias_act_backward(dtype, T, N, dy, ld_dy, pre, ld_pre, act, dz, ld_dz, grad_dtype, db,
+                         accumulate, workspace, workspace_bytes, stream=None):
+    _check("dc_bias_act_backward", lib().dc_bias_act_backward(
+        dtype, T, N, _dev(dy), ld_dy, _dev(pre), ld_pre, act, _dev(dz), ld_dz, grad_dtype, _dev(db),
+        accumulate, _dev(workspace), workspace_bytes, _stream(stream)))
+
+
+def dc_linear_backward(dtype, T, N, K, dz, ld_dz, w, ld_w, x, ld_x, dx, ld_dx, grad_dtype, dw, ld_dw,
+                       accumulate, workspace, workspace_bytes, stream=None):
+    _check("dc_linear_backward", lib().dc_linear_backward(
+        dtype, T, N, K, _dev(dz), ld_dz, _dev(w), ld_w, _dev(x), ld_x, _dev(dx), ld_dx, grad_dtype,
+        _dev(dw), ld_dw, accumulate, _dev(workspace), workspace_bytes, _stream(stream)))
+
+
+def dc_orthogonalize_workspace(dtype, mats, num):
+    """Host only; mats: MATRIX_DTYPE records.  Bytes of workspace."""
+    mp, _a = _host(mats, MATRIX_DTYPE)
+    n = ctypes.c_int64(0)
+    _check("dc_orthogonalize_workspace", lib().dc_orthogonalize_workspace(dtype, mp, num,
+                                                                          ctypes.byref(n)))
+    return n.value
+
+
+def dc_orthogonalize(dtype, mats, num, steps, coeffs, eps, workspace, workspace_bytes, stream=None):
+    """mats: MATRIX_DTYPE records (host); coeffs: steps x 3."""
+    mp, _a = _host(mats, MATRIX_DTYPE)
+    cp, _b = _host(coeffs, np.float32)
+    _check("dc_orthogonalize", lib().dc_orthogonalize(
+        dtype, mp, num, steps, cp, eps, _dev(workspace), workspace_bytes, _stream(stream)))
+
+
+def dc_muon_update(dtype, weight_dtype, mats, num, lr, lr_scale, mu, nesterov, weight_decay, scale_mode,
+                   steps, coeffs, eps, workspace, workspace_bytes, stream=None):
+    """mats: MATRIX_DTYPE records (host); coeffs: steps x 3; lr_scale: device
+    float or None."""
+    mp, _a = _host(mats, MATRIX_DTYPE)
+    cp, _b = _host(coeffs, np.float32)
+    _check("dc_muon_update", lib().dc_muon_update(
+        dtype, weight_dtype, mp, num, lr, _dev(lr_scale), mu, nesterov, weight_decay, scale_mode, steps,
+        cp, eps, _dev(workspace), workspace_bytes, _stream(stream)))
 
 
 def dc_round_bf16(in_, out, n, stream=None):

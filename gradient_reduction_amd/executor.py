@@ -18,6 +18,10 @@ the rows its sums go to), or on the device (dc_plan_flush_device, the same
 records); flush() then launches dc_flush_bucket_planned, the same sums with
 no per-tile search.
 
+register_matrices + muon_update take the step after the flush: every matrix
+parameter's orthogonalised momentum update (dc_muon_update), read from the
+row that holds its whole reduced gradient.
+
 torch supplies device memory and the stream; every step runs in libdc.so.
 """
 from dataclasses import dataclass
@@ -379,6 +383,70 @@ class Zero1FlushExecutor:
                                        self.d_bout.data_ptr() + 8 * t0 * self.W,
                                        self.comms, len(self.comms), self.pre_div, stream)
         self.flushes += 1
+
+    # -- the owners' update of matrix parameters ---------------------------------
+
+    def register_matrices(self, weights, momenta) -> None:
+        """weights, momenta: {param: [rows, cols] tensor}, rows * cols the
+        param's size; momenta fp32, weights all bf16 or all fp32, rows of
+        either contiguous.  muon_update() steps them from then on.  A param
+        needs its whole reduced gradient in one row: the owner's, or row 0
+        where it is AllReduced (every row has it).  ZeRO-2 spreads a param
+        over rows and a sub-communicator's blocks hold different sums, so
+        both are refused.  Synchronizes (the owner map is read back)."""
+        torch = self.torch
+        if self.zero2:
+            raise ValueError("register_matrices: ZeRO-2 leaves no row with a whole parameter")
+        if set(weights) != set(momenta):
+            raise ValueError("weights and momenta name different params")
+        place = {}
+        for bk in self.buckets:
+            for off, numel, param, comm in bk.tasks:
+                place.setdefault(param, []).append((bk.col + off, numel, comm))
+        if self.h_owner is None:
+            self.fetch_metadata()
+        kinds = {w.dtype for w in weights.values()}
+        if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
+            raise ValueError(f"weights are {sorted(map(str, kinds))}: all bfloat16 or all float32 are needed")
+        recs = np.zeros(len(weights), dc.MATRIX_DTYPE)
+        self.m_rows, self.m_cols = np.zeros(len(weights), np.int64), np.zeros(len(weights), np.int64)
+        for k, p in enumerate(sorted(weights)):
+            w, m = weights[p], momenta[p]
+            if p not in place or len(place[p]) != 1 or place[p][0][2] != 0:
+                raise ValueError(f"param {p} has no whole data-parallel task")
+            col, numel, _ = place[p][0]
+            if w.dim() != 2 or w.numel() != numel or m.shape != w.shape:
+                raise ValueError(f"param {p} of {numel}: weight {tuple(w.shape)}, momentum {tuple(m.shape)}")
+            if not (w.is_contiguous() and m.is_contiguous()) or m.dtype != torch.float32:
+                raise ValueError(f"param {p}: contiguous weight and float32 momentum are needed")
+            if w.device != self.d_owner.device or m.device != self.d_owner.device:
+                raise ValueError(f"param {p} is not on {self.d_owner.device}")
+            recs[k] = (0, w.data_ptr(), m.data_ptr(), w.shape[1], w.shape[1], w.shape[0], w.shape[1])
+            owner = int(self.h_owner[p]) if self.reduce_to_owner else -1
+            self.m_rows[k], self.m_cols[k] = max(owner, 0), col
+        self.m_recs = recs
+        self.m_wtype = dc.DC_F32 if torch.float32 in kinds else dc.DC_BF16
+        self.m_keep = (dict(weights), dict(momenta))
+        self.m_bytes = dc.dc_orthogonalize_workspace(self.dtype, recs, len(recs))
+
+    def muon_update(self, slab_out, ld_out: int, lr: float, mu: float = 0.95, nesterov: bool = True,
+                    weight_decay: float = 0.0, scale: str = "rms", steps: int = 5, coeffs=None,
+                    eps: float = 1e-7, lr_scale=None, stream=None) -> None:
+        """Steps the registered matrices from the flushed slab (after flush()
+        of every bucket into slab_out, on the same stream); arguments as in
+        muon.update()."""
+        from . import linear, muon
+        if scale not in muon.SCALES:
+            raise ValueError(f"scale {scale!r}: one of {sorted(muon.SCALES)}")
+        eb = 2 if self.dtype == dc.DC_BF16 else 4
+        base = slab_out if isinstance(slab_out, int) else slab_out.data_ptr()
+        recs = self.m_recs.copy()
+        recs["grad"] = base + (self.m_rows * ld_out + self.m_cols) * eb
+        table = muon._steps(steps, muon.COEFFS if coeffs is None else coeffs)
+        with linear.on(self.d_owner.device, stream):
+            dc.dc_muon_update(self.dtype, self.m_wtype, recs, len(recs), lr, lr_scale, mu,
+                              1 if nesterov else 0, weight_decay, muon.SCALES[scale], steps, table, eps,
+                              linear.workspace(self.m_bytes, self.d_owner.device), self.m_bytes)
 
     # -- one step as a HIP graph --------------------------------------------------
 

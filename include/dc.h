@@ -26,6 +26,12 @@
  *   under gradient    dc_accumulate for each micro-batch, then one
  *   accumulation      dc_deferred_reduce (or dc_accumulate_reduce for the
  *                     last micro-batch) ([MT] What)
+ *   a layer's         dc_linear forward, dc_bias_act_backward and
+ *   gradients         dc_linear_backward, whose weight gradient may go
+ *                     straight into an accumulator row
+ *   the owner's step  dc_muon_update on the parameters whose reduced
+ *                     gradient the owner holds whole (dc_orthogonalize: its
+ *                     orthogonalisation alone)
  *   collectives       dc_reduce_scatter / dc_all_gather and their ring-order,
  *                     step-by-step and relaid (dc_relayout_bucket +
  *                     dc_reduce_scatter_v) forms
@@ -81,6 +87,16 @@ typedef int32_t dc_status;
 #define DC_SCHED_RING 0      /* all-gather step schedules (dc_all_gather_step) */
 #define DC_SCHED_BIDIR 1
 #define DC_SCHED_RD 2
+
+#define DC_ACT_NONE 0        /* activations of the linear layer */
+#define DC_ACT_RELU 1
+#define DC_ACT_GELU 2        /* v Phi(v), Phi the normal distribution's */
+#define DC_ACT_SILU 3        /* v / (1 + exp(-v)) */
+
+#define DC_SCALE_NONE 0      /* shape factor of a matrix update: 1 */
+#define DC_SCALE_ASPECT 1    /* sqrt(max(1, rows / cols)) */
+#define DC_SCALE_RMS 2       /* 0.2 sqrt(max(rows, cols)) */
+#define DC_NS_MAX_STEPS 16   /* Newton-Schulz steps per call */
 
 #define DC_MAX_W 64          /* simulated ranks per slab */
 #define DC_MAX_GROUPS 64     /* parameter groups per owner map */
@@ -164,6 +180,24 @@ typedef struct {
   int32_t root;
   int32_t flags;
 } dc_tile;
+
+/* One matrix of dc_orthogonalize or dc_muon_update: rows x cols, row-major.
+ * 48 bytes.
+ *   grad, ld_grad  device, the gradient: row r starts at grad + r * ld_grad
+ *                  (in elements; any alignment), ld_grad >= cols
+ *   out, ld_out    device, the result, or the weights that are updated
+ *   momentum       device fp32 [rows][cols], read and written by
+ *                  dc_muon_update; not used by dc_orthogonalize
+ *   rows, cols     at least 1 */
+typedef struct {
+  const void* grad;
+  void* out;
+  float* momentum;
+  int64_t ld_grad;
+  int64_t ld_out;
+  int32_t rows;
+  int32_t cols;
+} dc_matrix;
 
 /* Library version string (static storage). */
 const char* dc_version(void);
@@ -762,6 +796,126 @@ dc_status dc_stream_rows(const void* src, int64_t src_ld_vec, int32_t rows_read,
 dc_status dc_stream_rows_shaped(const void* src, int64_t src_ld_vec, int32_t rows_read, void* dst,
                                 int64_t dst_ld_vec, int32_t rows_written, int64_t nvec,
                                 int32_t group, int32_t cap, void* stream);
+
+/* ---- A layer's products and the owner's update --------------------------
+ *
+ * These take matrices where a model keeps them: element-aligned bases (else
+ * DC_ERR_ALIGN) and any row stride of at least the row's length, in
+ * elements.  16-byte aligned operands with strides of whole 16 bytes run
+ * faster.  What an output's row holds between its length and its stride stays
+ * as it was.  Outputs must not overlap inputs or other outputs (DC_ERR_ARG)
+ * except where said; two matrices that interleave as column ranges of rows
+ * with one common stride do not overlap.  Sizes are at most 2^28 and the
+ * elements of one matrix at most 2^36 (2^34 for dc_matrix), else DC_ERR_SHAPE.
+ * A workspace is device memory, 16-byte aligned, of at least the bytes that
+ * the query gives for the same arguments (else DC_ERR_SHAPE; NULL is allowed
+ * when it gives 0); it is scratch: it need not be cleared, holds nothing
+ * between calls, and must not be shared by calls that may run at once. */
+
+/* Bytes of workspace of dc_linear, dc_linear_backward and
+ * dc_bias_act_backward for these sizes.  Host only. */
+dc_status dc_linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t* bytes);
+dc_status dc_linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t* bytes);
+dc_status dc_bias_act_workspace(int32_t dtype, int64_t T, int64_t N, int64_t* bytes);
+
+/* Linear layer on T rows (tokens), N outputs, K inputs:
+ *   pre[t][n] = sum_k x[t][k] w[n][k] + bias[n]
+ *   y[t][n]   = act(pre[t][n]) + residual[t][n]
+ * Sums, activation and residual in fp32, y and pre each rounded once.
+ *   x, ld_x          device [T, ld_x], ld_x >= K
+ *   w, ld_w          device [N, ld_w], ld_w >= K
+ *   bias             device [N] or NULL
+ *   residual, ld_res device [T, ld_res] or NULL; may be y itself (same ld)
+ *   act              DC_ACT_*
+ *   pre, ld_pre      device [T, ld_pre] out or NULL: what
+ *                    dc_bias_act_backward reads
+ *   y, ld_y          device [T, ld_y] out
+ * T = 0 writes nothing; N and K are at least 1. */
+dc_status dc_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x,
+                    const void* w, int64_t ld_w, const void* bias, const void* residual,
+                    int64_t ld_res, int32_t act, void* pre, int64_t ld_pre, void* y, int64_t ld_y,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Backward of the bias and the activation:
+ *   dz[t][n] = dy[t][n] act'(pre[t][n])         rounded once
+ *   db[n]    = (accumulate ? db[n] : 0) + sum_t dy[t][n] act'(pre[t][n])
+ * the sum in fp32 over the unrounded products, in an order fixed by the
+ * sizes.  The residual's gradient is dy itself.  act'(0) of relu is 0.
+ *   dy, ld_dy    device [T, ld_dy]
+ *   pre, ld_pre  device [T, ld_pre]; NULL with DC_ACT_NONE (else DC_ERR_NULL)
+ *   dz, ld_dz    device [T, ld_dz] out, or NULL; may be dy itself (same ld)
+ *   grad_dtype   of db: DC_F32, or dtype
+ *   db           device [N], or NULL
+ * T = 0 gives db's empty sum. */
+dc_status dc_bias_act_backward(int32_t dtype, int64_t T, int64_t N, const void* dy, int64_t ld_dy,
+                               const void* pre, int64_t ld_pre, int32_t act, void* dz,
+                               int64_t ld_dz, int32_t grad_dtype, void* db, int32_t accumulate,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Backward of the products:
+ *   dx[t][k] = sum_n dz[t][n] w[n][k]                              (dtype)
+ *   dw[n][k] = (accumulate ? dw[n][k] : 0) + sum_t dz[t][n] x[t][k] (grad_dtype)
+ * in fp32, rounded once.  With accumulate and DC_F32, dw is a parameter's
+ * place in a replica's accumulator row ([MT] What: micro-batch gradients add
+ * up locally), with no gradient written and read in between.
+ *   dz, ld_dz   device [T, ld_dz], ld_dz >= N
+ *   w, ld_w     device [N, ld_w]; read only when dx is given
+ *   x, ld_x     device [T, ld_x]; read only when dw is given
+ *   dx, ld_dx   device [T, ld_dx] out, or NULL
+ *   grad_dtype  of dw: DC_F32, or dtype
+ *   dw, ld_dw   device [N, ld_dw], or NULL
+ * T = 0 gives dw's empty sum. */
+dc_status dc_linear_backward(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* dz,
+                             int64_t ld_dz, const void* w, int64_t ld_w, const void* x, int64_t ld_x,
+                             void* dx, int64_t ld_dx, int32_t grad_dtype, void* dw, int64_t ld_dw,
+                             int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of workspace of dc_orthogonalize and dc_muon_update for this list
+ * (its rows and cols).  Host only. */
+dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32_t num,
+                                     int64_t* bytes);
+
+/* Every matrix orthogonalised by Newton-Schulz products.  With X the
+ * gradient (its transpose where rows > cols):
+ *   X <- X / (|X|_F + eps)
+ *   for every step (a, b, c):  A = X XT,  X <- a X + (b A + c A A) X
+ * and X (transposed back) is written to out: the singular vectors stay, the
+ * singular values go through the odd polynomials a s + b s^3 + c s^5.
+ * DC_F32 computes in fp32.  DC_BF16 holds X, A and B in fp16 (11 bits, by
+ * powers of two that the polynomials' bounds keep from overflowing) with
+ * fp32 sums: about 1.5e-3 of |out|_F before the rounding to bf16.  |X|_F is
+ * summed in fp64.  A zero matrix gives zero (NaN when eps is 0); a NaN or
+ * infinity anywhere gives NaN in the whole of its matrix and no other.
+ *   mats, num       host dc_matrix[num], num <= 2^20; out has the dtype of the gradients
+ *                   and may be the gradient itself (same ld), otherwise
+ *                   overlaps no gradient and no other out
+ *   steps, coeffs   host float[steps][3], 1 <= steps <= DC_NS_MAX_STEPS; the
+ *                   bound on the singular values must stay under 64
+ *                   (else DC_ERR_ARG: the steps diverge)
+ *   eps             >= 0 */
+dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, int32_t steps,
+                           const float* coeffs, float eps, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* The owner's update of whole matrices from their reduced gradients ([DS]
+ * problem statement: after reduce-to-owner one rank holds a parameter's whole
+ * gradient).  For every matrix:
+ *   m <- mu m + g                              (fp32, stored)
+ *   u  = nesterov ? mu m + g : m
+ *   O  = u orthogonalised, as dc_orthogonalize (in the precision of dtype)
+ *   w <- (1 - l weight_decay) w - l s O        (fp32, rounded to weight_dtype)
+ * with l = lr, times *lr_scale when given (device float[1], read when the
+ * work runs: a recorded graph follows a schedule through it), and s the
+ * shape's factor (DC_SCALE_*).
+ *   dtype         of the gradients; weight_dtype: of out, the weights
+ *   mats, num     host dc_matrix[num]; weights and momenta overlap nothing
+ * Other arguments as in dc_orthogonalize. */
+dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, const dc_matrix* mats, int32_t num,
+                         float lr, const float* lr_scale, float mu, int32_t nesterov,
+                         float weight_decay, int32_t scale_mode, int32_t steps,
+                         const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
+                         void* stream);
 
 #ifdef __cplusplus
 }
