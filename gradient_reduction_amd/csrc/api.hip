@@ -1093,6 +1093,7 @@ namespace {
 constexpr int64_t kMaxSide = (int64_t)1 << 28;      // of a product's matrices
 constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of one of them
 constexpr int64_t kMaxUpdated = (int64_t)1 << 34;   // of a dc_matrix
+constexpr int64_t kMaxUpdatedSide = (int64_t)1 << 20;  // a tile's rows stay within 2^31 bytes
 
 // A [rows, ld] matrix of `cols` columns where a model keeps it.
 struct Rows {
@@ -1176,8 +1177,8 @@ dc_status check_matrices(const dc_matrix* mats, int32_t num) {
   for (int32_t k = 0; k < num; ++k) {
     const dc_matrix& m = mats[k];
     if (m.rows < 1 || m.cols < 1) return fail(DC_ERR_ARG, "matrix %d: %d x %d", k, m.rows, m.cols);
-    if (m.rows > kMaxSide || m.cols > kMaxSide || (int64_t)m.rows * m.cols > kMaxUpdated)
-      return fail(DC_ERR_SHAPE, "matrix %d: %d x %d exceeds 2^28 a side or 2^34 elements", k, m.rows, m.cols);
+    if (m.rows > kMaxUpdatedSide || m.cols > kMaxUpdatedSide || (int64_t)m.rows * m.cols > kMaxUpdated)
+      return fail(DC_ERR_SHAPE, "matrix %d: %d x %d exceeds 2^20 a side or 2^34 elements", k, m.rows, m.cols);
   }
   return DC_OK;
 }

@@ -36,21 +36,23 @@ __device__ __forceinline__ float activation_slope(float v, int act) {
   }
 }
 
-// What happens to the sums of columns j .. j + 3 of row i.
+// What happens to the sums v of columns j .. of row i.
 template <class T>
 struct LinearEpilogue {  // y = act(v + bias) + residual, pre = v + bias
   LinearOut o;
   int64_t n_cols;
-  __device__ void operator()(int64_t i, int64_t j, f32x4 v) const {
-    const int n = (int)(n_cols - j < 4 ? n_cols - j : 4);
-    if (o.bias) v += load4(static_cast<const T*>(o.bias) + j, n);
-    if (o.pre) store4(static_cast<T*>(o.pre) + i * o.ld_pre + j, v, n);
+  template <class V>
+  __device__ void operator()(int64_t i, int64_t j, V v) const {
+    constexpr int N = sizeof(V) / 4;
+    const int64_t n = n_cols - j;
+    if (o.bias) v += load_n<N>(static_cast<const T*>(o.bias) + j, n);
+    if (o.pre) store_n<N>(static_cast<T*>(o.pre) + i * o.ld_pre + j, v, n);
     if (o.act != DC_ACT_NONE) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[t] = activate(v[t], o.act);
+      for (int t = 0; t < N; ++t) v[t] = activate(v[t], o.act);
     }
-    if (o.residual) v += load4(static_cast<const T*>(o.residual) + i * o.ld_res + j, n);
-    store4(static_cast<T*>(o.out) + i * o.ld_out + j, v, n);
+    if (o.residual) v += load_n<N>(static_cast<const T*>(o.residual) + i * o.ld_res + j, n);
+    store_n<N>(static_cast<T*>(o.out) + i * o.ld_out + j, v, n);
   }
 };
 
@@ -58,11 +60,12 @@ template <class G>
 struct GradEpilogue {  // out = (accumulate ? out : 0) + v
   LinearOut o;
   int64_t n_cols;
-  __device__ void operator()(int64_t i, int64_t j, f32x4 v) const {
-    const int n = (int)(n_cols - j < 4 ? n_cols - j : 4);
+  template <class V>
+  __device__ void operator()(int64_t i, int64_t j, V v) const {
+    constexpr int N = sizeof(V) / 4;
     G* p = static_cast<G*>(o.out) + i * o.ld_out + j;
-    if (o.accumulate) v += load4(p, n);
-    store4(p, v, n);
+    if (o.accumulate) v += load_n<N>(p, n_cols - j);
+    store_n<N>(p, v, n_cols - j);
   }
 };
 
@@ -73,14 +76,15 @@ struct ProductArgs {
   int64_t tiles_m, tiles_n;
   int32_t splits;
   int64_t k_per_split;  // a multiple of the stage depth
-  float* partial;       // [splits][m][n rounded up to 4] when splits > 1
+  float* partial;       // [splits][m][ld_partial] when splits > 1
   int64_t ld_partial;
 };
 
-template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, class Epi>
+template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, bool DIRECT, class Epi>
 __global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi) {
-  using P = TileProduct<T, BM, BN, WM, WN, KCA, KCB>;
-  __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+  using P = TileProduct<T, BM, BN, WM, WN, KCA, KCB, DIRECT>;
+  __shared__ __attribute__((aligned(16))) char lds[P::kStage];
+  __shared__ __attribute__((aligned(16))) char lds2[DIRECT ? P::kStage : 16];
   const int64_t per = g.tiles_m * g.tiles_n;
   const int64_t t = xcd_run(blockIdx.x, gridDim.x);
   const int32_t split = (int32_t)(t / per);
@@ -94,17 +98,16 @@ __global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi
   const int64_t k0 = split * g.k_per_split;
   const int64_t k1 = k0 + g.k_per_split < g.k ? k0 + g.k_per_split : g.k;
   f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, k0, k1, lds, acc);
-  if (g.splits > 1) {
-    float* out = g.partial + split * g.m * g.ld_partial;
-    P::each(acc, [&](int i, int j, f32x4 v) {
-      if (i < a.rows && j < b.rows) store4(out + (i0 + i) * g.ld_partial + j0 + j, v, 4);
-    });
-  } else {
-    P::each(acc, [&](int i, int j, f32x4 v) {
-      if (i < a.rows && j < b.rows) epi(i0 + i, j0 + j, v);
-    });
-  }
+  P::run(a, b, k0, k1, lds, lds2, acc);
+  float* part = g.splits > 1 ? g.partial + split * g.m * g.ld_partial : nullptr;
+  P::each(
+      acc, lds, lds2, true, false,
+      [&](int i, int j, f32x8 v) {
+        if (i >= a.rows || j >= b.rows) return;
+        if (part) store_n<8>(part + (i0 + i) * g.ld_partial + j0 + j, v, 8);
+        else epi(i0 + i, j0 + j, v);
+      },
+      [](int, int, f32x8) {});
 }
 
 // The splits of a long k added in their order, then the epilogue.
@@ -121,8 +124,10 @@ __global__ void __launch_bounds__(256) k_product_join(const float* partial, int6
   epi(i, j, v);
 }
 
-// How a product of m x n over k is cut: 128 x 128 tiles when those (with k
-// split at 16 stages or more) give every compute unit work, else 64 x 64.
+// How a product of m x n over k is cut: the tile (256, 128 or 64 square) and
+// the splits of k whose estimated time is least.  A compute unit multiplies
+// at a rate that falls with the tile, holds 1, 2 or 4 workgroups, and runs
+// whole rounds of them; splits cost their sums' traffic and a launch.
 struct Cut {
   int32_t tile, splits;
   int64_t k_per_split, ld_partial;
@@ -130,31 +135,54 @@ struct Cut {
 };
 
 Cut cut(int32_t dtype, int64_t m, int64_t n, int64_t k) {
-  constexpr int64_t kUnits = 256;  // compute units
+  constexpr int64_t kUnits = 256;
+  struct Shape {
+    int32_t tile, held;
+    double rate;  // of a compute unit, products per us at bf16
+  };
+  constexpr Shape kShapes[] = {{256, 1, 2.4e6}, {128, 2, 2.0e6}, {64, 4, 1.0e6}};
   const int64_t bk = dtype == DC_F32 ? 32 : 64;
+  const double slow = dtype == DC_F32 ? 12.0 : 1.0;
   const int64_t stages = std::max<int64_t>(1, (k + bk - 1) / bk);
-  Cut c;
-  auto tiles = [&](int64_t b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
-  const int64_t most = std::max<int64_t>(1, stages / 8);
-  c.tile = tiles(128) * most >= kUnits ? 128 : 64;
-  const int64_t t = std::max<int64_t>(1, tiles(c.tile));
-  int64_t s = t >= kUnits ? 1 : std::min<int64_t>(most, (kUnits + t - 1) / t);
-  const int64_t per = (stages + s - 1) / s;
-  c.splits = (int32_t)((stages + per - 1) / per);
-  c.k_per_split = per * bk;
-  c.ld_partial = (n + 3) / 4 * 4;
-  return c;
+  Cut best{};
+  double least = 0;
+  for (const Shape& s : kShapes) {
+    const int64_t tiles = std::max<int64_t>(1, ((m + s.tile - 1) / s.tile) * ((n + s.tile - 1) / s.tile));
+    for (int64_t want = 1; want <= 64; ++want) {
+      if (want > 1 && (want > stages / 4 || tiles * want > 4 * kUnits)) break;
+      const int64_t per = (stages + want - 1) / want, splits = (stages + per - 1) / per;
+      const int64_t groups = tiles * splits, slots = kUnits * s.held;
+      const int64_t full = groups / slots, rest = groups - full * slots;
+      // a unit holding h workgroups shares its rate among them
+      const double rounds = full * s.held + (rest + kUnits - 1) / kUnits;
+      double us = rounds * s.tile * s.tile * (per * bk) * slow / s.rate + 1.0 + 0.4 * per / s.held;
+      if (splits > 1) us += 2.5 + splits * m * n * 8.0 / 4e6;
+      if (best.tile == 0 || us < least) {
+        least = us;
+        best = Cut{s.tile, (int32_t)splits, per * bk, (n + 7) / 8 * 8};
+      }
+    }
+  }
+  return best;
+}
+
+template <class T, int BT, int WM, int WN, bool KCA, bool KCB, class Epi>
+void launch_product(const ProductArgs& g, bool direct, const Epi& epi, hipStream_t stream) {
+  const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n * g.splits));
+  if (direct) k_product<T, BT, BT, WM, WN, KCA, KCB, true, Epi><<<grid, WM * WN * 64, 0, stream>>>(g, epi);
+  else k_product<T, BT, BT, WM, WN, KCA, KCB, false, Epi><<<grid, WM * WN * 64, 0, stream>>>(g, epi);
 }
 
 template <class T, bool KCA, bool KCB, class Epi>
 hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t m, int64_t n,
                    int64_t k, float* partial, const Epi& epi, hipStream_t stream) {
   const Cut c = cut(dtype, m, n, k);
-  ProductArgs g{a, b, ld_a, ld_b, m, n, k, (m + c.tile - 1) / c.tile, (n + c.tile - 1) / c.tile, c.splits,
-                c.k_per_split, partial, c.ld_partial};
-  const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n * c.splits));
-  if (c.tile == 128) k_product<T, 128, 128, 2, 2, KCA, KCB, Epi><<<grid, 256, 0, stream>>>(g, epi);
-  else k_product<T, 64, 64, 2, 2, KCA, KCB, Epi><<<grid, 256, 0, stream>>>(g, epi);
+  const ProductArgs g{a, b, ld_a, ld_b, m, n, k, (m + c.tile - 1) / c.tile, (n + c.tile - 1) / c.tile, c.splits,
+                      c.k_per_split, partial, c.ld_partial};
+  const bool direct = direct_operand<T>(a, ld_a, KCA ? k : m) && direct_operand<T>(b, ld_b, KCB ? k : n);
+  if (c.tile == 256) launch_product<T, 256, 2, 4, KCA, KCB>(g, direct, epi, stream);
+  else if (c.tile == 128) launch_product<T, 128, 2, 2, KCA, KCB>(g, direct, epi, stream);
+  else launch_product<T, 64, 2, 2, KCA, KCB>(g, direct, epi, stream);
   if (c.splits > 1) {
     const int64_t groups = m * ((n + 3) / 4);
     k_product_join<Epi><<<dim3((uint32_t)((groups + 255) / 256)), 256, 0, stream>>>(partial, c.ld_partial, c.splits,

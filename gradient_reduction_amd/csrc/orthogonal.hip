@@ -105,14 +105,14 @@ __global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsU
       c = (q - r * per_row) * 4;
     }
     const int n = (int)(x.cols - c < 4 ? x.cols - c : 4);
-    f32x4 u = load4(grad + r * x.ld_grad + c, n);
+    f32x4 u = load_n<4>(grad + r * x.ld_grad + c, n);
     if constexpr (MOM) {
       float* mp = x.momentum + r * x.cols + c;
       const f32x4 g = u;
-      u = load4(mp, n);
+      u = load_n<4>(mp, n);
 #pragma unroll
       for (int t = 0; t < 4; ++t) u[t] = fmaf(up.mu, u[t], g[t]);
-      store4(mp, u, n);
+      store_n<4>(mp, u, n);
       if (up.nesterov) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) u[t] = fmaf(up.mu, u[t], g[t]);
@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
     f32x4 u = {0.f, 0.f, 0.f, 0.f};
     if (r < x.rows && col < x.cols) {
       const int n = (int)(x.cols - col < 4 ? x.cols - col : 4);
-      u = load4(grad + r * x.ld_grad + col, n);
+      u = load_n<4>(grad + r * x.ld_grad + col, n);
       if constexpr (MOM) {
         const f32x4 g = u;
-        u = load4(x.momentum + r * x.cols + col, n);
+        u = load_n<4>(x.momentum + r * x.cols + col, n);
         if (up.nesterov) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) u[k] = fmaf(up.mu, u[k], g[k]);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
       for (int k = 0; k < 4; ++k) u[k] = (float)((double)u[k] * f);
     }
     if (!sh.flip) {
-      if (r < sh.m && col < sh.ldx) store4(out + r * sh.ldx + col, u, 4);
+      if (r < sh.m && col < sh.ldx) store_n<4>(out + r * sh.ldx + col, u, 4);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) tile[rr][c + k] = u[k];
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
       f32x4 u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) u[k] = tile[c + k][l + 16 * p];
-      if (i < sh.m && j < sh.ldx) store4(out + i * sh.ldx + j, u, 4);
+      if (i < sh.m && j < sh.ldx) store_n<4>(out + i * sh.ldx + j, u, 4);
     }
   }
 }
@@ -205,11 +205,12 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
 
 // A = alpha X XT (POLY false: src = X, dst = A), or B = beta A + alpha A A
 // (POLY true: src = A, dst = B; A is its own transpose).
-template <class T, int BT, bool POLY>
-__global__ void __launch_bounds__(256) k_ns_symmetric(NsTable tab, NsTiles tiles, T* planes, int32_t next, float alpha,
-                                                      float beta) {
-  using P = TileProduct<T, BT, BT, 2, 2, true, true>;
-  __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+template <class T, int BT, int WM, int WN, bool POLY>
+__global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsTable tab, NsTiles tiles, T* planes, int32_t next,
+                                                               float alpha, float beta) {
+  using P = TileProduct<T, BT, BT, WM, WN, true, true, true>;
+  __shared__ __attribute__((aligned(16))) char lds[P::kStage];
+  __shared__ __attribute__((aligned(16))) char lds2[P::kStage];
   const int32_t t = (int32_t)xcd_run(blockIdx.x, gridDim.x);
   const int e = find_matrix(tiles, tab.count, t);
   const NsShape sh(tab.m[e].rows, tab.m[e].cols);
@@ -224,28 +225,34 @@ __global__ void __launch_bounds__(256) k_ns_symmetric(NsTable tab, NsTiles tiles
   const Operand<T> a{src + i0 * ld, ld, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
   const Operand<T> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
   f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, 0, ld, lds, acc);
-  P::each(acc, [&](int i, int j, f32x4 v) {
-    if (i >= a.rows || j0 + j >= sh.lda) return;
-    v *= alpha;
-    if constexpr (POLY) v += beta * load4(src + (i0 + i) * ld + j0 + j, 4);
-    store4(dst + (i0 + i) * sh.lda + j0 + j, v, 4);  // columns m .. lda - 1 get zeros
-    if (ti != tj) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (j + k < b.rows) dst[(j0 + j + k) * sh.lda + i0 + i] = (T)v[k];
-    }
-  });
+  P::run(a, b, 0, ld, lds, lds2, acc);
+  // Columns m .. lda - 1 get zeros.  The mirrored tile adds the same beta A,
+  // read where it lies.
+  P::each(
+      acc, lds, lds2, true, ti != tj,
+      [&](int i, int j, f32x8 v) {
+        if (i >= a.rows || j0 + j >= sh.lda) return;
+        v *= alpha;
+        if constexpr (POLY) v += beta * load_n<8>(src + (i0 + i) * ld + j0 + j, 8);
+        store_n<8>(dst + (i0 + i) * sh.lda + j0 + j, v, 8);
+      },
+      [&](int j, int i, f32x8 v) {
+        if (j >= b.rows || i >= a.rows) return;
+        v *= alpha;
+        if constexpr (POLY) v += beta * load_n<8>(src + (j0 + j) * ld + i0 + i, 8);
+        store_n<8>(dst + (j0 + j) * sh.lda + i0 + i, v, 8);
+      });
 }
 
 // X <- a X + beta B X into the other X plane, or out of it in the last step.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
-template <class T, class O, int BT, int LAST>
-__global__ void __launch_bounds__(256) k_ns_step(NsTable tab, NsTiles tiles, T* planes, int32_t next, float a_coef,
-                                                 float beta, NsUpdate up) {
-  using P = TileProduct<T, BT, BT, 2, 2, true, false>;
-  __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+template <class T, class O, int BT, int WM, int WN, int LAST>
+__global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles tiles, T* planes, int32_t next,
+                                                          float a_coef, float beta, NsUpdate up) {
+  using P = TileProduct<T, BT, BT, WM, WN, true, false, true>;
+  __shared__ __attribute__((aligned(16))) char lds[P::kStage];
+  __shared__ __attribute__((aligned(16))) char lds2[P::kStage];
   const int32_t t = (int32_t)xcd_run(blockIdx.x, gridDim.x);
   const int e = find_matrix(tiles, tab.count, t);
   const NsMatrix& x = tab.m[e];
@@ -259,34 +266,31 @@ __global__ void __launch_bounds__(256) k_ns_step(NsTable tab, NsTiles tiles, T* 
   const Operand<T> a{poly + i0 * sh.lda, sh.lda, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
   const Operand<T> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
   f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, 0, sh.m, lds, acc);
-  const float scale = LAST == kNsWeight ? x.scale * (up.lr_scale ? *up.lr_scale : 1.f) : 1.f;
-  const float keep = LAST == kNsWeight ? 1.f - up.decay * (up.lr_scale ? *up.lr_scale : 1.f) : 1.f;
-  P::each(acc, [&](int i, int j, f32x4 v) {
-    if (i >= a.rows || j >= b.rows) return;
-    v = beta * v + a_coef * load4(src + (i0 + i) * sh.ldx + j0 + j, 4);
-    if constexpr (LAST == kNsNext) {
-      store4(dst + (i0 + i) * sh.ldx + j0 + j, v, 4);
-    } else {
-      const int64_t left = sh.n - (j0 + j);
-      if (left <= 0) return;
-      const int n = (int)(left < 4 ? left : 4);
-      O* out = static_cast<O*>(x.out);
-      if (!sh.flip) {
-        O* p = out + (i0 + i) * x.ld_out + j0 + j;
-        if constexpr (LAST == kNsWeight) v = keep * load4(p, n) - scale * v;
-        store4(p, v, n);
-      } else {
+  P::run(a, b, 0, sh.m, lds, lds2, acc);
+  const float rate = LAST == kNsWeight && up.lr_scale ? *up.lr_scale : 1.f;
+  const float scale = x.scale * rate, keep = 1.f - up.decay * rate;
+  O* out = static_cast<O*>(x.out);
+  auto write = [&](O* p, f32x8 v, int64_t n) {
+    if constexpr (LAST == kNsWeight) v = keep * load_n<8>(p, n) - scale * v;
+    store_n<8>(p, v, n);
+  };
+  const bool flip = LAST != kNsNext && sh.flip;
+  P::each(
+      acc, lds, lds2, !flip, flip,
+      [&](int i, int j, f32x8 v) {
+        if (i >= a.rows || j >= b.rows) return;
+        v = beta * v + a_coef * load_n<8>(src + (i0 + i) * sh.ldx + j0 + j, 8);
+        if constexpr (LAST == kNsNext) store_n<8>(dst + (i0 + i) * sh.ldx + j0 + j, v, 8);
+        else write(out + (i0 + i) * x.ld_out + j0 + j, v, sh.n - (j0 + j));
+      },
+      [&](int j, int i, f32x8 v) {
+        if (j0 + j >= sh.n || i >= a.rows) return;
+        const int64_t n = a.rows - i;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < n) {
-            O* p = out + (j0 + j + k) * x.ld_out + i0 + i;
-            if constexpr (LAST == kNsWeight) *p = (O)(keep * (float)*p - scale * v[k]);
-            else *p = (O)v[k];
-          }
-      }
-    }
-  });
+        for (int k = 0; k < 8; ++k)
+          if (k < n) v[k] = beta * v[k] + a_coef * (float)src[(i0 + i + k) * sh.ldx + j0 + j];
+        write(out + (j0 + j) * x.ld_out + i0 + i, v, n);
+      });
 }
 
 // Largest |a x + b x^3 + c x^5| for 0 <= x <= top: at the ends or where the
@@ -375,7 +379,7 @@ int32_t fill_tiles(NsTiles& tiles, const NsTable& tab, F&& count) {
   return (int32_t)t;
 }
 
-template <class T, class G, class O, bool MOM, int BT>
+template <class T, class G, class O, bool MOM, int BT, int WM, int WN>
 void ns_chunk(const NsTable& tab, const NsLaunch& a, const NsScales& sc, const NsUpdate& up, double* parts,
               T* planes, hipStream_t stream) {
   NsTiles tiles;
@@ -396,13 +400,13 @@ void ns_chunk(const NsTable& tab, const NsLaunch& a, const NsScales& sc, const N
   for (int32_t k = 0; k < a.steps; ++k) {
     const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
     const int32_t next = k & 1;
-    k_ns_symmetric<T, BT, false><<<n_square, 256, 0, stream>>>(tab, square, planes, next, sc.a / (sc.x * sc.x), 0.f);
-    k_ns_symmetric<T, BT, true><<<n_square, 256, 0, stream>>>(tab, square, planes, next,
+    k_ns_symmetric<T, BT, WM, WN, false><<<n_square, WM * WN * 64, 0, stream>>>(tab, square, planes, next, sc.a / (sc.x * sc.x), 0.f);
+    k_ns_symmetric<T, BT, WM, WN, true><<<n_square, WM * WN * 64, 0, stream>>>(tab, square, planes, next,
                                                               cc * (sc.b[k] / (sc.a * sc.a)), cb * (sc.b[k] / sc.a));
     if (k + 1 < a.steps) {
-      k_ns_step<T, O, BT, kNsNext><<<n_wide, 256, 0, stream>>>(tab, wide, planes, next, ca, 1.f / sc.b[k], up);
+      k_ns_step<T, O, BT, WM, WN, kNsNext><<<n_wide, WM * WN * 64, 0, stream>>>(tab, wide, planes, next, ca, 1.f / sc.b[k], up);
     } else {
-      k_ns_step<T, O, BT, MOM ? kNsWeight : kNsOut><<<n_wide, 256, 0, stream>>>(
+      k_ns_step<T, O, BT, WM, WN, MOM ? kNsWeight : kNsOut><<<n_wide, WM * WN * 64, 0, stream>>>(
           tab, wide, planes, next, ca / sc.x, 1.f / (sc.b[k] * sc.x), up);
     }
   }
@@ -418,18 +422,21 @@ hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
     last = chunk_end(a.mats, a.num, first);
     NsTable tab;
     tab.count = last - first;
-    int64_t base = 0, tiles = 0;
+    int64_t base = 0, t256 = 0, t128 = 0;
     for (int32_t k = first; k < last; ++k) {
       const dc_matrix& d = a.mats[k];
       const NsShape sh(d.rows, d.cols);
       tab.m[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
                                   a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
       base += sh.values();
-      tiles += ((sh.m + 127) / 128) * ((sh.n + 127) / 128);
+      t256 += ((sh.m + 255) / 256) * ((sh.m + 255) / 256 + 1) / 2;
+      t128 += ((sh.m + 127) / 128) * ((sh.m + 127) / 128 + 1) / 2;
     }
-    // 128 x 128 tiles once they give every compute unit one
-    if (tiles >= 256) ns_chunk<T, G, O, MOM, 128>(tab, a, sc, up, parts, planes, stream);
-    else ns_chunk<T, G, O, MOM, 64>(tab, a, sc, up, parts, planes, stream);
+    // the largest tile whose symmetric products still give every compute unit
+    // about one
+    if (t256 >= 200) ns_chunk<T, G, O, MOM, 256, 2, 4>(tab, a, sc, up, parts, planes, stream);
+    else if (t128 >= 200) ns_chunk<T, G, O, MOM, 128, 2, 2>(tab, a, sc, up, parts, planes, stream);
+    else ns_chunk<T, G, O, MOM, 64, 2, 2>(tab, a, sc, up, parts, planes, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -21,7 +21,7 @@
 
 namespace dc {
 
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
@@ -45,6 +45,8 @@ __device__ __forceinline__ f32x4 mma_slice(u32x4 b, u32x4 a, f32x4 c, float) {
     c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[t]), __uint_as_float(a[t]), c, 0, 0, 0);
   return c;
 }
+
+typedef __attribute__((address_space(3))) char* LdsPtr;
 
 // One operand of a tile: `p` is the first value of the tile's first row (KC)
 // or column (KS), `rows` how many rows of the tile exist.
@@ -73,21 +75,30 @@ struct StageMap {
     else return (((line >> 1) & 1) | (((line >> 3) & 1) << 1)) << 1;
   }
 
-  // Fragment of 16 rows from `row0` for k-slice `ks`, for lane (q, r) =
-  // (lane / 16, lane % 16): this lane's share of row row0 + r.
-  __device__ static u32x4 fragment(const char* lds, int row0, int ks, int q, int r) {
+  // Where lane (q, r) = (lane / 16, lane % 16) finds its share of the 16-row
+  // fragments of rows row0, row0 + 16, ..: row0 is a multiple of all the
+  // fragments' rows.  The permutation depends on the lane alone, so fragment
+  // i and k-slice ks are reached from here by an XOR or a constant offset.
+  __device__ static uint32_t lane_base(int row0, int q, int r) {
     if constexpr (KC) {
-      const int row = row0 + r;
-      return *reinterpret_cast<const u32x4*>(lds + row * 128 + (((ks * 4 + q) ^ swizzle(row)) << 4));
+      return (row0 + r) * 128 + ((q ^ swizzle(r)) << 4);
+    } else if constexpr (ES == 4) {
+      return q * 4 * (CPR * 16) + ((((row0 + r) >> 2) ^ swizzle(q * 4)) << 4) + ((r & 3) << 2);
+    } else {
+      const int k = q * 8 + (r >> 2), col = row0 + ((r & 3) << 2);
+      return k * (CPR * 16) + (((col >> 3) ^ swizzle(k)) << 4) + ((col & 4) << 1);
+    }
+  }
+
+  __device__ static u32x4 fragment(LdsPtr lds, uint32_t base, int i, int ks) {
+    if constexpr (KC) {
+      return *(const __attribute__((address_space(3))) u32x4*)(lds + (base ^ (ks << 6)) + i * 2048);
     } else if constexpr (ES == 4) {
       u32x4 v;
-      const int col = row0 + r;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int k = ks * 16 + q * 4 + t;
-        v[t] = *reinterpret_cast<const uint32_t*>(lds + k * (CPR * 16) + (((col >> 2) ^ swizzle(k)) << 4) +
-                                                  ((col & 3) << 2));
-      }
+      for (int t = 0; t < 4; ++t)
+        v[t] = *(const __attribute__((address_space(3))) uint32_t*)(lds + (base ^ (i << 6)) +
+                                                                    (ks * 16 + t) * (CPR * 16));
       return v;
     } else {
       // The transposing read: the 16 lanes of a group name 16 runs of four
@@ -96,11 +107,8 @@ struct StageMap {
       u32x4 v;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = ks * 32 + q * 8 + h * 4 + (r >> 2);
-        const int col = row0 + ((r & 3) << 2);
-        const char* p = lds + k * (CPR * 16) + (((col >> 3) ^ swizzle(k)) << 4) + ((col & 4) << 1);
         const i16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) i16x4*)(p));
+            (__attribute__((address_space(3))) i16x4*)(lds + (base ^ (i << 5)) + (ks * 32 + h * 4) * (CPR * 16)));
         const uint64_t u = __builtin_bit_cast(uint64_t, t);
         v[2 * h] = (uint32_t)u;
         v[2 * h + 1] = (uint32_t)(u >> 32);
@@ -155,93 +163,227 @@ struct RegisterLoader {
   }
 };
 
+// Loads straight into LDS, for operands whose chunks are whole and aligned
+// (see direct_operand): a wave's 64 chunks land behind each other, so the
+// permutation is applied to the addresses they come from.  What is outside
+// gets an offset past the resource's end and arrives as zero.
+template <class T, int ROWS, bool KC, int NT>
+struct DirectLoader {
+  using Map = StageMap<T, ROWS, KC>;
+  static constexpr int kPer = Map::kChunks / NT;
+  static constexpr uint32_t kOutside = 0x80000000u;
+  uint32_t offset[kPer];
+
+  __device__ void init(const Operand<T>& op, int tid) {
+#pragma unroll
+    for (int s = 0; s < kPer; ++s) {
+      const int c = s * NT + tid;
+      const int line = c / Map::CPR, chunk = (c % Map::CPR) ^ Map::swizzle(line);
+      const bool in = KC ? line < op.rows : chunk * Map::EPC < op.rows;
+      offset[s] = in ? (uint32_t)line * (uint32_t)(op.ld * Map::ES) + chunk * 16 : kOutside;
+    }
+  }
+
+  // The stage at k0 into lds; `left` = k_end - k0.
+  __device__ void load(const Operand<T>& op, int64_t k0, int64_t left, char* lds, int tid, int wave) const {
+    const T* base = op.p + (KC ? k0 : k0 * op.ld);
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), (short)0, (int)kOutside, kBufferFlags);
+    auto issue = [&](int s, uint32_t off) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(lds + (s * NT + wave * 64) * 16), 16, (int)off, 0, 0, 0);
+    };
+    if (left >= Map::BK) {
+#pragma unroll
+      for (int s = 0; s < kPer; ++s) issue(s, offset[s]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kPer; ++s) {
+        const int c = s * NT + tid;
+        const int line = c / Map::CPR, chunk = (c % Map::CPR) ^ Map::swizzle(line);
+        issue(s, (KC ? chunk * Map::EPC : line) < left ? offset[s] : kOutside);
+      }
+    }
+  }
+};
+
+// Whether a stage of `op`'s matrix can be loaded straight into LDS: 16-byte
+// rows, contiguous lengths of whole chunks, and offsets inside a tile under
+// 2^31 bytes.
+template <class T>
+inline bool direct_operand(const void* p, int64_t ld, int64_t contiguous) {
+  constexpr int64_t epc = 16 / sizeof(T);
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % epc == 0 && contiguous % epc == 0 &&
+         ld * (int64_t)sizeof(T) * 256 < ((int64_t)1 << 31);
+}
+
 // One BM x BN tile by WM x WN waves; each wave holds MI x NI blocks of 16x16.
-template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB>
+template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, bool DIRECT>
 struct TileProduct {
   static constexpr int NT = WM * WN * 64;
   static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   using MapA = StageMap<T, BM, KCA>;
   using MapB = StageMap<T, BN, KCB>;
   static constexpr int BK = MapA::BK;
-  static constexpr int kLds = MapA::kBytes + MapB::kBytes;
+  static constexpr int kStage = MapA::kBytes + MapB::kBytes;
+  static constexpr int kLds = DIRECT ? 2 * kStage : kStage;
+
+  __device__ static void slice(LdsPtr la, LdsPtr lb, int ks, uint32_t base_a, uint32_t base_b,
+                               f32x4 (&acc)[MI][NI]) {
+    u32x4 fa[MI], fb[NI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[i] = MapA::fragment(la, base_a, i, ks);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[j] = MapB::fragment(lb, base_b, j, ks);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = mma_slice(fb[j], fa[i], acc[i][j], T{});
+  }
 
   // acc += A B over k in [k0, k_end); lds holds kLds bytes, 16-byte aligned.
   __device__ static void run(const Operand<T>& a, const Operand<T>& b, int64_t k0, int64_t k_end, char* lds,
-                             f32x4 (&acc)[MI][NI]) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+                             char* lds2, f32x4 (&acc)[MI][NI]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
-    const int row_a = (wave / WN) * (BM / WM), row_b = (wave % WN) * (BN / WN);
-    char* la = lds;
-    char* lb = lds + MapA::kBytes;
-    RegisterLoader<T, BM, KCA, NT> ra;
-    RegisterLoader<T, BN, KCB, NT> rb;
-    ra.load(a, k0, k_end, tid);
-    rb.load(b, k0, k_end, tid);
-    for (; k0 < k_end; k0 += BK) {
-      __syncthreads();  // every wave is done with the stage in LDS
-      ra.store(la, tid);
-      rb.store(lb, tid);
-      __syncthreads();
-      if (k0 + BK < k_end) {
-        ra.load(a, k0 + BK, k_end, tid);
-        rb.load(b, k0 + BK, k_end, tid);
+    const uint32_t base_a = MapA::lane_base((wave / WN) * (BM / WM), q, r);
+    const uint32_t base_b = MapB::lane_base((wave % WN) * (BN / WN), q, r);
+    if constexpr (DIRECT) {
+      // Two stages in LDS: while one is multiplied the next one arrives.
+      DirectLoader<T, BM, KCA, NT> da;
+      DirectLoader<T, BN, KCB, NT> db;
+      da.init(a, tid);
+      db.init(b, tid);
+      da.load(a, k0, k_end - k0, lds, tid, wave);
+      db.load(b, k0, k_end - k0, lds + MapA::kBytes, tid, wave);
+      // One stage; the two buffers are named apart, so that the compiler sees
+      // that reading one does not wait for what is arriving in the other.
+      auto stage = [&](char* cur, char* next) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of the stage is there
+        __syncthreads();                     // everybody's is, and the other stage is free
+        if (k0 + BK < k_end) {
+          da.load(a, k0 + BK, k_end - k0 - BK, next, tid, wave);
+          db.load(b, k0 + BK, k_end - k0 - BK, next + MapA::kBytes, tid, wave);
+        }
+        const LdsPtr la = (LdsPtr)cur;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) slice(la, la + MapA::kBytes, ks, base_a, base_b, acc);
+        k0 += BK;
+      };
+      while (k0 < k_end) {
+        stage(lds, lds2);
+        if (k0 < k_end) stage(lds2, lds);
       }
+    } else {
+      RegisterLoader<T, BM, KCA, NT> ra;
+      RegisterLoader<T, BN, KCB, NT> rb;
+      ra.load(a, k0, k_end, tid);
+      rb.load(b, k0, k_end, tid);
+      for (; k0 < k_end; k0 += BK) {
+        __syncthreads();  // every wave is done with the stage in LDS
+        ra.store(lds, tid);
+        rb.store(lds + MapA::kBytes, tid);
+        __syncthreads();
+        if (k0 + BK < k_end) {
+          ra.load(a, k0 + BK, k_end, tid);
+          rb.load(b, k0 + BK, k_end, tid);
+        }
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        u32x4 fa[MI], fb[NI];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i] = MapA::fragment(la, row_a + i * 16, ks, q, r);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) fb[j] = MapB::fragment(lb, row_b + j * 16, ks, q, r);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NI; ++j) acc[i][j] = mma_slice(fb[j], fa[i], acc[i][j], T{});
+        for (int ks = 0; ks < 2; ++ks) slice((LdsPtr)lds, (LdsPtr)lds + MapA::kBytes, ks, base_a, base_b, acc);
       }
     }
   }
 
-  // f(i, j, v): rows and columns inside the tile, v the sums of columns
-  // j .. j + 3 of row i.
-  template <class F>
-  __device__ static void each(const f32x4 (&acc)[MI][NI], F&& f) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row_a = (wave / WN) * (BM / WM) + (lane & 15), row_b = (wave % WN) * (BN / WN) + (lane >> 4) * 4;
+  // Hands the tile out eight values at a time: f(i, j, v) gets columns
+  // j .. j + 7 of row i when `rows` is set, ft(j, i, v) rows i .. i + 7 of
+  // column j when `cols` is, both inside the tile.  The accumulators go
+  // through the stages' memory, each wave by itself, so that a wave's accesses
+  // to the result are runs of whole rows (or columns) and the code for eight
+  // values exists once: with it in place for every accumulator, an epilogue
+  // with an activation no longer fitted the instruction cache and took ten
+  // times the product.
+  template <class F, class FT>
+  __device__ static void each(const f32x4 (&acc)[MI][NI], char* lds, char* lds2, bool rows, bool cols, F&& f,
+                              FT&& ft) {
+    constexpr int WR = BM / WM, WC = BN / WN;
+    constexpr int kHalf = DIRECT ? WM * WN / 2 : WM * WN;  // waves per stage's memory
+    constexpr int kWave = kStage / kHalf;
+    constexpr int RP = kWave / (WC * 4) < WR ? kWave / (WC * 4) : WR;  // rows per pass
+    static_assert(RP % 16 == 0 && WR % RP == 0, "passes");
+    constexpr int kMask = WC / 4 - 1;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, r = lane & 15;
+    const int row0 = (wave / WN) * WR, col0 = (wave % WN) * WC;
+    const LdsPtr mem = (LdsPtr)(wave < kHalf ? lds : lds2) + (wave % kHalf) * kWave;
+    auto chunk = [&](int row, int c) { return mem + row * (WC * 4) + ((c ^ (row & kMask)) << 4); };
+    __syncthreads();  // every wave is done with the last stage
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int p = 0; p < WR; p += RP) {
 #pragma unroll
-      for (int j = 0; j < NI; ++j) f(row_a + i * 16, row_b + j * 16, acc[i][j]);
+      for (int i = 0; i < RP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          *(__attribute__((address_space(3))) f32x4*)chunk(i * 16 + r, j * 4 + q) = acc[p / 16 + i][j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (rows) {
+        constexpr int kLanes = WC / 8;
+#pragma unroll 1
+        for (int k = lane / kLanes; k < RP; k += 64 / kLanes) {
+          const int c = (lane % kLanes) * 2;
+          const f32x4 lo = *(const __attribute__((address_space(3))) f32x4*)chunk(k, c);
+          const f32x4 hi = *(const __attribute__((address_space(3))) f32x4*)chunk(k, c + 1);
+          f(row0 + p + k, col0 + c * 4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+      }
+      if (cols) {
+        constexpr int kLanes = RP / 8;
+#pragma unroll 1
+        for (int c = lane / kLanes; c < WC; c += 64 / kLanes) {
+          const int k = (lane % kLanes) * 8;
+          f32x8 v;
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            v[t] = *(const __attribute__((address_space(3))) float*)(chunk(k + t, c >> 2) + ((c & 3) << 2));
+          ft(col0 + c, row0 + p + k, v);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
   }
 };
 
-// Four neighbouring values of a row as fp32, and back; `n` of them exist
-// (at least one).  The whole group is one access, unaligned where the row is.
-template <class T>
-__device__ __forceinline__ f32x4 load4(const T* p, int n) {
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (n >= 4) {
-    T e[4];
+// N neighbouring values of a row as fp32, and back; `n` of them exist (at
+// least one).  A whole group is one access (16 bytes at most), unaligned where
+// the row is.
+template <int N, class T>
+__device__ __forceinline__ auto load_n(const T* p, int64_t n) {
+  typedef float V __attribute__((ext_vector_type(N)));
+  V v = (V)(0.f);
+  if (n >= N) {
+    T e[N];
     __builtin_memcpy(e, p, sizeof e);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v[t] = (float)e[t];
+    for (int t = 0; t < N; ++t) v[t] = (float)e[t];
   } else {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < N; ++t)
       if (t < n) v[t] = (float)p[t];
   }
   return v;
 }
 
-template <class T>
-__device__ __forceinline__ void store4(T* p, f32x4 v, int n) {
-  if (n >= 4) {
-    T e[4];
+template <int N, class T, class V>
+__device__ __forceinline__ void store_n(T* p, V v, int64_t n) {
+  if (n >= N) {
+    T e[N];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) e[t] = (T)v[t];
+    for (int t = 0; t < N; ++t) e[t] = (T)v[t];
     __builtin_memcpy(p, e, sizeof e);
   } else {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < N; ++t)
       if (t < n) p[t] = (T)v[t];
   }
 }

@@ -806,7 +806,8 @@ dc_status dc_stream_rows_shaped(const void* src, int64_t src_ld_vec, int32_t row
  * as it was.  Outputs must not overlap inputs or other outputs (DC_ERR_ARG)
  * except where said; two matrices that interleave as column ranges of rows
  * with one common stride do not overlap.  Sizes are at most 2^28 and the
- * elements of one matrix at most 2^36 (2^34 for dc_matrix), else DC_ERR_SHAPE.
+ * elements of one matrix at most 2^36 (2^20 and 2^34 for dc_matrix), else
+ * DC_ERR_SHAPE.
  * A workspace is device memory, 16-byte aligned, of at least the bytes that
  * the query gives for the same arguments (else DC_ERR_SHAPE; NULL is allowed
  * when it gives 0); it is scratch: it need not be cleared, holds nothing
