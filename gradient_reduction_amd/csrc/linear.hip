@@ -80,11 +80,9 @@ struct ProductArgs {
   int64_t ld_partial;
 };
 
-template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, bool DIRECT, class Epi>
+template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, int S, class Epi>
 __global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi) {
-  using P = TileProduct<T, BM, BN, WM, WN, KCA, KCB, DIRECT>;
-  __shared__ __attribute__((aligned(16))) char lds[P::kStage];
-  __shared__ __attribute__((aligned(16))) char lds2[DIRECT ? P::kStage : 16];
+  using P = TileProduct<T, BM, BN, WM, WN, KCA, KCB, S>;
   const int64_t per = g.tiles_m * g.tiles_n;
   const int64_t t = xcd_run(blockIdx.x, gridDim.x);
   const int32_t split = (int32_t)(t / per);
@@ -98,10 +96,10 @@ __global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi
   const int64_t k0 = split * g.k_per_split;
   const int64_t k1 = k0 + g.k_per_split < g.k ? k0 + g.k_per_split : g.k;
   f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, k0, k1, lds, lds2, acc);
+  P::run(a, b, k0, k1, acc);
   float* part = g.splits > 1 ? g.partial + split * g.m * g.ld_partial : nullptr;
   P::each(
-      acc, lds, lds2, true, false,
+      acc, true, false,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j >= b.rows) return;
         if (part) store_n<8>(part + (i0 + i) * g.ld_partial + j0 + j, v, 8);
@@ -125,9 +123,7 @@ __global__ void __launch_bounds__(256) k_product_join(const float* partial, int6
 }
 
 // How a product of m x n over k is cut: the tile (256, 128 or 64 square) and
-// the splits of k whose estimated time is least.  A compute unit multiplies
-// at a rate that falls with the tile, holds 1, 2 or 4 workgroups, and runs
-// whole rounds of them; splits cost their sums' traffic and a launch.
+// the splits of k whose estimated time is least.
 struct Cut {
   int32_t tile, splits;
   int64_t k_per_split, ld_partial;
@@ -135,42 +131,33 @@ struct Cut {
 };
 
 Cut cut(int32_t dtype, int64_t m, int64_t n, int64_t k) {
-  constexpr int64_t kUnits = 256;
-  struct Shape {
-    int32_t tile, held;
-    double rate;  // of a compute unit, products per us at bf16
-  };
-  constexpr Shape kShapes[] = {{256, 1, 2.4e6}, {128, 2, 2.0e6}, {64, 4, 1.0e6}};
   const int64_t bk = dtype == DC_F32 ? 32 : 64;
-  const double slow = dtype == DC_F32 ? 12.0 : 1.0;
   const int64_t stages = std::max<int64_t>(1, (k + bk - 1) / bk);
   Cut best{};
   double least = 0;
-  for (const Shape& s : kShapes) {
-    const int64_t tiles = std::max<int64_t>(1, ((m + s.tile - 1) / s.tile) * ((n + s.tile - 1) / s.tile));
+  for (const int32_t tile : {256, 128, 64}) {
+    const int64_t tiles = std::max<int64_t>(1, ((m + tile - 1) / tile) * ((n + tile - 1) / tile));
     for (int64_t want = 1; want <= 64; ++want) {
-      if (want > 1 && (want > stages / 4 || tiles * want > 4 * kUnits)) break;
+      if (want > 1 && (want > stages / 4 || tiles * want > 4 * kComputeUnits)) break;
       const int64_t per = (stages + want - 1) / want, splits = (stages + per - 1) / per;
-      const int64_t groups = tiles * splits, slots = kUnits * s.held;
-      const int64_t full = groups / slots, rest = groups - full * slots;
-      // a unit holding h workgroups shares its rate among them
-      const double rounds = full * s.held + (rest + kUnits - 1) / kUnits;
-      double us = rounds * s.tile * s.tile * (per * bk) * slow / s.rate + 1.0 + 0.4 * per / s.held;
-      if (splits > 1) us += 2.5 + splits * m * n * 8.0 / 4e6;
+      const int64_t rounds = (tiles * splits + kComputeUnits - 1) / kComputeUnits;
+      double us = rounds * per * stage_us(dtype == DC_F32, tile);
+      // the sums written and read again, and a launch more
+      if (splits > 1) us += 3.0 + splits * m * n * 8.0 / 4e6;
       if (best.tile == 0 || us < least) {
         least = us;
-        best = Cut{s.tile, (int32_t)splits, per * bk, (n + 7) / 8 * 8};
+        best = Cut{tile, (int32_t)splits, per * bk, (n + 7) / 8 * 8};
       }
     }
   }
   return best;
 }
 
-template <class T, int BT, int WM, int WN, bool KCA, bool KCB, class Epi>
+template <class T, int BT, int WM, int WN, int S, bool KCA, bool KCB, class Epi>
 void launch_product(const ProductArgs& g, bool direct, const Epi& epi, hipStream_t stream) {
   const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n * g.splits));
-  if (direct) k_product<T, BT, BT, WM, WN, KCA, KCB, true, Epi><<<grid, WM * WN * 64, 0, stream>>>(g, epi);
-  else k_product<T, BT, BT, WM, WN, KCA, KCB, false, Epi><<<grid, WM * WN * 64, 0, stream>>>(g, epi);
+  if (direct) k_product<T, BT, BT, WM, WN, KCA, KCB, S, Epi><<<grid, WM * WN * 64, 0, stream>>>(g, epi);
+  else k_product<T, BT, BT, WM, WN, KCA, KCB, 1, Epi><<<grid, WM * WN * 64, 0, stream>>>(g, epi);
 }
 
 template <class T, bool KCA, bool KCB, class Epi>
@@ -180,9 +167,12 @@ hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, in
   const ProductArgs g{a, b, ld_a, ld_b, m, n, k, (m + c.tile - 1) / c.tile, (n + c.tile - 1) / c.tile, c.splits,
                       c.k_per_split, partial, c.ld_partial};
   const bool direct = direct_operand<T>(a, ld_a, KCA ? k : m) && direct_operand<T>(b, ld_b, KCB ? k : n);
-  if (c.tile == 256) launch_product<T, 256, 2, 4, KCA, KCB>(g, direct, epi, stream);
-  else if (c.tile == 128) launch_product<T, 128, 2, 2, KCA, KCB>(g, direct, epi, stream);
-  else launch_product<T, 64, 2, 2, KCA, KCB>(g, direct, epi, stream);
+  const bool deep = deep_launch(g.tiles_m * g.tiles_n * g.splits);
+  if (c.tile == 256) launch_product<T, 256, 2, 4, 2, KCA, KCB>(g, direct, epi, stream);
+  else if (c.tile == 128 && deep) launch_product<T, 128, 2, 4, 4, KCA, KCB>(g, direct, epi, stream);
+  else if (c.tile == 128) launch_product<T, 128, 2, 4, 2, KCA, KCB>(g, direct, epi, stream);
+  else if (deep) launch_product<T, 64, 2, 2, 8, KCA, KCB>(g, direct, epi, stream);
+  else launch_product<T, 64, 2, 2, 3, KCA, KCB>(g, direct, epi, stream);
   if (c.splits > 1) {
     const int64_t groups = m * ((n + 3) / 4);
     k_product_join<Epi><<<dim3((uint32_t)((groups + 255) / 256)), 256, 0, stream>>>(partial, c.ld_partial, c.splits,

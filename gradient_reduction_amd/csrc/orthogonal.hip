@@ -79,6 +79,13 @@ __device__ __forceinline__ int find_matrix(const NsTiles& tiles, int count, int3
   return lo;
 }
 
+// This workgroup's tile of its matrix: one XCD's workgroups take a run of
+// neighbouring tiles of every matrix.  (Runs over the whole list would give
+// the matrices with the longest sums, which come first, to one XCD.)
+__device__ __forceinline__ int32_t matrix_tile(const NsTiles& tiles, int e) {
+  return (int32_t)xcd_run((int32_t)blockIdx.x - tiles.begin[e], tiles.begin[e + 1] - tiles.begin[e]);
+}
+
 struct NsUpdate {
   float mu, decay;   // decay = lr wd
   int32_t nesterov;
@@ -205,14 +212,12 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
 
 // A = alpha X XT (POLY false: src = X, dst = A), or B = beta A + alpha A A
 // (POLY true: src = A, dst = B; A is its own transpose).
-template <class T, int BT, int WM, int WN, bool POLY>
+template <class T, int BT, int WM, int WN, int S, bool POLY>
 __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsTable tab, NsTiles tiles, T* planes, int32_t next,
                                                                float alpha, float beta) {
-  using P = TileProduct<T, BT, BT, WM, WN, true, true, true>;
-  __shared__ __attribute__((aligned(16))) char lds[P::kStage];
-  __shared__ __attribute__((aligned(16))) char lds2[P::kStage];
-  const int32_t t = (int32_t)xcd_run(blockIdx.x, gridDim.x);
-  const int e = find_matrix(tiles, tab.count, t);
+  using P = TileProduct<T, BT, BT, WM, WN, true, true, S>;
+  const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
+  const int32_t t = matrix_tile(tiles, e);
   const NsShape sh(tab.m[e].rows, tab.m[e].cols);
   T* x = planes + tab.m[e].base;
   T* a_plane = x + 2 * sh.x_size;
@@ -220,16 +225,16 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsTable tab, NsTi
   T* dst = POLY ? a_plane + sh.a_size : a_plane;
   const int64_t ld = POLY ? sh.lda : sh.ldx;
   int32_t ti, tj;
-  triangle_tile(t - tiles.begin[e], (int32_t)((sh.m + BT - 1) / BT), ti, tj);
+  triangle_tile(t, (int32_t)((sh.m + BT - 1) / BT), ti, tj);
   const int64_t i0 = (int64_t)ti * BT, j0 = (int64_t)tj * BT;
   const Operand<T> a{src + i0 * ld, ld, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
   const Operand<T> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
   f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, 0, ld, lds, lds2, acc);
+  P::run(a, b, 0, ld, acc);
   // Columns m .. lda - 1 get zeros.  The mirrored tile adds the same beta A,
   // read where it lies.
   P::each(
-      acc, lds, lds2, true, ti != tj,
+      acc, true, ti != tj,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j0 + j >= sh.lda) return;
         v *= alpha;
@@ -247,26 +252,24 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsTable tab, NsTi
 // X <- a X + beta B X into the other X plane, or out of it in the last step.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
-template <class T, class O, int BT, int WM, int WN, int LAST>
+template <class T, class O, int BT, int WM, int WN, int S, int LAST>
 __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles tiles, T* planes, int32_t next,
                                                           float a_coef, float beta, NsUpdate up) {
-  using P = TileProduct<T, BT, BT, WM, WN, true, false, true>;
-  __shared__ __attribute__((aligned(16))) char lds[P::kStage];
-  __shared__ __attribute__((aligned(16))) char lds2[P::kStage];
-  const int32_t t = (int32_t)xcd_run(blockIdx.x, gridDim.x);
-  const int e = find_matrix(tiles, tab.count, t);
+  using P = TileProduct<T, BT, BT, WM, WN, true, false, S>;
+  const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
+  const int32_t t = matrix_tile(tiles, e);
   const NsMatrix& x = tab.m[e];
   const NsShape sh(x.rows, x.cols);
   const T* src = planes + x.base + (next ? sh.x_size : 0);
   T* dst = planes + x.base + (next ? 0 : sh.x_size);
   const T* poly = planes + x.base + 2 * sh.x_size + sh.a_size;
   int64_t ti, tj;
-  band_tile(t - tiles.begin[e], (sh.m + BT - 1) / BT, (sh.n + BT - 1) / BT, 8, ti, tj);
+  band_tile(t, (sh.m + BT - 1) / BT, (sh.n + BT - 1) / BT, 8, ti, tj);
   const int64_t i0 = ti * BT, j0 = tj * BT;
   const Operand<T> a{poly + i0 * sh.lda, sh.lda, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
   const Operand<T> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
   f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, 0, sh.m, lds, lds2, acc);
+  P::run(a, b, 0, sh.m, acc);
   const float rate = LAST == kNsWeight && up.lr_scale ? *up.lr_scale : 1.f;
   const float scale = x.scale * rate, keep = 1.f - up.decay * rate;
   O* out = static_cast<O*>(x.out);
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles t
   };
   const bool flip = LAST != kNsNext && sh.flip;
   P::each(
-      acc, lds, lds2, !flip, flip,
+      acc, !flip, flip,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j >= b.rows) return;
         v = beta * v + a_coef * load_n<8>(src + (i0 + i) * sh.ldx + j0 + j, 8);
@@ -379,7 +382,78 @@ int32_t fill_tiles(NsTiles& tiles, const NsTable& tab, F&& count) {
   return (int32_t)t;
 }
 
-template <class T, class G, class O, bool MOM, int BT, int WM, int WN>
+// The products of a step.
+enum Product : int { kGram, kPoly, kStep };
+
+// The tile (256, 128 or 64 square) that is estimated to take a product of the
+// whole chunk fastest.  A compute unit takes stage_us for each stage and
+// tile_us for a tile's beginning and end; tiles of one length run in whole
+// rounds, of several lengths in the longest one's time or everybody's share
+// and half a shortest one.
+int ns_tile(const NsTable& tab, Product p, bool f32) {
+  int best = 0;
+  double least = 0;
+  for (const int tile : {256, 128, 64}) {
+    const double tile_us = tile == 256 ? 6.0 : tile == 128 ? 1.5 : 0.5;
+    double total = 0, count = 0, longest = 0, shortest = 1e30;
+    for (int k = 0; k < tab.count; ++k) {
+      const NsShape s(tab.m[k].rows, tab.m[k].cols);
+      const double tm = (double)((s.m + tile - 1) / tile), tn = (double)((s.n + tile - 1) / tile);
+      const double stages = std::ceil((p == kGram ? s.ldx : s.lda) / (f32 ? 32.0 : 64.0));
+      const double us = stages * stage_us(f32, tile) + tile_us;
+      const double tiles = p == kStep ? tm * tn : tm * (tm + 1) / 2;
+      total += tiles * us;
+      count += tiles;
+      longest = std::max(longest, us);
+      shortest = std::min(shortest, us);
+    }
+    const double us = shortest == longest ? std::ceil(count / kComputeUnits) * longest
+                                          : std::max(longest, total / kComputeUnits + shortest / 2);
+    if (best == 0 || us < least) {
+      least = us;
+      best = tile;
+    }
+  }
+  return best;
+}
+
+// The first tiles of a product's launch; returns their number.
+int32_t product_tiles(NsTiles& tiles, const NsTable& tab, Product p, int tile) {
+  return fill_tiles(tiles, tab, [&](const NsShape& s, const NsMatrix&) {
+    const int64_t tm = (s.m + tile - 1) / tile, tn = (s.n + tile - 1) / tile;
+    return p == kStep ? tm * tn : tm * (tm + 1) / 2;
+  });
+}
+
+template <class T, bool POLY>
+void launch_symmetric(const NsTable& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
+                      float alpha, float beta, hipStream_t stream) {
+  auto launch = [&](auto kernel, int threads) {
+    kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, alpha, beta);
+  };
+  const bool deep = deep_launch(n);
+  if (tile == 256) launch(k_ns_symmetric<T, 256, 2, 4, 2, POLY>, 512);
+  else if (tile == 128 && deep) launch(k_ns_symmetric<T, 128, 2, 4, 4, POLY>, 512);
+  else if (tile == 128) launch(k_ns_symmetric<T, 128, 2, 4, 2, POLY>, 512);
+  else if (deep) launch(k_ns_symmetric<T, 64, 2, 2, 8, POLY>, 256);
+  else launch(k_ns_symmetric<T, 64, 2, 2, 3, POLY>, 256);
+}
+
+template <class T, class O, int LAST>
+void launch_step(const NsTable& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
+                 float a_coef, float beta, const NsUpdate& up, hipStream_t stream) {
+  auto launch = [&](auto kernel, int threads) {
+    kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, a_coef, beta, up);
+  };
+  const bool deep = deep_launch(n);
+  if (tile == 256) launch(k_ns_step<T, O, 256, 2, 4, 2, LAST>, 512);
+  else if (tile == 128 && deep) launch(k_ns_step<T, O, 128, 2, 4, 4, LAST>, 512);
+  else if (tile == 128) launch(k_ns_step<T, O, 128, 2, 4, 2, LAST>, 512);
+  else if (deep) launch(k_ns_step<T, O, 64, 2, 2, 8, LAST>, 256);
+  else launch(k_ns_step<T, O, 64, 2, 2, 3, LAST>, 256);
+}
+
+template <class T, class G, class O, bool MOM>
 void ns_chunk(const NsTable& tab, const NsLaunch& a, const NsScales& sc, const NsUpdate& up, double* parts,
               T* planes, hipStream_t stream) {
   NsTiles tiles;
@@ -389,26 +463,27 @@ void ns_chunk(const NsTable& tab, const NsLaunch& a, const NsScales& sc, const N
     return (int64_t)((x.rows + 63) / 64) * ((x.cols + 63) / 64);
   });
   k_ns_load<T, G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts, a.eps, sc.x, planes);
-  NsTiles square, wide;
-  const int32_t n_square = fill_tiles(square, tab, [](const NsShape& s, const NsMatrix&) {
-    const int64_t nt = (s.m + BT - 1) / BT;
-    return nt * (nt + 1) / 2;
-  });
-  const int32_t n_wide = fill_tiles(wide, tab, [](const NsShape& s, const NsMatrix&) {
-    return ((s.m + BT - 1) / BT) * ((s.n + BT - 1) / BT);
-  });
+  constexpr bool f32 = sizeof(T) == 4;
+  const int gram_tile = ns_tile(tab, kGram, f32), poly_tile = ns_tile(tab, kPoly, f32),
+            step_tile = ns_tile(tab, kStep, f32);
+  // The last step of an update also reads and writes fp32 weights: two
+  // 128 tiles in a compute unit overlap that with products (4096 x 1024 and
+  // 1024 x 1024 matrices: 295 us against 356 us of one 256 tile).
+  const int last_tile = MOM && step_tile == 256 ? 128 : step_tile;
+  NsTiles gram, poly, step, last;
+  const int32_t n_gram = product_tiles(gram, tab, kGram, gram_tile), n_poly = product_tiles(poly, tab, kPoly, poly_tile),
+                n_step = product_tiles(step, tab, kStep, step_tile), n_last = product_tiles(last, tab, kStep, last_tile);
   for (int32_t k = 0; k < a.steps; ++k) {
     const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
     const int32_t next = k & 1;
-    k_ns_symmetric<T, BT, WM, WN, false><<<n_square, WM * WN * 64, 0, stream>>>(tab, square, planes, next, sc.a / (sc.x * sc.x), 0.f);
-    k_ns_symmetric<T, BT, WM, WN, true><<<n_square, WM * WN * 64, 0, stream>>>(tab, square, planes, next,
-                                                              cc * (sc.b[k] / (sc.a * sc.a)), cb * (sc.b[k] / sc.a));
-    if (k + 1 < a.steps) {
-      k_ns_step<T, O, BT, WM, WN, kNsNext><<<n_wide, WM * WN * 64, 0, stream>>>(tab, wide, planes, next, ca, 1.f / sc.b[k], up);
-    } else {
-      k_ns_step<T, O, BT, WM, WN, MOM ? kNsWeight : kNsOut><<<n_wide, WM * WN * 64, 0, stream>>>(
-          tab, wide, planes, next, ca / sc.x, 1.f / (sc.b[k] * sc.x), up);
-    }
+    launch_symmetric<T, false>(tab, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
+    launch_symmetric<T, true>(tab, poly, n_poly, poly_tile, planes, next, cc * (sc.b[k] / (sc.a * sc.a)),
+                              cb * (sc.b[k] / sc.a), stream);
+    if (k + 1 < a.steps)
+      launch_step<T, O, kNsNext>(tab, step, n_step, step_tile, planes, next, ca, 1.f / sc.b[k], up, stream);
+    else
+      launch_step<T, O, MOM ? kNsWeight : kNsOut>(tab, last, n_last, last_tile, planes, next, ca / sc.x,
+                                                  1.f / (sc.b[k] * sc.x), up, stream);
   }
 }
 
@@ -422,21 +497,19 @@ hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
     last = chunk_end(a.mats, a.num, first);
     NsTable tab;
     tab.count = last - first;
-    int64_t base = 0, t256 = 0, t128 = 0;
+    int64_t base = 0;
     for (int32_t k = first; k < last; ++k) {
       const dc_matrix& d = a.mats[k];
       const NsShape sh(d.rows, d.cols);
       tab.m[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
                                   a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
       base += sh.values();
-      t256 += ((sh.m + 255) / 256) * ((sh.m + 255) / 256 + 1) / 2;
-      t128 += ((sh.m + 127) / 128) * ((sh.m + 127) / 128 + 1) / 2;
     }
-    // the largest tile whose symmetric products still give every compute unit
-    // about one
-    if (t256 >= 200) ns_chunk<T, G, O, MOM, 256, 2, 4>(tab, a, sc, up, parts, planes, stream);
-    else if (t128 >= 200) ns_chunk<T, G, O, MOM, 128, 2, 2>(tab, a, sc, up, parts, planes, stream);
-    else ns_chunk<T, G, O, MOM, 64, 2, 2>(tab, a, sc, up, parts, planes, stream);
+    // the longest sums first, so that short ones fill what they leave
+    std::sort(tab.m, tab.m + tab.count, [](const NsMatrix& x, const NsMatrix& y) {
+      return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
+    });
+    ns_chunk<T, G, O, MOM>(tab, a, sc, up, parts, planes, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

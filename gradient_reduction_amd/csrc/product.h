@@ -16,6 +16,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "device_common.h"
 #include "internal.h"
 
@@ -172,38 +175,31 @@ struct DirectLoader {
   using Map = StageMap<T, ROWS, KC>;
   static constexpr int kPer = Map::kChunks / NT;
   static constexpr uint32_t kOutside = 0x80000000u;
-  uint32_t offset[kPer];
+  uint32_t offset[kPer], last[kPer];  // of whole stages, and of one of `rest` values of k
 
-  __device__ void init(const Operand<T>& op, int tid) {
+  __device__ void init(const Operand<T>& op, int rest, int tid) {
 #pragma unroll
     for (int s = 0; s < kPer; ++s) {
       const int c = s * NT + tid;
       const int line = c / Map::CPR, chunk = (c % Map::CPR) ^ Map::swizzle(line);
       const bool in = KC ? line < op.rows : chunk * Map::EPC < op.rows;
       offset[s] = in ? (uint32_t)line * (uint32_t)(op.ld * Map::ES) + chunk * 16 : kOutside;
+      last[s] = (KC ? chunk * Map::EPC : line) < rest ? offset[s] : kOutside;
     }
   }
 
-  // The stage at k0 into lds; `left` = k_end - k0.
-  __device__ void load(const Operand<T>& op, int64_t k0, int64_t left, char* lds, int tid, int wave) const {
+  // The stage at k0 into lds; `left` = k_end - k0.  One past the end reads
+  // nothing (its resource is empty).
+  __device__ void load(const Operand<T>& op, int64_t k0, int64_t left, char* lds, int wave) const {
     const T* base = op.p + (KC ? k0 : k0 * op.ld);
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), (short)0, (int)kOutside, kBufferFlags);
-    auto issue = [&](int s, uint32_t off) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<T*>(base), (short)0, left > 0 ? (int)kOutside : 0, kBufferFlags);
+    const bool whole = left >= Map::BK;
+#pragma unroll
+    for (int s = 0; s < kPer; ++s)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void*)(lds + (s * NT + wave * 64) * 16), 16, (int)off, 0, 0, 0);
-    };
-    if (left >= Map::BK) {
-#pragma unroll
-      for (int s = 0; s < kPer; ++s) issue(s, offset[s]);
-    } else {
-#pragma unroll
-      for (int s = 0; s < kPer; ++s) {
-        const int c = s * NT + tid;
-        const int line = c / Map::CPR, chunk = (c % Map::CPR) ^ Map::swizzle(line);
-        issue(s, (KC ? chunk * Map::EPC : line) < left ? offset[s] : kOutside);
-      }
-    }
+          rsrc, (__attribute__((address_space(3))) void*)(lds + (s * NT + wave * 64) * 16), 16,
+          (int)(whole ? offset[s] : last[s]), 0, 0, 0);
   }
 };
 
@@ -218,7 +214,21 @@ inline bool direct_operand(const void* p, int64_t ld, int64_t contiguous) {
 }
 
 // One BM x BN tile by WM x WN waves; each wave holds MI x NI blocks of 16x16.
-template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, bool DIRECT>
+// A stage's memory: one variable per stage, so that the compiler sees that
+// reading one does not wait for what is arriving in another.
+template <int I, int BYTES>
+__device__ __forceinline__ char* stage_memory() {
+  __shared__ __attribute__((aligned(16))) char memory[BYTES];
+  return memory;
+}
+
+template <class F, int... I>
+__device__ __forceinline__ void each_index(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
+// S stages are in flight or being multiplied; loads through registers use one.
+template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, int S>
 struct TileProduct {
   static constexpr int NT = WM * WN * 64;
   static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -226,7 +236,10 @@ struct TileProduct {
   using MapB = StageMap<T, BN, KCB>;
   static constexpr int BK = MapA::BK;
   static constexpr int kStage = MapA::kBytes + MapB::kBytes;
-  static constexpr int kLds = DIRECT ? 2 * kStage : kStage;
+  static constexpr bool kDirect = S > 1;
+
+  template <int I>
+  __device__ static char* memory() { return stage_memory<I % S, kStage>(); }
 
   __device__ static void slice(LdsPtr la, LdsPtr lb, int ks, uint32_t base_a, uint32_t base_b,
                                f32x4 (&acc)[MI][NI]) {
@@ -241,42 +254,54 @@ struct TileProduct {
       for (int j = 0; j < NI; ++j) acc[i][j] = mma_slice(fb[j], fa[i], acc[i][j], T{});
   }
 
-  // acc += A B over k in [k0, k_end); lds holds kLds bytes, 16-byte aligned.
-  __device__ static void run(const Operand<T>& a, const Operand<T>& b, int64_t k0, int64_t k_end, char* lds,
-                             char* lds2, f32x4 (&acc)[MI][NI]) {
+  // acc += A B over k in [k0, k_end).
+  __device__ static void run(const Operand<T>& a, const Operand<T>& b, int64_t k0, int64_t k_end,
+                             f32x4 (&acc)[MI][NI]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
     const uint32_t base_a = MapA::lane_base((wave / WN) * (BM / WM), q, r);
     const uint32_t base_b = MapB::lane_base((wave % WN) * (BN / WN), q, r);
-    if constexpr (DIRECT) {
-      // Two stages in LDS: while one is multiplied the next one arrives.
+    if constexpr (kDirect) {
       DirectLoader<T, BM, KCA, NT> da;
       DirectLoader<T, BN, KCB, NT> db;
-      da.init(a, tid);
-      db.init(b, tid);
-      da.load(a, k0, k_end - k0, lds, tid, wave);
-      db.load(b, k0, k_end - k0, lds + MapA::kBytes, tid, wave);
-      // One stage; the two buffers are named apart, so that the compiler sees
-      // that reading one does not wait for what is arriving in the other.
-      auto stage = [&](char* cur, char* next) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of the stage is there
-        __syncthreads();                     // everybody's is, and the other stage is free
-        if (k0 + BK < k_end) {
-          da.load(a, k0 + BK, k_end - k0 - BK, next, tid, wave);
-          db.load(b, k0 + BK, k_end - k0 - BK, next + MapA::kBytes, tid, wave);
-        }
+      const int rest = (int)((k_end - k0) % BK);
+      da.init(a, rest, tid);
+      db.init(b, rest, tid);
+      // Stages past the end are loaded too, which reads nothing and keeps the
+      // count of loads in flight the same.
+      auto load = [&](char* to, int64_t k) {
+        da.load(a, k, k_end - k, to, wave);
+        db.load(b, k, k_end - k, to + MapA::kBytes, wave);
+      };
+      constexpr int kFlight = (S - 2) * (da.kPer + db.kPer);
+      constexpr int kWait = (kFlight & 15) | (7 << 4) | ((kFlight >> 4) << 14);
+      auto stage = [&](char* cur, char* last) {
+        // this wave's part of the stage is there, and its reads of the one
+        // before are done; then everybody's
+        __builtin_amdgcn_s_waitcnt(kWait);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        load(last, k0 + (S - 1) * BK);
+        __builtin_amdgcn_sched_barrier(0);  // the loads go out first (left to the end: 15% slower)
         const LdsPtr la = (LdsPtr)cur;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) slice(la, la + MapA::kBytes, ks, base_a, base_b, acc);
         k0 += BK;
       };
-      while (k0 < k_end) {
-        stage(lds, lds2);
-        if (k0 < k_end) stage(lds2, lds);
-      }
+      each_index([&](auto i) { load(memory<i.value>(), k0 + i.value * BK); },
+                 std::make_integer_sequence<int, S - 1>{});
+      while (k0 < k_end)
+        each_index(
+            [&](auto i) {
+              if (i.value == 0 || k0 < k_end) stage(memory<i.value>(), memory<i.value + S - 1>());
+            },
+            std::make_integer_sequence<int, S>{});
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // nothing arrives any more
     } else {
       RegisterLoader<T, BM, KCA, NT> ra;
       RegisterLoader<T, BN, KCB, NT> rb;
+      char* lds = memory<0>();
       ra.load(a, k0, k_end, tid);
       rb.load(b, k0, k_end, tid);
       for (; k0 < k_end; k0 += BK) {
@@ -303,18 +328,24 @@ struct TileProduct {
   // with an activation no longer fitted the instruction cache and took ten
   // times the product.
   template <class F, class FT>
-  __device__ static void each(const f32x4 (&acc)[MI][NI], char* lds, char* lds2, bool rows, bool cols, F&& f,
-                              FT&& ft) {
+  __device__ static void each(const f32x4 (&acc)[MI][NI], bool rows, bool cols, F&& f, FT&& ft) {
     constexpr int WR = BM / WM, WC = BN / WN;
-    constexpr int kHalf = DIRECT ? WM * WN / 2 : WM * WN;  // waves per stage's memory
-    constexpr int kWave = kStage / kHalf;
-    constexpr int RP = kWave / (WC * 4) < WR ? kWave / (WC * 4) : WR;  // rows per pass
-    static_assert(RP % 16 == 0 && WR % RP == 0, "passes");
+    constexpr int kShare = (WM * WN + S - 1) / S;  // waves per stage's memory
+    constexpr int kWave = kStage / kShare;
+    constexpr int kFit = kWave / (WC * 4);
+    constexpr int RP = kFit >= WR ? WR : kFit >= WR / 2 ? WR / 2 : WR / 4;  // rows per pass
+    static_assert(RP % 16 == 0 && RP <= kFit, "passes");
     constexpr int kMask = WC / 4 - 1;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, r = lane & 15;
     const int row0 = (wave / WN) * WR, col0 = (wave % WN) * WC;
-    const LdsPtr mem = (LdsPtr)(wave < kHalf ? lds : lds2) + (wave % kHalf) * kWave;
+    char* own = memory<0>();
+    each_index(
+        [&](auto i) {
+          if (wave / kShare == i.value) own = memory<i.value>();
+        },
+        std::make_integer_sequence<int, S>{});
+    const LdsPtr mem = (LdsPtr)own + (wave % kShare) * kWave;
     auto chunk = [&](int row, int c) { return mem + row * (WC * 4) + ((c ^ (row & kMask)) << 4); };
     __syncthreads();  // every wave is done with the last stage
 #pragma unroll
@@ -386,6 +417,22 @@ __device__ __forceinline__ void store_n(T* p, V v, int64_t n) {
     for (int t = 0; t < N; ++t)
       if (t < n) p[t] = (T)v[t];
   }
+}
+
+constexpr int64_t kComputeUnits = 256;
+
+// Stages in flight of a launch of `tiles` tiles: with no more tiles than
+// compute units each has a unit's memory for itself, and then as many stages
+// as fit hide the latency of what the launch before left in other caches.
+inline bool deep_launch(int64_t tiles) { return tiles <= kComputeUnits; }
+
+// Microseconds that a compute unit takes for a stage of a tile, as measured
+// with the unit busy (one 256 tile, two of 128, three of 64 resident) and, the
+// same, with one 128 or 64 tile alone: 2 tile^2 64 operations at 1.26, 1.0 and
+// 0.7 PFLOP/s over the chip; fp32 is held by the matrix cores' fp32 rate.
+inline double stage_us(bool f32, int tile) {
+  if (f32) return tile == 256 ? 6.9 : tile == 128 ? 1.75 : 0.45;
+  return tile == 256 ? 1.65 : tile == 128 ? 0.54 : 0.19;
 }
 
 // Workgroup b of n, with the workgroups of one XCD (b mod 8) on one run of
