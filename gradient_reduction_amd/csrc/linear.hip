@@ -11,14 +11,50 @@
 namespace dc {
 namespace {
 
-// act(v) and its slope, in fp32.  gelu is the exact one: v Phi(v), with
-// Phi(v) = erfc(-v / sqrt 2) / 2, which keeps its relative accuracy in the
-// lower tail.
+// Activations and their slopes in fp32, to about 2^-21 of the result, from
+// the hardware's 2^x and 1/x: with the library's exp, erfc and correctly
+// rounded division the elementwise backward was bound by its arithmetic (129
+// us on 8192 x 11008 bf16 where its bytes take 84).
+
+// exp(x), x <= 88 taken: 2^(x log2 e) with what the product rounds off.
+__device__ __forceinline__ float exp_fast(float x) {
+  x = fminf(x, 88.f);
+  const float t = x * 1.44269504f;
+  const float r = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * 0.693147181f, e);
+}
+
+// 1 / (1 + exp(-v)).
+__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + exp_fast(-v)); }
+
+// Phi(v), the normal distribution's, and e = exp(-v^2 / 2).  With z = |v| /
+// sqrt 2 and t = 1 / (1 + z / 2), erfc(z) exp(z^2) / t is a smooth function of
+// t on (0, 1]: the polynomial is its least-squares fit in relative error,
+// reweighted towards the least maximum (4e-8 over z < 9.5, 4e-7 as computed
+// here); past that e is zero in fp32.
+__device__ __forceinline__ float normal_cdf(float v, float& e) {
+  e = exp_fast(-0.5f * v * v);
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.353553391f, 1.f));
+  float p = -5.889142478e-02f;
+  p = fmaf(p, t, 2.837050295e-01f);
+  p = fmaf(p, t, -4.853898047e-01f);
+  p = fmaf(p, t, 2.759848175e-01f);
+  p = fmaf(p, t, -2.518203246e-02f);
+  p = fmaf(p, t, 2.020715627e-01f);
+  p = fmaf(p, t, 2.432606008e-01f);
+  p = fmaf(p, t, 2.823535357e-01f);
+  p = fmaf(p, t, 2.820876737e-01f);
+  const float tail = 0.5f * e * p * t;
+  return v < 0.f ? tail : 1.f - tail;
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
+  float e;
   switch (act) {
     case DC_ACT_RELU: return v > 0.f || v != v ? v : 0.f;
-    case DC_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case DC_ACT_SILU: return v / (1.f + expf(-v));
+    case DC_ACT_GELU: return v * normal_cdf(v, e);
+    case DC_ACT_SILU: return v * sigmoid(v);
     default: return v;
   }
 }
@@ -26,11 +62,14 @@ __device__ __forceinline__ float activate(float v, int act) {
 __device__ __forceinline__ float activation_slope(float v, int act) {
   switch (act) {
     case DC_ACT_RELU: return v > 0.f ? 1.f : 0.f;
-    case DC_ACT_GELU:
-      return 0.5f * erfcf(-0.70710678118654752f * v) + 0.39894228040143268f * v * expf(-0.5f * v * v);
+    case DC_ACT_GELU: {
+      float e;
+      const float phi = normal_cdf(v, e);
+      return fmaf(0.39894228040143268f * v, e, phi);
+    }
     case DC_ACT_SILU: {
-      const float p = 1.f / (1.f + expf(-v));
-      return p * (1.f + v * (1.f - p));
+      const float p = sigmoid(v);
+      return p * fmaf(v, 1.f - p, 1.f);
     }
     default: return 1.f;
   }
@@ -181,6 +220,84 @@ hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, in
   return hipGetLastError();
 }
 
+// A few rows (a single token's, or a decoding batch's): x wT with w streamed
+// once from memory straight into the matrix cores' layout, no LDS between.  A
+// workgroup takes 16 NI outputs and its eight waves a share of k each, so that
+// w's rows are read by enough waves to keep the memory busy; their sums are
+// added in the waves' order.  Bound by w's bytes.
+template <class T, int TI, int NI, class Epi>
+__global__ void __launch_bounds__(512) k_linear_few(const T* x, int64_t ld_x, const T* w, int64_t ld_w, int32_t rows,
+                                                    int64_t n, int64_t k, Epi epi) {
+  constexpr int EPC = 16 / sizeof(T), kSlice = 4 * EPC, kWaves = 8, U = 4;
+  __shared__ f32x4 sums[kWaves][TI * NI][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int64_t j0 = (int64_t)blockIdx.x * (16 * NI);
+  // whole groups of U slices per wave, so that a group's loads are in flight
+  // together
+  const int64_t groups = (k + kSlice * U - 1) / (kSlice * U), share = (groups + kWaves - 1) / kWaves;
+  const int64_t k0 = wave * share * (kSlice * U), k1 = k0 + share * (kSlice * U) < k ? k0 + share * (kSlice * U) : k;
+  f32x4 acc[TI][NI] = {};
+  auto chunk = [&](const T* row, bool there, int64_t at) {
+    u32x4 v = {0, 0, 0, 0};
+    const int64_t left = there ? k1 - at : 0;
+    if (left >= EPC) {
+      __builtin_memcpy(&v, row + at, 16);
+    } else if (left > 0) {
+      T e[EPC];
+#pragma unroll
+      for (int t = 0; t < EPC; ++t) e[t] = t < left ? row[at + t] : (T)0;
+      __builtin_memcpy(&v, e, 16);
+    }
+    return v;
+  };
+  for (int64_t at = k0 + q * EPC; at < k1 + q * EPC; at += kSlice * U) {
+    u32x4 fw[U][NI], fx[U][TI];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int b = 0; b < NI; ++b)
+        fw[u][b] = chunk(w + (j0 + b * 16 + r) * ld_w, j0 + b * 16 + r < n, at + u * kSlice);
+#pragma unroll
+      for (int a = 0; a < TI; ++a) fx[u][a] = chunk(x + (a * 16 + r) * ld_x, a * 16 + r < rows, at + u * kSlice);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int a = 0; a < TI; ++a)
+#pragma unroll
+        for (int b = 0; b < NI; ++b) acc[a][b] = mma_slice(fw[u][b], fx[u][a], acc[a][b], T{});
+  }
+#pragma unroll
+  for (int a = 0; a < TI; ++a)
+#pragma unroll
+    for (int b = 0; b < NI; ++b) sums[wave][a * NI + b][lane] = acc[a][b];
+  __syncthreads();
+  // wave f adds up the blocks f, f + 8, ..
+  for (int f = wave; f < TI * NI; f += kWaves) {
+    f32x4 v = sums[0][f][lane];
+#pragma unroll
+    for (int s = 1; s < kWaves; ++s) v += sums[s][f][lane];
+    const int64_t i = (f / NI) * 16 + r, j = j0 + (f % NI) * 16 + q * 4;
+    if (i < rows && j < n) epi(i, j, v);
+  }
+}
+
+constexpr int64_t kFewRows = 64;
+
+template <class T, class Epi>
+hipError_t few_rows(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int64_t rows, int64_t n, int64_t k,
+                    const Epi& epi, hipStream_t stream) {
+  auto launch = [&](auto kernel, int per) {
+    kernel<<<dim3((uint32_t)((n + per - 1) / per)), 512, 0, stream>>>(
+        static_cast<const T*>(x), ld_x, static_cast<const T*>(w), ld_w, (int32_t)rows, n, k, epi);
+  };
+  if (rows <= 16) launch(k_linear_few<T, 1, 1, Epi>, 16);
+  else if (rows <= 32) launch(k_linear_few<T, 2, 1, Epi>, 16);
+  else launch(k_linear_few<T, 4, 2, Epi>, 32);
+  return hipGetLastError();
+}
+
 // dz = dy act'(pre) and the column sums of dz, in strips of `strip` rows: one
 // workgroup per 32 chunks of 16 bytes of columns and strip, eight rows at a
 // time.  The strips' sums go to partial[strip][n] and are added in order by
@@ -197,36 +314,46 @@ __global__ void __launch_bounds__(256) k_bias_act(int64_t rows, int64_t n, const
   const int64_t left = n - j;
   float s[V] = {};
   if (left > 0) {
-    for (int64_t i = i0 + l; i < i1; i += 8) {
-      T d[V] = {}, z[V] = {};
+    auto load = [&](const T* p, T* to) {
       if (left >= V) {
-        __builtin_memcpy(d, dy + i * ld_dy + j, 16);
-        if (pre) __builtin_memcpy(z, pre + i * ld_pre + j, 16);
+        __builtin_memcpy(to, p, 16);
       } else {
 #pragma unroll
-        for (int t = 0; t < V; ++t)
-          if (t < left) {
-            d[t] = dy[i * ld_dy + j + t];
-            if (pre) z[t] = pre[i * ld_pre + j + t];
-          }
+        for (int t = 0; t < V; ++t) to[t] = t < left ? p[t] : (T)0;
       }
-      T o[V];
+    };
+    // U rows' loads in flight at once
+    constexpr int U = 4;
+    for (int64_t i = i0 + l; i < i1; i += 8 * U) {
+      T d[U][V], z[U][V];
 #pragma unroll
-      for (int t = 0; t < V; ++t) {
-        float v = (float)d[t];
-        if (pre) v *= activation_slope((float)z[t], act);
-        s[t] += v;
-        o[t] = (T)v;
-      }
-      if (dz) {
-        if (left >= V) {
-          __builtin_memcpy(dz + i * ld_dz + j, o, 16);
-        } else {
-#pragma unroll
-          for (int t = 0; t < V; ++t)
-            if (t < left) dz[i * ld_dz + j + t] = o[t];
+      for (int u = 0; u < U; ++u)
+        if (i + 8 * u < i1) {
+          load(dy + (i + 8 * u) * ld_dy + j, d[u]);
+          if (pre) load(pre + (i + 8 * u) * ld_pre + j, z[u]);
         }
-      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + 8 * u < i1) {
+          T o[V];
+#pragma unroll
+          for (int t = 0; t < V; ++t) {
+            float v = (float)d[u][t];
+            if (pre) v *= activation_slope((float)z[u][t], act);
+            s[t] += v;
+            o[t] = (T)v;
+          }
+          if (dz) {
+            T* p = dz + (i + 8 * u) * ld_dz + j;
+            if (left >= V) {
+              __builtin_memcpy(p, o, 16);
+            } else {
+#pragma unroll
+              for (int t = 0; t < V; ++t)
+                if (t < left) p[t] = o[t];
+            }
+          }
+        }
     }
   }
   if (!db) return;
@@ -294,6 +421,7 @@ hipError_t bias_act(int32_t dtype, int64_t rows, int64_t n, const void* dy, int6
 }  // namespace
 
 int64_t linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K) {
+  if (T <= kFewRows) return 0;
   return cut(dtype, T, N, K).partial_bytes(T);
 }
 
@@ -309,6 +437,10 @@ int64_t bias_act_workspace(int32_t dtype, int64_t T, int64_t N) {
 hipError_t launch_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x, const void* w,
                          int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream) {
   if (T == 0) return hipSuccess;
+  if (T <= kFewRows) {
+    if (dtype == DC_BF16) return few_rows<__bf16>(x, ld_x, w, ld_w, T, N, K, LinearEpilogue<__bf16>{o, N}, stream);
+    return few_rows<float>(x, ld_x, w, ld_w, T, N, K, LinearEpilogue<float>{o, N}, stream);
+  }
   float* ws = static_cast<float*>(workspace);
   if (dtype == DC_BF16)
     return product<__bf16, true, true>(dtype, x, ld_x, w, ld_w, T, N, K, ws, LinearEpilogue<__bf16>{o, N}, stream);

@@ -4,7 +4,7 @@
 //   X <- U / (|U|_F + eps)              U = G, or the momentum's look-ahead
 //   repeat: A = X XT; B = b A + c A A; X <- a X + B X
 //   O = X, or W <- (1 - lr wd) W - lr s X
-// Every step is one launch for a chunk of up to kNsChunk matrices: a workgroup
+// Every product is one launch for a chunk of up to kNsChunk matrices: a workgroup
 // finds its matrix by its tile number.  A and B are symmetric, so only tiles
 // on and above their diagonal are computed and each is written twice.
 #include <hip/hip_runtime.h>
@@ -18,7 +18,8 @@
 namespace dc {
 namespace {
 
-constexpr int kNsChunk = 40;          // matrices per launch: their table is a kernel argument
+constexpr int kNsChunk = 128;         // matrices whose products share launches
+constexpr int kNsPart = 48;           // of them whose addresses fit one launch's arguments
 constexpr int kNormParts = 256;       // partial sums of squares per matrix, at most
 constexpr int64_t kNormSpan = 16384;  // elements per partial sum, at least
 
@@ -34,17 +35,29 @@ struct NsMatrix {
   float scale;  // lr times the shape's factor (update only)
 };
 
+// Tables that travel as kernel arguments: up to kNsPart matrices with their
+// addresses, or a whole chunk's planes.
 struct NsTable {
   int32_t count;
-  NsMatrix m[kNsChunk];
+  int32_t first;  // of the chunk
+  NsMatrix m[kNsPart];
 };
 
-// First tile of every matrix of the chunk, and their number.
+struct NsPlanes {
+  int32_t count;
+  struct {
+    int64_t base;
+    int32_t rows, cols;
+  } m[kNsChunk];
+};
+
+// First tile of every matrix of a table, and their number.
 struct NsTiles {
   int32_t begin[kNsChunk + 1];
 };
 
 static_assert(sizeof(NsTable) + sizeof(NsTiles) + 128 <= 4096, "kernel arguments");
+static_assert(sizeof(NsPlanes) + sizeof(NsTiles) + 128 <= 4096, "kernel arguments");
 
 __host__ __device__ inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 __host__ __device__ inline int64_t up128(int64_t v) { return (v + 127) / 128 * 128; }
@@ -69,14 +82,13 @@ __host__ __device__ inline int32_t norm_parts(int64_t rows, int64_t cols) {
   return (int32_t)(p < 1 ? 1 : p > kNormParts ? kNormParts : p);
 }
 
-// The matrix of tile t: the last one whose first tile is at or before t.
+// The matrix of tile t: the last one whose first tile is at or before t.  Every
+// lane looks at one or two.
 __device__ __forceinline__ int find_matrix(const NsTiles& tiles, int count, int32_t t) {
-  int lo = 0, hi = count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tiles.begin[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
+  const int lane = threadIdx.x & 63;
+  int n = __popcll(__ballot(lane < count && tiles.begin[lane] <= t));
+  if (count > 64) n += __popcll(__ballot(lane + 64 < count && tiles.begin[lane + 64] <= t));
+  return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 // This workgroup's tile of its matrix: one XCD's workgroups take a run of
@@ -133,7 +145,7 @@ __global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsU
   for (int d = 32; d > 0; d >>= 1) s += __shfl_down(s, d);
   if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) parts[(int64_t)e * kNormParts + part] = sum[0] + sum[1] + sum[2] + sum[3];
+  if (threadIdx.x == 0) parts[(int64_t)(tab.first + e) * kNormParts + part] = sum[0] + sum[1] + sum[2] + sum[3];
 }
 
 // X = U scale / (|U|_F + eps), transposed where rows > cols, 64 x 64 at a
@@ -147,7 +159,7 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
   __shared__ float tile[64][65];
   __shared__ double total[4];
   const int np = norm_parts(x.rows, x.cols);
-  double s = threadIdx.x < (unsigned)np ? parts[(int64_t)e * kNormParts + threadIdx.x] : 0.0;
+  double s = threadIdx.x < (unsigned)np ? parts[(int64_t)(tab.first + e) * kNormParts + threadIdx.x] : 0.0;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) s += __shfl_down(s, d);
   if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = s;
@@ -213,7 +225,7 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
 // A = alpha X XT (POLY false: src = X, dst = A), or B = beta A + alpha A A
 // (POLY true: src = A, dst = B; A is its own transpose).
 template <class T, int BT, int WM, int WN, int S, bool POLY>
-__global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsTable tab, NsTiles tiles, T* planes, int32_t next,
+__global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsTiles tiles, T* planes, int32_t next,
                                                                float alpha, float beta) {
   using P = TileProduct<T, BT, BT, WM, WN, true, true, S>;
   const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
@@ -252,13 +264,13 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsTable tab, NsTi
 // X <- a X + beta B X into the other X plane, or out of it in the last step.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
-template <class T, class O, int BT, int WM, int WN, int S, int LAST>
-__global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles tiles, T* planes, int32_t next,
+template <class T, class O, int BT, int WM, int WN, int S, int LAST, class Table>
+__global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles tiles, T* planes, int32_t next,
                                                           float a_coef, float beta, NsUpdate up) {
   using P = TileProduct<T, BT, BT, WM, WN, true, false, S>;
   const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
   const int32_t t = matrix_tile(tiles, e);
-  const NsMatrix& x = tab.m[e];
+  const auto& x = tab.m[e];
   const NsShape sh(x.rows, x.cols);
   const T* src = planes + x.base + (next ? sh.x_size : 0);
   T* dst = planes + x.base + (next ? 0 : sh.x_size);
@@ -270,9 +282,16 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles t
   const Operand<T> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
   f32x4 acc[P::MI][P::NI] = {};
   P::run(a, b, 0, sh.m, acc);
-  const float rate = LAST == kNsWeight && up.lr_scale ? *up.lr_scale : 1.f;
-  const float scale = x.scale * rate, keep = 1.f - up.decay * rate;
-  O* out = static_cast<O*>(x.out);
+  O* out = nullptr;
+  int64_t ld_out = 0;
+  float scale = 1.f, keep = 1.f;
+  if constexpr (LAST != kNsNext) {
+    out = static_cast<O*>(x.out);
+    ld_out = x.ld_out;
+    const float rate = LAST == kNsWeight && up.lr_scale ? *up.lr_scale : 1.f;
+    scale = x.scale * rate;
+    keep = 1.f - up.decay * rate;
+  }
   auto write = [&](O* p, f32x8 v, int64_t n) {
     if constexpr (LAST == kNsWeight) v = keep * load_n<8>(p, n) - scale * v;
     store_n<8>(p, v, n);
@@ -284,7 +303,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles t
         if (i >= a.rows || j >= b.rows) return;
         v = beta * v + a_coef * load_n<8>(src + (i0 + i) * sh.ldx + j0 + j, 8);
         if constexpr (LAST == kNsNext) store_n<8>(dst + (i0 + i) * sh.ldx + j0 + j, v, 8);
-        else write(out + (i0 + i) * x.ld_out + j0 + j, v, sh.n - (j0 + j));
+        else write(out + (i0 + i) * ld_out + j0 + j, v, sh.n - (j0 + j));
       },
       [&](int j, int i, f32x8 v) {
         if (j0 + j >= sh.n || i >= a.rows) return;
@@ -292,7 +311,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(NsTable tab, NsTiles t
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < n) v[k] = beta * v[k] + a_coef * (float)src[(i0 + i + k) * sh.ldx + j0 + j];
-        write(out + (j0 + j) * x.ld_out + i0 + i, v, n);
+        write(out + (j0 + j) * ld_out + i0 + i, v, n);
       });
 }
 
@@ -356,7 +375,9 @@ NsScales ns_scales(int32_t dtype, int32_t steps, const float* coeffs) {
 int32_t chunk_end(const dc_matrix* mats, int32_t n, int32_t first) {
   int64_t tiles = 0;
   int32_t k = first;
-  for (; k < n && k < first + kNsChunk; ++k) {
+  // what is left, in chunks of about one size
+  const int32_t left = n - first, even = (left + (left + kNsChunk - 1) / kNsChunk - 1) / ((left + kNsChunk - 1) / kNsChunk);
+  for (; k < n && k < first + even; ++k) {
     tiles += ((int64_t)(mats[k].rows + 63) / 64) * ((mats[k].cols + 63) / 64);
     if (k > first && tiles > ((int64_t)1 << 22)) break;
   }
@@ -371,12 +392,12 @@ int64_t chunk_values(const dc_matrix* mats, int32_t first, int32_t last) {
 
 constexpr int64_t kPartsBytes = (int64_t)kNsChunk * kNormParts * 8;
 
-template <class F>
-int32_t fill_tiles(NsTiles& tiles, const NsTable& tab, F&& count) {
+template <class Table, class F>
+int32_t fill_tiles(NsTiles& tiles, const Table& tab, F&& count) {
   int64_t t = 0;
   for (int k = 0; k < tab.count; ++k) {
     tiles.begin[k] = (int32_t)t;
-    t += count(NsShape(tab.m[k].rows, tab.m[k].cols), tab.m[k]);
+    t += count(NsShape(tab.m[k].rows, tab.m[k].cols));
   }
   for (int k = tab.count; k <= kNsChunk; ++k) tiles.begin[k] = (int32_t)t;
   return (int32_t)t;
@@ -390,7 +411,7 @@ enum Product : int { kGram, kPoly, kStep };
 // tile_us for a tile's beginning and end; tiles of one length run in whole
 // rounds, of several lengths in the longest one's time or everybody's share
 // and half a shortest one.
-int ns_tile(const NsTable& tab, Product p, bool f32) {
+int ns_tile(const NsPlanes& tab, Product p, bool f32) {
   int best = 0;
   double least = 0;
   for (const int tile : {256, 128, 64}) {
@@ -418,15 +439,16 @@ int ns_tile(const NsTable& tab, Product p, bool f32) {
 }
 
 // The first tiles of a product's launch; returns their number.
-int32_t product_tiles(NsTiles& tiles, const NsTable& tab, Product p, int tile) {
-  return fill_tiles(tiles, tab, [&](const NsShape& s, const NsMatrix&) {
+template <class Table>
+int32_t product_tiles(NsTiles& tiles, const Table& tab, Product p, int tile) {
+  return fill_tiles(tiles, tab, [&](const NsShape& s) {
     const int64_t tm = (s.m + tile - 1) / tile, tn = (s.n + tile - 1) / tile;
     return p == kStep ? tm * tn : tm * (tm + 1) / 2;
   });
 }
 
 template <class T, bool POLY>
-void launch_symmetric(const NsTable& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
+void launch_symmetric(const NsPlanes& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
                       float alpha, float beta, hipStream_t stream) {
   auto launch = [&](auto kernel, int threads) {
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, alpha, beta);
@@ -439,51 +461,75 @@ void launch_symmetric(const NsTable& tab, const NsTiles& tiles, int32_t n, int t
   else launch(k_ns_symmetric<T, 64, 2, 2, 3, POLY>, 256);
 }
 
-template <class T, class O, int LAST>
-void launch_step(const NsTable& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
+template <class T, class O, int LAST, class Table>
+void launch_step(const Table& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
                  float a_coef, float beta, const NsUpdate& up, hipStream_t stream) {
   auto launch = [&](auto kernel, int threads) {
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, a_coef, beta, up);
   };
   const bool deep = deep_launch(n);
-  if (tile == 256) launch(k_ns_step<T, O, 256, 2, 4, 2, LAST>, 512);
-  else if (tile == 128 && deep) launch(k_ns_step<T, O, 128, 2, 4, 4, LAST>, 512);
-  else if (tile == 128) launch(k_ns_step<T, O, 128, 2, 4, 2, LAST>, 512);
-  else if (deep) launch(k_ns_step<T, O, 64, 2, 2, 8, LAST>, 256);
-  else launch(k_ns_step<T, O, 64, 2, 2, 3, LAST>, 256);
+  if (tile == 256) launch(k_ns_step<T, O, 256, 2, 4, 2, LAST, Table>, 512);
+  else if (tile == 128 && deep) launch(k_ns_step<T, O, 128, 2, 4, 4, LAST, Table>, 512);
+  else if (tile == 128) launch(k_ns_step<T, O, 128, 2, 4, 2, LAST, Table>, 512);
+  else if (deep) launch(k_ns_step<T, O, 64, 2, 2, 8, LAST, Table>, 256);
+  else launch(k_ns_step<T, O, 64, 2, 2, 3, LAST, Table>, 256);
 }
 
+// One chunk: `mats` in the order of their sums' lengths.
 template <class T, class G, class O, bool MOM>
-void ns_chunk(const NsTable& tab, const NsLaunch& a, const NsScales& sc, const NsUpdate& up, double* parts,
-              T* planes, hipStream_t stream) {
-  NsTiles tiles;
-  int32_t n = fill_tiles(tiles, tab, [](const NsShape&, const NsMatrix& x) { return norm_parts(x.rows, x.cols); });
-  k_ns_norm<G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts);
-  n = fill_tiles(tiles, tab, [](const NsShape&, const NsMatrix& x) {
-    return (int64_t)((x.rows + 63) / 64) * ((x.cols + 63) / 64);
+void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsScales& sc, const NsUpdate& up,
+              double* parts, T* planes, hipStream_t stream) {
+  // f(table of up to kNsPart matrices) over the chunk
+  auto by_part = [&](auto f) {
+    for (int32_t first = 0; first < count; first += kNsPart) {
+      NsTable tab;
+      tab.first = first;
+      tab.count = std::min(kNsPart, count - first);
+      std::copy(mats + first, mats + first + tab.count, tab.m);
+      f(tab);
+    }
+  };
+  by_part([&](const NsTable& tab) {
+    NsTiles tiles;
+    int32_t n = 0;
+    for (int32_t k = 0; k < tab.count; n += norm_parts(tab.m[k].rows, tab.m[k].cols), ++k) tiles.begin[k] = n;
+    for (int32_t k = tab.count; k <= kNsChunk; ++k) tiles.begin[k] = n;
+    k_ns_norm<G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts);
   });
-  k_ns_load<T, G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts, a.eps, sc.x, planes);
+  by_part([&](const NsTable& tab) {
+    NsTiles tiles;
+    const int32_t n = fill_tiles(tiles, tab, [](const NsShape& s) { return ((s.m + 63) / 64) * ((s.n + 63) / 64); });
+    k_ns_load<T, G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts, a.eps, sc.x, planes);
+  });
+  NsPlanes all;
+  all.count = count;
+  for (int32_t k = 0; k < count; ++k) all.m[k] = {mats[k].base, mats[k].rows, mats[k].cols};
   constexpr bool f32 = sizeof(T) == 4;
-  const int gram_tile = ns_tile(tab, kGram, f32), poly_tile = ns_tile(tab, kPoly, f32),
-            step_tile = ns_tile(tab, kStep, f32);
-  // The last step of an update also reads and writes fp32 weights: two
-  // 128 tiles in a compute unit overlap that with products (4096 x 1024 and
-  // 1024 x 1024 matrices: 295 us against 356 us of one 256 tile).
+  const int gram_tile = ns_tile(all, kGram, f32), poly_tile = ns_tile(all, kPoly, f32),
+            step_tile = ns_tile(all, kStep, f32);
+  // The last step of an update also reads and writes the weights: two 128
+  // tiles in a compute unit overlap that with products (40 matrices of 1024 x
+  // 1024 and 4096 x 1024, fp32 weights: 295 us against 356 us of one 256 tile).
   const int last_tile = MOM && step_tile == 256 ? 128 : step_tile;
-  NsTiles gram, poly, step, last;
-  const int32_t n_gram = product_tiles(gram, tab, kGram, gram_tile), n_poly = product_tiles(poly, tab, kPoly, poly_tile),
-                n_step = product_tiles(step, tab, kStep, step_tile), n_last = product_tiles(last, tab, kStep, last_tile);
+  NsTiles gram, poly, step;
+  const int32_t n_gram = product_tiles(gram, all, kGram, gram_tile), n_poly = product_tiles(poly, all, kPoly, poly_tile),
+                n_step = product_tiles(step, all, kStep, step_tile);
   for (int32_t k = 0; k < a.steps; ++k) {
     const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
     const int32_t next = k & 1;
-    launch_symmetric<T, false>(tab, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
-    launch_symmetric<T, true>(tab, poly, n_poly, poly_tile, planes, next, cc * (sc.b[k] / (sc.a * sc.a)),
+    launch_symmetric<T, false>(all, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
+    launch_symmetric<T, true>(all, poly, n_poly, poly_tile, planes, next, cc * (sc.b[k] / (sc.a * sc.a)),
                               cb * (sc.b[k] / sc.a), stream);
-    if (k + 1 < a.steps)
-      launch_step<T, O, kNsNext>(tab, step, n_step, step_tile, planes, next, ca, 1.f / sc.b[k], up, stream);
-    else
-      launch_step<T, O, MOM ? kNsWeight : kNsOut>(tab, last, n_last, last_tile, planes, next, ca / sc.x,
-                                                  1.f / (sc.b[k] * sc.x), up, stream);
+    if (k + 1 < a.steps) {
+      launch_step<T, O, kNsNext>(all, step, n_step, step_tile, planes, next, ca, 1.f / sc.b[k], up, stream);
+    } else {
+      by_part([&](const NsTable& tab) {
+        NsTiles last;
+        const int32_t n = product_tiles(last, tab, kStep, last_tile);
+        launch_step<T, O, MOM ? kNsWeight : kNsOut>(tab, last, n, last_tile, planes, next, ca / sc.x,
+                                                    1.f / (sc.b[k] * sc.x), up, stream);
+      });
+    }
   }
 }
 
@@ -495,21 +541,19 @@ hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
   const NsUpdate up{a.mu, a.lr * a.weight_decay, a.nesterov, a.lr_scale};
   for (int32_t first = 0, last; first < a.num; first = last) {
     last = chunk_end(a.mats, a.num, first);
-    NsTable tab;
-    tab.count = last - first;
+    NsMatrix mats[kNsChunk];
     int64_t base = 0;
     for (int32_t k = first; k < last; ++k) {
       const dc_matrix& d = a.mats[k];
-      const NsShape sh(d.rows, d.cols);
-      tab.m[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
-                                  a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
-      base += sh.values();
+      mats[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
+                                 a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
+      base += NsShape(d.rows, d.cols).values();
     }
     // the longest sums first, so that short ones fill what they leave
-    std::sort(tab.m, tab.m + tab.count, [](const NsMatrix& x, const NsMatrix& y) {
+    std::sort(mats, mats + (last - first), [](const NsMatrix& x, const NsMatrix& y) {
       return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
     });
-    ns_chunk<T, G, O, MOM>(tab, a, sc, up, parts, planes, stream);
+    ns_chunk<T, G, O, MOM>(mats, last - first, a, sc, up, parts, planes, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

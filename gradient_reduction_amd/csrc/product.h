@@ -427,12 +427,12 @@ constexpr int64_t kComputeUnits = 256;
 inline bool deep_launch(int64_t tiles) { return tiles <= kComputeUnits; }
 
 // Microseconds that a compute unit takes for a stage of a tile, as measured
-// with the unit busy (one 256 tile, two of 128, three of 64 resident) and, the
-// same, with one 128 or 64 tile alone: 2 tile^2 64 operations at 1.26, 1.0 and
-// 0.7 PFLOP/s over the chip; fp32 is held by the matrix cores' fp32 rate.
+// with the unit busy (one 256 tile, two of 128, three of 64 resident): 2
+// tile^2 64 operations at 1.26, 1.0 and 0.55 PFLOP/s over the chip; fp32 is
+// held by the matrix cores' fp32 rate.
 inline double stage_us(bool f32, int tile) {
   if (f32) return tile == 256 ? 6.9 : tile == 128 ? 1.75 : 0.45;
-  return tile == 256 ? 1.65 : tile == 128 ? 0.54 : 0.19;
+  return tile == 256 ? 1.65 : tile == 128 ? 0.54 : 0.25;
 }
 
 // Workgroup b of n, with the workgroups of one XCD (b mod 8) on one run of
