@@ -222,10 +222,13 @@ hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, in
 
 // A few rows (a single token's, or a decoding batch's): x wT with w streamed
 // once from memory straight into the matrix cores' layout, no LDS between.  A
-// workgroup takes 16 NI outputs and its eight waves a share of k each, so that
-// w's rows are read by enough waves to keep the memory busy; their sums are
-// added in the waves' order.  Bound by w's bytes.
-template <class T, int TI, int NI, class Epi>
+// workgroup takes 16 NI outputs and its eight waves k's groups in turn, so that
+// enough loads are in flight and what is being read of a row is one run; their
+// sums are added in the waves' order.  Bound by w's bytes and, from about eight
+// rows on, by what a compute unit can fetch, which x shares: 16 x 4096 x 11008
+// bf16 takes 22 us, 17 with x left out, and more loads in flight, 16 waves or
+// 32 outputs a workgroup take 24, 24 and 33.
+template <class T, int TI, int NI, bool DIRECT, class Epi>
 __global__ void __launch_bounds__(512) k_linear_few(const T* x, int64_t ld_x, const T* w, int64_t ld_w, int32_t rows,
                                                     int64_t n, int64_t k, Epi epi) {
   constexpr int EPC = 16 / sizeof(T), kSlice = 4 * EPC, kWaves = 8, U = 4;
@@ -233,40 +236,62 @@ __global__ void __launch_bounds__(512) k_linear_few(const T* x, int64_t ld_x, co
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
   const int64_t j0 = (int64_t)blockIdx.x * (16 * NI);
-  // whole groups of U slices per wave, so that a group's loads are in flight
-  // together
-  const int64_t groups = (k + kSlice * U - 1) / (kSlice * U), share = (groups + kWaves - 1) / kWaves;
-  const int64_t k0 = wave * share * (kSlice * U), k1 = k0 + share * (kSlice * U) < k ? k0 + share * (kSlice * U) : k;
+  // Groups of U slices go to the waves in turn, so that a row's part that is
+  // being read is one long run of memory.
   f32x4 acc[TI][NI] = {};
-  auto chunk = [&](const T* row, bool there, int64_t at) {
+  // Whole aligned chunks come through buffer resources, where one that is
+  // outside has its offset outside and is zero: no branch between the loads.
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<T*>(w + j0 * ld_w), (short)0, (int)0x80000000u, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rx =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(x), (short)0, (int)0x80000000u, kBufferFlags);
+  auto chunk = [&](const __amdgpu_buffer_rsrc_t& rsrc, const T* base, int64_t ld, int row, bool there, int64_t at) {
     u32x4 v = {0, 0, 0, 0};
-    const int64_t left = there ? k1 - at : 0;
-    if (left >= EPC) {
-      __builtin_memcpy(&v, row + at, 16);
-    } else if (left > 0) {
-      T e[EPC];
+    if constexpr (DIRECT) {
+      const uint32_t off = (uint32_t)(row * (int)ld + (int)at) * (uint32_t)sizeof(T);
+      v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, there && at < k ? (int)off : (int)0x80000000u, 0, 0);
+    } else {
+      const int64_t left = there ? k - at : 0;
+      const T* p = base + row * ld + at;
+      if (left >= EPC) {
+        __builtin_memcpy(&v, p, 16);
+      } else if (left > 0) {
+        T e[EPC];
 #pragma unroll
-      for (int t = 0; t < EPC; ++t) e[t] = t < left ? row[at + t] : (T)0;
-      __builtin_memcpy(&v, e, 16);
+        for (int t = 0; t < EPC; ++t) e[t] = t < left ? p[t] : (T)0;
+        __builtin_memcpy(&v, e, 16);
+      }
     }
     return v;
   };
-  for (int64_t at = k0 + q * EPC; at < k1 + q * EPC; at += kSlice * U) {
-    u32x4 fw[U][NI], fx[U][TI];
+  // The next group is on its way while one is multiplied.
+  u32x4 fw[2][U][NI], fx[2][U][TI];
+  auto load = [&](int to, int64_t at) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int b = 0; b < NI; ++b)
-        fw[u][b] = chunk(w + (j0 + b * 16 + r) * ld_w, j0 + b * 16 + r < n, at + u * kSlice);
+        fw[to][u][b] = chunk(rw, w + j0 * ld_w, ld_w, b * 16 + r, j0 + b * 16 + r < n, at + u * kSlice);
 #pragma unroll
-      for (int a = 0; a < TI; ++a) fx[u][a] = chunk(x + (a * 16 + r) * ld_x, a * 16 + r < rows, at + u * kSlice);
+      for (int a = 0; a < TI; ++a) fx[to][u][a] = chunk(rx, x, ld_x, a * 16 + r, a * 16 + r < rows, at + u * kSlice);
     }
+  };
+  auto multiply = [&](int from) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int a = 0; a < TI; ++a)
 #pragma unroll
-        for (int b = 0; b < NI; ++b) acc[a][b] = mma_slice(fw[u][b], fx[u][a], acc[a][b], T{});
+        for (int b = 0; b < NI; ++b) acc[a][b] = mma_slice(fw[from][u][b], fx[from][u][a], acc[a][b], T{});
+  };
+  constexpr int64_t kGroup = kSlice * U, kTurn = kGroup * kWaves;
+  const int64_t k0 = wave * kGroup;
+  if (k0 < k) load(0, k0 + q * EPC);
+  for (int64_t at = k0; at < k; at += 2 * kTurn) {
+    load(1, at + kTurn + q * EPC);  // past the end: zeros, nothing read
+    multiply(0);
+    load(0, at + 2 * kTurn + q * EPC);
+    multiply(1);
   }
 #pragma unroll
   for (int a = 0; a < TI; ++a)
@@ -285,66 +310,73 @@ __global__ void __launch_bounds__(512) k_linear_few(const T* x, int64_t ld_x, co
 
 constexpr int64_t kFewRows = 64;
 
-template <class T, class Epi>
+template <class T, bool DIRECT, class Epi>
 hipError_t few_rows(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int64_t rows, int64_t n, int64_t k,
                     const Epi& epi, hipStream_t stream) {
   auto launch = [&](auto kernel, int per) {
     kernel<<<dim3((uint32_t)((n + per - 1) / per)), 512, 0, stream>>>(
         static_cast<const T*>(x), ld_x, static_cast<const T*>(w), ld_w, (int32_t)rows, n, k, epi);
   };
-  if (rows <= 16) launch(k_linear_few<T, 1, 1, Epi>, 16);
-  else if (rows <= 32) launch(k_linear_few<T, 2, 1, Epi>, 16);
-  else launch(k_linear_few<T, 4, 2, Epi>, 32);
+  if (rows <= 16) launch(k_linear_few<T, 1, 1, DIRECT, Epi>, 16);
+  else if (rows <= 32) launch(k_linear_few<T, 2, 1, DIRECT, Epi>, 16);
+  else launch(k_linear_few<T, 4, 2, DIRECT, Epi>, 32);
   return hipGetLastError();
 }
 
+// A 16-byte access at any address of an element.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // dz = dy act'(pre) and the column sums of dz, in strips of `strip` rows: one
-// workgroup per 32 chunks of 16 bytes of columns and strip, eight rows at a
-// time.  The strips' sums go to partial[strip][n] and are added in order by
+// workgroup per 64 chunks of 16 bytes of columns and strip, a wave to a row
+// and two rows in flight per wave.  dy and pre are read past the caches, dz
+// is left in them for the products that read it next (8192 x 11008 bf16: 103
+// us so, 155 us with ordinary loads, 109 us with the stores past them too).
+// Bound by those bytes.  The strips' sums go to partial[strip][n] and are added in order by
 // k_column_join, or straight to db when there is one strip.
-template <class T, class G>
+template <class T, class G, int ACT>
 __global__ void __launch_bounds__(256) k_bias_act(int64_t rows, int64_t n, const T* dy, int64_t ld_dy, const T* pre,
-                                                  int64_t ld_pre, int act, T* dz, int64_t ld_dz, float* partial,
+                                                  int64_t ld_pre, T* dz, int64_t ld_dz, float* partial,
                                                   G* db, int accumulate, int64_t strip) {
   constexpr int V = 16 / sizeof(T);
-  __shared__ float sum[8][32][V + 1];
-  const int c = threadIdx.x & 31, l = threadIdx.x >> 5;
-  const int64_t j = ((int64_t)blockIdx.x * 32 + c) * V;
+  __shared__ float sum[4][64][V + 1];
+  const int c = threadIdx.x & 63, l = threadIdx.x >> 6;
+  const int64_t j = ((int64_t)blockIdx.x * 64 + c) * V;
   const int64_t i0 = (int64_t)blockIdx.y * strip, i1 = i0 + strip < rows ? i0 + strip : rows;
   const int64_t left = n - j;
   float s[V] = {};
   if (left > 0) {
     auto load = [&](const T* p, T* to) {
       if (left >= V) {
-        __builtin_memcpy(to, p, 16);
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+        __builtin_memcpy(to, &v, 16);
       } else {
 #pragma unroll
         for (int t = 0; t < V; ++t) to[t] = t < left ? p[t] : (T)0;
       }
     };
     // U rows' loads in flight at once
-    constexpr int U = 4;
-    for (int64_t i = i0 + l; i < i1; i += 8 * U) {
+    constexpr int U = 2;
+    for (int64_t i = i0 + l; i < i1; i += 4 * U) {
       T d[U][V], z[U][V];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + 8 * u < i1) {
-          load(dy + (i + 8 * u) * ld_dy + j, d[u]);
-          if (pre) load(pre + (i + 8 * u) * ld_pre + j, z[u]);
+        if (i + 4 * u < i1) {
+          load(dy + (i + 4 * u) * ld_dy + j, d[u]);
+          if constexpr (ACT != DC_ACT_NONE) load(pre + (i + 4 * u) * ld_pre + j, z[u]);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + 8 * u < i1) {
+        if (i + 4 * u < i1) {
           T o[V];
 #pragma unroll
           for (int t = 0; t < V; ++t) {
             float v = (float)d[u][t];
-            if (pre) v *= activation_slope((float)z[u][t], act);
+            if constexpr (ACT != DC_ACT_NONE) v *= activation_slope((float)z[u][t], ACT);
             s[t] += v;
             o[t] = (T)v;
           }
           if (dz) {
-            T* p = dz + (i + 8 * u) * ld_dz + j;
+            T* p = dz + (i + 4 * u) * ld_dz + j;
             if (left >= V) {
               __builtin_memcpy(p, o, 16);
             } else {
@@ -360,13 +392,13 @@ __global__ void __launch_bounds__(256) k_bias_act(int64_t rows, int64_t n, const
 #pragma unroll
   for (int t = 0; t < V; ++t) sum[l][c][t] = s[t];
   __syncthreads();
-  if (threadIdx.x < 32 * V) {
-    const int cc = threadIdx.x / V, t = threadIdx.x % V;
-    const int64_t jj = ((int64_t)blockIdx.x * 32 + cc) * V + t;
+  for (int at = threadIdx.x; at < 64 * V; at += 256) {
+    const int cc = at / V, t = at % V;
+    const int64_t jj = ((int64_t)blockIdx.x * 64 + cc) * V + t;
     if (jj < n) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) v += sum[w][cc][t];
+      for (int w = 0; w < 4; ++w) v += sum[w][cc][t];
       if (gridDim.y > 1) partial[(int64_t)blockIdx.y * n + jj] = v;
       else db[jj] = (G)(accumulate ? (float)db[jj] + v : v);
     }
@@ -394,7 +426,7 @@ __global__ void __launch_bounds__(256) k_column_join(const float* partial, int32
 
 // Rows per strip: about 2048 workgroups over the chip, at least 32 rows each.
 int64_t strip_rows(int32_t dtype, int64_t rows, int64_t n) {
-  const int64_t per = dtype == DC_F32 ? 128 : 256;
+  const int64_t per = dtype == DC_F32 ? 256 : 512;
   const int64_t across = (n + per - 1) / per;
   const int64_t strips = std::max<int64_t>(1, 2048 / across);
   const int64_t r = std::max<int64_t>(32, (rows + strips - 1) / strips);
@@ -407,11 +439,16 @@ hipError_t bias_act(int32_t dtype, int64_t rows, int64_t n, const void* dy, int6
                     hipStream_t stream) {
   const int64_t strip = strip_rows(dtype, rows, n);
   const int64_t strips = std::max<int64_t>(1, (rows + strip - 1) / strip);
-  constexpr int64_t per = 32 * (16 / sizeof(T));
+  constexpr int64_t per = 64 * (16 / sizeof(T));
   const dim3 grid((uint32_t)((n + per - 1) / per), (uint32_t)strips);
-  k_bias_act<T, G><<<grid, 256, 0, stream>>>(rows, n, static_cast<const T*>(dy), ld_dy, static_cast<const T*>(pre),
-                                             ld_pre, act, static_cast<T*>(dz), ld_dz, partial, static_cast<G*>(db),
-                                             accumulate, strip);
+  auto launch = [&](auto kernel) {
+    kernel<<<grid, 256, 0, stream>>>(rows, n, static_cast<const T*>(dy), ld_dy, static_cast<const T*>(pre), ld_pre,
+                                     static_cast<T*>(dz), ld_dz, partial, static_cast<G*>(db), accumulate, strip);
+  };
+  if (act == DC_ACT_RELU) launch(k_bias_act<T, G, DC_ACT_RELU>);
+  else if (act == DC_ACT_GELU) launch(k_bias_act<T, G, DC_ACT_GELU>);
+  else if (act == DC_ACT_SILU) launch(k_bias_act<T, G, DC_ACT_SILU>);
+  else launch(k_bias_act<T, G, DC_ACT_NONE>);
   if (db && strips > 1)
     k_column_join<G><<<dim3((uint32_t)((n + 31) / 32)), 256, 0, stream>>>(partial, (int32_t)strips, n,
                                                                          static_cast<G*>(db), accumulate);
@@ -438,8 +475,14 @@ hipError_t launch_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const v
                          int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   if (T <= kFewRows) {
-    if (dtype == DC_BF16) return few_rows<__bf16>(x, ld_x, w, ld_w, T, N, K, LinearEpilogue<__bf16>{o, N}, stream);
-    return few_rows<float>(x, ld_x, w, ld_w, T, N, K, LinearEpilogue<float>{o, N}, stream);
+    auto few = [&](auto type) {
+      using E = decltype(type);
+      const LinearEpilogue<E> epi{o, N};
+      return direct_operand<E>(x, ld_x, K) && direct_operand<E>(w, ld_w, K)
+                 ? few_rows<E, true>(x, ld_x, w, ld_w, T, N, K, epi, stream)
+                 : few_rows<E, false>(x, ld_x, w, ld_w, T, N, K, epi, stream);
+    };
+    return dtype == DC_BF16 ? few(__bf16{}) : few(float{});
   }
   float* ws = static_cast<float*>(workspace);
   if (dtype == DC_BF16)
