@@ -23,8 +23,15 @@ constexpr int kNsPart = 48;           // of them whose addresses fit one launch'
 constexpr int kNormParts = 256;       // partial sums of squares per matrix, at most
 constexpr int64_t kNormSpan = 16384;  // elements per partial sum, at least
 
+// What X, A and B are held in.  One fp16 (11 bits) for bf16 gradients; two for
+// fp32 ones, a value and what it leaves (22 bits), multiplied as high high +
+// high low + low high: three products of 16 bits take a fifth of one product
+// of fp32 on these matrix cores.
+using Held = _Float16;
+
 // One matrix of a chunk.  Its planes in the workspace, in values from the
-// planes' base: X [m][ldx], the next X [m][ldx], A [m][lda], B [m][lda].
+// planes' base: X [m][ldx], the next X [m][ldx], A [m][lda], B [m][lda]; with
+// two values each is a pair of planes.
 struct NsMatrix {
   const void* grad;
   void* out;
@@ -74,7 +81,7 @@ struct NsShape {
     x_size = up128(m * ldx);
     a_size = up128(m * lda);
   }
-  __host__ __device__ int64_t values() const { return 2 * (x_size + a_size); }
+  __host__ __device__ int64_t values(int pair) const { return 2 * pair * (x_size + a_size); }
 };
 
 __host__ __device__ inline int32_t norm_parts(int64_t rows, int64_t cols) {
@@ -148,11 +155,30 @@ __global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsU
   if (threadIdx.x == 0) parts[(int64_t)(tab.first + e) * kNormParts + part] = sum[0] + sum[1] + sum[2] + sum[3];
 }
 
+// Eight (or four) held values at `at` of a plane; the second plane of a pair
+// lies `size` values on.
+template <int P, int N>
+__device__ __forceinline__ auto load_held(const Held* p, int64_t at, int64_t size) {
+  auto v = load_n<N>(p + at, N);
+  if constexpr (P == 2) v += load_n<N>(p + size + at, N);
+  return v;
+}
+
+template <int P, int N, class V>
+__device__ __forceinline__ void store_held(Held* p, int64_t at, int64_t size, V v) {
+  store_n<N>(p + at, v, N);
+  if constexpr (P == 2) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) v[t] -= (float)(Held)v[t];
+    store_n<N>(p + size + at, v, N);
+  }
+}
+
 // X = U scale / (|U|_F + eps), transposed where rows > cols, 64 x 64 at a
 // time; columns n .. ldx - 1 of X are zero.
-template <class T, class G, bool MOM>
+template <int P, class G, bool MOM>
 __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsUpdate up, const double* parts,
-                                                 float eps, float scale, T* planes) {
+                                                 float eps, float scale, Held* planes) {
   const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
   const NsMatrix& x = tab.m[e];
   const NsShape sh(x.rows, x.cols);
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
   const int64_t r0 = (int64_t)(t / across) * 64, c0 = (int64_t)(t % across) * 64;
   const G* grad = static_cast<const G*>(x.grad);
   const int c = (threadIdx.x & 15) * 4, l = threadIdx.x >> 4;
-  T* out = planes + x.base;
+  Held* out = planes + x.base;
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int rr = l + 16 * p;
@@ -192,7 +218,7 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
       for (int k = 0; k < 4; ++k) u[k] = (float)((double)u[k] * f);
     }
     if (!sh.flip) {
-      if (r < sh.m && col < sh.ldx) store_n<4>(out + r * sh.ldx + col, u, 4);
+      if (r < sh.m && col < sh.ldx) store_held<P, 4>(out, r * sh.ldx + col, sh.x_size, u);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) tile[rr][c + k] = u[k];
@@ -206,9 +232,25 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
       f32x4 u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) u[k] = tile[c + k][l + 16 * p];
-      if (i < sh.m && j < sh.ldx) store_n<4>(out + i * sh.ldx + j, u, 4);
+      if (i < sh.m && j < sh.ldx) store_held<P, 4>(out, i * sh.ldx + j, sh.x_size, u);
     }
   }
+}
+
+// The product of two operands that are pairs of planes, size_a and size_b
+// apart; the small products first.
+template <class Tile, int P, class Acc>
+__device__ __forceinline__ void held_product(Operand<Held> a, int64_t size_a, Operand<Held> b, int64_t size_b,
+                                             int64_t k, Acc& acc) {
+  if constexpr (P == 2) {
+    Operand<Held> low = b;
+    low.p += size_b;
+    Tile::run(a, low, 0, k, acc);
+    low = a;
+    low.p += size_a;
+    Tile::run(low, b, 0, k, acc);
+  }
+  Tile::run(a, b, 0, k, acc);
 }
 
 // Tile t of the upper triangle of an nt x nt grid, by rows.
@@ -224,64 +266,64 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
 
 // A = alpha X XT (POLY false: src = X, dst = A), or B = beta A + alpha A A
 // (POLY true: src = A, dst = B; A is its own transpose).
-template <class T, int BT, int WM, int WN, int S, bool POLY>
-__global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsTiles tiles, T* planes, int32_t next,
+template <int P, int BT, int WM, int WN, int S, bool POLY>
+__global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsTiles tiles, Held* planes, int32_t next,
                                                                float alpha, float beta) {
-  using P = TileProduct<T, BT, BT, WM, WN, true, true, S>;
+  using Tile = TileProduct<Held, BT, BT, WM, WN, true, true, S>;
   const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
   const int32_t t = matrix_tile(tiles, e);
   const NsShape sh(tab.m[e].rows, tab.m[e].cols);
-  T* x = planes + tab.m[e].base;
-  T* a_plane = x + 2 * sh.x_size;
-  const T* src = POLY ? a_plane : x + (next ? sh.x_size : 0);
-  T* dst = POLY ? a_plane + sh.a_size : a_plane;
-  const int64_t ld = POLY ? sh.lda : sh.ldx;
+  Held* x = planes + tab.m[e].base;
+  Held* a_plane = x + 2 * P * sh.x_size;
+  const Held* src = POLY ? a_plane : x + (next ? P * sh.x_size : 0);
+  Held* dst = POLY ? a_plane + P * sh.a_size : a_plane;
+  const int64_t ld = POLY ? sh.lda : sh.ldx, size = POLY ? sh.a_size : sh.x_size;
   int32_t ti, tj;
   triangle_tile(t, (int32_t)((sh.m + BT - 1) / BT), ti, tj);
   const int64_t i0 = (int64_t)ti * BT, j0 = (int64_t)tj * BT;
-  const Operand<T> a{src + i0 * ld, ld, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
-  const Operand<T> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
-  f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, 0, ld, acc);
+  const Operand<Held> a{src + i0 * ld, ld, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
+  const Operand<Held> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
+  f32x4 acc[Tile::MI][Tile::NI] = {};
+  held_product<Tile, P>(a, size, b, size, ld, acc);
   // Columns m .. lda - 1 get zeros.  The mirrored tile adds the same beta A,
   // read where it lies.
-  P::each(
+  Tile::each(
       acc, true, ti != tj,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j0 + j >= sh.lda) return;
         v *= alpha;
-        if constexpr (POLY) v += beta * load_n<8>(src + (i0 + i) * ld + j0 + j, 8);
-        store_n<8>(dst + (i0 + i) * sh.lda + j0 + j, v, 8);
+        if constexpr (POLY) v += beta * load_held<P, 8>(src, (i0 + i) * ld + j0 + j, size);
+        store_held<P, 8>(dst, (i0 + i) * sh.lda + j0 + j, sh.a_size, v);
       },
       [&](int j, int i, f32x8 v) {
         if (j >= b.rows || i >= a.rows) return;
         v *= alpha;
-        if constexpr (POLY) v += beta * load_n<8>(src + (j0 + j) * ld + i0 + i, 8);
-        store_n<8>(dst + (j0 + j) * sh.lda + i0 + i, v, 8);
+        if constexpr (POLY) v += beta * load_held<P, 8>(src, (j0 + j) * ld + i0 + i, size);
+        store_held<P, 8>(dst, (j0 + j) * sh.lda + i0 + i, sh.a_size, v);
       });
 }
 
 // X <- a X + beta B X into the other X plane, or out of it in the last step.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
-template <class T, class O, int BT, int WM, int WN, int S, int LAST, class Table>
-__global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles tiles, T* planes, int32_t next,
+template <int P, class O, int BT, int WM, int WN, int S, int LAST, class Table>
+__global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles tiles, Held* planes, int32_t next,
                                                           float a_coef, float beta, NsUpdate up) {
-  using P = TileProduct<T, BT, BT, WM, WN, true, false, S>;
+  using Tile = TileProduct<Held, BT, BT, WM, WN, true, false, S>;
   const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
   const int32_t t = matrix_tile(tiles, e);
   const auto& x = tab.m[e];
   const NsShape sh(x.rows, x.cols);
-  const T* src = planes + x.base + (next ? sh.x_size : 0);
-  T* dst = planes + x.base + (next ? 0 : sh.x_size);
-  const T* poly = planes + x.base + 2 * sh.x_size + sh.a_size;
+  const Held* src = planes + x.base + (next ? P * sh.x_size : 0);
+  Held* dst = planes + x.base + (next ? 0 : P * sh.x_size);
+  const Held* poly = planes + x.base + 2 * P * sh.x_size + P * sh.a_size;
   int64_t ti, tj;
   band_tile(t, (sh.m + BT - 1) / BT, (sh.n + BT - 1) / BT, 8, ti, tj);
   const int64_t i0 = ti * BT, j0 = tj * BT;
-  const Operand<T> a{poly + i0 * sh.lda, sh.lda, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
-  const Operand<T> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
-  f32x4 acc[P::MI][P::NI] = {};
-  P::run(a, b, 0, sh.m, acc);
+  const Operand<Held> a{poly + i0 * sh.lda, sh.lda, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
+  const Operand<Held> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
+  f32x4 acc[Tile::MI][Tile::NI] = {};
+  held_product<Tile, P>(a, sh.a_size, b, sh.x_size, sh.m, acc);
   O* out = nullptr;
   int64_t ld_out = 0;
   float scale = 1.f, keep = 1.f;
@@ -297,12 +339,13 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
     store_n<8>(p, v, n);
   };
   const bool flip = LAST != kNsNext && sh.flip;
-  P::each(
+  Tile::each(
       acc, !flip, flip,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j >= b.rows) return;
-        v = beta * v + a_coef * load_n<8>(src + (i0 + i) * sh.ldx + j0 + j, 8);
-        if constexpr (LAST == kNsNext) store_n<8>(dst + (i0 + i) * sh.ldx + j0 + j, v, 8);
+        const int64_t at = (i0 + i) * sh.ldx + j0 + j;
+        v = beta * v + a_coef * load_held<P, 8>(src, at, sh.x_size);
+        if constexpr (LAST == kNsNext) store_held<P, 8>(dst, at, sh.x_size, v);
         else write(out + (i0 + i) * ld_out + j0 + j, v, sh.n - (j0 + j));
       },
       [&](int j, int i, f32x8 v) {
@@ -310,7 +353,12 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
         const int64_t n = a.rows - i;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (k < n) v[k] = beta * v[k] + a_coef * (float)src[(i0 + i + k) * sh.ldx + j0 + j];
+          if (k < n) {
+            const int64_t at = (i0 + i + k) * sh.ldx + j0 + j;
+            float old = (float)src[at];
+            if constexpr (P == 2) old += (float)src[sh.x_size + at];
+            v[k] = beta * v[k] + a_coef * old;
+          }
         write(out + (j0 + j) * ld_out + i0 + i, v, n);
       });
 }
@@ -342,7 +390,7 @@ double step_top(const float* co, double top) {
 // its polynomial (with a thousandth for what is held having been rounded),
 // |A| by the square, |B| by |b| A + |c| A A.  In fp16 the bound is held at
 // 2^13 to 2^14, a quarter of the type's largest value; values down to 2^-27 of
-// it keep all 11 bits.  In fp32 nothing is scaled.
+// it keep all 11 bits.
 constexpr double kSlack = 1.001;
 
 struct NsScales {
@@ -350,10 +398,8 @@ struct NsScales {
   float b[DC_NS_MAX_STEPS];
 };
 
-NsScales ns_scales(int32_t dtype, int32_t steps, const float* coeffs) {
+NsScales ns_scales(int32_t steps, const float* coeffs) {
   NsScales s;
-  for (int k = 0; k < steps; ++k) s.b[k] = 1.f;
-  if (dtype == DC_F32) return s;
   double top[DC_NS_MAX_STEPS + 1], most = kSlack;
   top[0] = kSlack;
   for (int k = 0; k < steps; ++k) {
@@ -384,9 +430,9 @@ int32_t chunk_end(const dc_matrix* mats, int32_t n, int32_t first) {
   return k;
 }
 
-int64_t chunk_values(const dc_matrix* mats, int32_t first, int32_t last) {
+int64_t chunk_values(const dc_matrix* mats, int32_t first, int32_t last, int pair) {
   int64_t v = 0;
-  for (int32_t k = first; k < last; ++k) v += NsShape(mats[k].rows, mats[k].cols).values();
+  for (int32_t k = first; k < last; ++k) v += NsShape(mats[k].rows, mats[k].cols).values(pair);
   return v;
 }
 
@@ -411,7 +457,7 @@ enum Product : int { kGram, kPoly, kStep };
 // tile_us for a tile's beginning and end; tiles of one length run in whole
 // rounds, of several lengths in the longest one's time or everybody's share
 // and half a shortest one.
-int ns_tile(const NsPlanes& tab, Product p, bool f32) {
+int ns_tile(const NsPlanes& tab, Product p, int pair) {
   int best = 0;
   double least = 0;
   for (const int tile : {256, 128, 64}) {
@@ -420,8 +466,8 @@ int ns_tile(const NsPlanes& tab, Product p, bool f32) {
     for (int k = 0; k < tab.count; ++k) {
       const NsShape s(tab.m[k].rows, tab.m[k].cols);
       const double tm = (double)((s.m + tile - 1) / tile), tn = (double)((s.n + tile - 1) / tile);
-      const double stages = std::ceil((p == kGram ? s.ldx : s.lda) / (f32 ? 32.0 : 64.0));
-      const double us = stages * stage_us(f32, tile) + tile_us;
+      const double stages = std::ceil((p == kGram ? s.ldx : s.lda) / 64.0) * (pair == 2 ? 3 : 1);
+      const double us = stages * stage_us(false, tile) + tile_us;
       const double tiles = p == kStep ? tm * tn : tm * (tm + 1) / 2;
       total += tiles * us;
       count += tiles;
@@ -447,38 +493,38 @@ int32_t product_tiles(NsTiles& tiles, const Table& tab, Product p, int tile) {
   });
 }
 
-template <class T, bool POLY>
-void launch_symmetric(const NsPlanes& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
+template <int P, bool POLY>
+void launch_symmetric(const NsPlanes& tab, const NsTiles& tiles, int32_t n, int tile, Held* planes, int32_t next,
                       float alpha, float beta, hipStream_t stream) {
   auto launch = [&](auto kernel, int threads) {
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, alpha, beta);
   };
   const bool deep = deep_launch(n);
-  if (tile == 256) launch(k_ns_symmetric<T, 256, 2, 4, 2, POLY>, 512);
-  else if (tile == 128 && deep) launch(k_ns_symmetric<T, 128, 2, 4, 4, POLY>, 512);
-  else if (tile == 128) launch(k_ns_symmetric<T, 128, 2, 4, 2, POLY>, 512);
-  else if (deep) launch(k_ns_symmetric<T, 64, 2, 2, 8, POLY>, 256);
-  else launch(k_ns_symmetric<T, 64, 2, 2, 3, POLY>, 256);
+  if (tile == 256) launch(k_ns_symmetric<P, 256, 2, 4, 2, POLY>, 512);
+  else if (tile == 128 && deep) launch(k_ns_symmetric<P, 128, 2, 4, 4, POLY>, 512);
+  else if (tile == 128) launch(k_ns_symmetric<P, 128, 2, 4, 2, POLY>, 512);
+  else if (deep) launch(k_ns_symmetric<P, 64, 2, 2, 8, POLY>, 256);
+  else launch(k_ns_symmetric<P, 64, 2, 2, 3, POLY>, 256);
 }
 
-template <class T, class O, int LAST, class Table>
-void launch_step(const Table& tab, const NsTiles& tiles, int32_t n, int tile, T* planes, int32_t next,
+template <int P, class O, int LAST, class Table>
+void launch_step(const Table& tab, const NsTiles& tiles, int32_t n, int tile, Held* planes, int32_t next,
                  float a_coef, float beta, const NsUpdate& up, hipStream_t stream) {
   auto launch = [&](auto kernel, int threads) {
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, a_coef, beta, up);
   };
   const bool deep = deep_launch(n);
-  if (tile == 256) launch(k_ns_step<T, O, 256, 2, 4, 2, LAST, Table>, 512);
-  else if (tile == 128 && deep) launch(k_ns_step<T, O, 128, 2, 4, 4, LAST, Table>, 512);
-  else if (tile == 128) launch(k_ns_step<T, O, 128, 2, 4, 2, LAST, Table>, 512);
-  else if (deep) launch(k_ns_step<T, O, 64, 2, 2, 8, LAST, Table>, 256);
-  else launch(k_ns_step<T, O, 64, 2, 2, 3, LAST, Table>, 256);
+  if (tile == 256) launch(k_ns_step<P, O, 256, 2, 4, 2, LAST, Table>, 512);
+  else if (tile == 128 && deep) launch(k_ns_step<P, O, 128, 2, 4, 4, LAST, Table>, 512);
+  else if (tile == 128) launch(k_ns_step<P, O, 128, 2, 4, 2, LAST, Table>, 512);
+  else if (deep) launch(k_ns_step<P, O, 64, 2, 2, 8, LAST, Table>, 256);
+  else launch(k_ns_step<P, O, 64, 2, 2, 3, LAST, Table>, 256);
 }
 
 // One chunk: `mats` in the order of their sums' lengths.
-template <class T, class G, class O, bool MOM>
+template <int P, class G, class O, bool MOM>
 void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsScales& sc, const NsUpdate& up,
-              double* parts, T* planes, hipStream_t stream) {
+              double* parts, Held* planes, hipStream_t stream) {
   // f(table of up to kNsPart matrices) over the chunk
   auto by_part = [&](auto f) {
     for (int32_t first = 0; first < count; first += kNsPart) {
@@ -499,14 +545,12 @@ void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsSc
   by_part([&](const NsTable& tab) {
     NsTiles tiles;
     const int32_t n = fill_tiles(tiles, tab, [](const NsShape& s) { return ((s.m + 63) / 64) * ((s.n + 63) / 64); });
-    k_ns_load<T, G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts, a.eps, sc.x, planes);
+    k_ns_load<P, G, MOM><<<n, 256, 0, stream>>>(tab, tiles, up, parts, a.eps, sc.x, planes);
   });
   NsPlanes all;
   all.count = count;
   for (int32_t k = 0; k < count; ++k) all.m[k] = {mats[k].base, mats[k].rows, mats[k].cols};
-  constexpr bool f32 = sizeof(T) == 4;
-  const int gram_tile = ns_tile(all, kGram, f32), poly_tile = ns_tile(all, kPoly, f32),
-            step_tile = ns_tile(all, kStep, f32);
+  const int gram_tile = ns_tile(all, kGram, P), poly_tile = ns_tile(all, kPoly, P), step_tile = ns_tile(all, kStep, P);
   // The last step of an update also reads and writes the weights: two 128
   // tiles in a compute unit overlap that with products (40 matrices of 1024 x
   // 1024 and 4096 x 1024, fp32 weights: 295 us against 356 us of one 256 tile).
@@ -517,27 +561,27 @@ void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsSc
   for (int32_t k = 0; k < a.steps; ++k) {
     const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
     const int32_t next = k & 1;
-    launch_symmetric<T, false>(all, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
-    launch_symmetric<T, true>(all, poly, n_poly, poly_tile, planes, next, cc * (sc.b[k] / (sc.a * sc.a)),
+    launch_symmetric<P, false>(all, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
+    launch_symmetric<P, true>(all, poly, n_poly, poly_tile, planes, next, cc * (sc.b[k] / (sc.a * sc.a)),
                               cb * (sc.b[k] / sc.a), stream);
     if (k + 1 < a.steps) {
-      launch_step<T, O, kNsNext>(all, step, n_step, step_tile, planes, next, ca, 1.f / sc.b[k], up, stream);
+      launch_step<P, O, kNsNext>(all, step, n_step, step_tile, planes, next, ca, 1.f / sc.b[k], up, stream);
     } else {
       by_part([&](const NsTable& tab) {
         NsTiles last;
         const int32_t n = product_tiles(last, tab, kStep, last_tile);
-        launch_step<T, O, MOM ? kNsWeight : kNsOut>(tab, last, n, last_tile, planes, next, ca / sc.x,
+        launch_step<P, O, MOM ? kNsWeight : kNsOut>(tab, last, n, last_tile, planes, next, ca / sc.x,
                                                     1.f / (sc.b[k] * sc.x), up, stream);
       });
     }
   }
 }
 
-template <class T, class G, class O, bool MOM>
+template <int P, class G, class O, bool MOM>
 hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
-  const NsScales sc = ns_scales(a.dtype, a.steps, a.coeffs);
+  const NsScales sc = ns_scales(a.steps, a.coeffs);
   double* parts = static_cast<double*>(a.workspace);
-  T* planes = reinterpret_cast<T*>(static_cast<char*>(a.workspace) + kPartsBytes);
+  Held* planes = reinterpret_cast<Held*>(static_cast<char*>(a.workspace) + kPartsBytes);
   const NsUpdate up{a.mu, a.lr * a.weight_decay, a.nesterov, a.lr_scale};
   for (int32_t first = 0, last; first < a.num; first = last) {
     last = chunk_end(a.mats, a.num, first);
@@ -547,13 +591,13 @@ hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
       const dc_matrix& d = a.mats[k];
       mats[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
                                  a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
-      base += NsShape(d.rows, d.cols).values();
+      base += NsShape(d.rows, d.cols).values(P);
     }
     // the longest sums first, so that short ones fill what they leave
     std::sort(mats, mats + (last - first), [](const NsMatrix& x, const NsMatrix& y) {
       return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
     });
-    ns_chunk<T, G, O, MOM>(mats, last - first, a, sc, up, parts, planes, stream);
+    ns_chunk<P, G, O, MOM>(mats, last - first, a, sc, up, parts, planes, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -578,23 +622,23 @@ int64_t ns_workspace(int32_t dtype, const dc_matrix* mats, int32_t num) {
   int64_t most = 0;
   for (int32_t first = 0, last; first < num; first = last) {
     last = chunk_end(mats, num, first);
-    most = std::max(most, chunk_values(mats, first, last));
+    most = std::max(most, chunk_values(mats, first, last, dtype == DC_F32 ? 2 : 1));
   }
-  return num ? kPartsBytes + most * (dtype == DC_F32 ? 4 : 2) : 0;
+  return num ? kPartsBytes + most * (int64_t)sizeof(Held) : 0;
 }
 
 hipError_t launch_ns(const NsLaunch& a, hipStream_t stream) {
   if (a.num == 0) return hipSuccess;
   if (!a.update) {
-    if (a.dtype == DC_F32) return ns_run<float, float, float, false>(a, stream);
-    return ns_run<_Float16, __bf16, __bf16, false>(a, stream);
+    if (a.dtype == DC_F32) return ns_run<2, float, float, false>(a, stream);
+    return ns_run<1, __bf16, __bf16, false>(a, stream);
   }
   if (a.dtype == DC_F32) {
-    if (a.out_dtype == DC_F32) return ns_run<float, float, float, true>(a, stream);
-    return ns_run<float, float, __bf16, true>(a, stream);
+    if (a.out_dtype == DC_F32) return ns_run<2, float, float, true>(a, stream);
+    return ns_run<2, float, __bf16, true>(a, stream);
   }
-  if (a.out_dtype == DC_F32) return ns_run<_Float16, __bf16, float, true>(a, stream);
-  return ns_run<_Float16, __bf16, __bf16, true>(a, stream);
+  if (a.out_dtype == DC_F32) return ns_run<1, __bf16, float, true>(a, stream);
+  return ns_run<1, __bf16, __bf16, true>(a, stream);
 }
 
 }  // namespace dc

@@ -262,6 +262,7 @@ struct TileProduct {
     const uint32_t base_a = MapA::lane_base((wave / WN) * (BM / WM), q, r);
     const uint32_t base_b = MapB::lane_base((wave % WN) * (BN / WN), q, r);
     if constexpr (kDirect) {
+      __syncthreads();  // a product before this one is done with the stages
       DirectLoader<T, BM, KCA, NT> da;
       DirectLoader<T, BN, KCB, NT> db;
       const int rest = (int)((k_end - k0) % BK);
@@ -299,22 +300,32 @@ struct TileProduct {
             std::make_integer_sequence<int, S>{});
       __builtin_amdgcn_s_waitcnt(0x0f70);  // nothing arrives any more
     } else {
-      RegisterLoader<T, BM, KCA, NT> ra;
-      RegisterLoader<T, BN, KCB, NT> rb;
+      // kAhead stages are on their way into registers: with one, a stage of a
+      // 64 tile took 1.4 us, most of it waiting.
+      constexpr int kAhead = BM <= 64 ? 4 : BM <= 128 ? 2 : 1;
+      RegisterLoader<T, BM, KCA, NT> ra[kAhead];
+      RegisterLoader<T, BN, KCB, NT> rb[kAhead];
       char* lds = memory<0>();
-      ra.load(a, k0, k_end, tid);
-      rb.load(b, k0, k_end, tid);
-      for (; k0 < k_end; k0 += BK) {
-        __syncthreads();  // every wave is done with the stage in LDS
-        ra.store(lds, tid);
-        rb.store(lds + MapA::kBytes, tid);
-        __syncthreads();
-        if (k0 + BK < k_end) {
-          ra.load(a, k0 + BK, k_end, tid);
-          rb.load(b, k0 + BK, k_end, tid);
-        }
+      const LdsPtr la = (LdsPtr)lds;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) slice((LdsPtr)lds, (LdsPtr)lds + MapA::kBytes, ks, base_a, base_b, acc);
+      for (int i = 0; i < kAhead; ++i) {  // past the end: zeros, nothing read
+        ra[i].load(a, k0 + i * BK, k_end, tid);
+        rb[i].load(b, k0 + i * BK, k_end, tid);
+      }
+      while (k0 < k_end) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (i > 0 && k0 >= k_end) break;
+          __syncthreads();  // every wave is done with the stage in LDS
+          ra[i].store(lds, tid);
+          rb[i].store(lds + MapA::kBytes, tid);
+          __syncthreads();
+          ra[i].load(a, k0 + kAhead * BK, k_end, tid);
+          rb[i].load(b, k0 + kAhead * BK, k_end, tid);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) slice(la, la + MapA::kBytes, ks, base_a, base_b, acc);
+          k0 += BK;
+        }
       }
     }
   }

@@ -883,10 +883,10 @@ dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32
  *   for every step (a, b, c):  A = X XT,  X <- a X + (b A + c A A) X
  * and X (transposed back) is written to out: the singular vectors stay, the
  * singular values go through the odd polynomials a s + b s^3 + c s^5.
- * DC_F32 computes in fp32.  DC_BF16 holds X, A and B in fp16 (11 bits, by
- * powers of two that the polynomials' bounds keep from overflowing) with
- * fp32 sums: about 1.5e-3 of |out|_F before the rounding to bf16.  |X|_F is
- * summed in fp64.  A zero matrix gives zero (NaN when eps is 0); a NaN or
+ * X, A and B are held in fp16, by powers of two that the polynomials' bounds
+ * keep from overflowing, with fp32 sums: for DC_BF16 one fp16 (11 bits),
+ * about 1.5e-3 of |out|_F before the rounding to bf16; for DC_F32 a pair (22
+ * bits), about 5e-7.  |X|_F is summed in fp64.  A zero matrix gives zero (NaN when eps is 0); a NaN or
  * infinity anywhere gives NaN in the whole of its matrix and no other.
  *   mats, num       host dc_matrix[num], num <= 2^20; out has the dtype of the gradients
  *                   and may be the gradient itself (same ld), otherwise
