@@ -170,17 +170,24 @@ struct Cut {
 };
 
 Cut cut(int32_t dtype, int64_t m, int64_t n, int64_t k) {
-  const int64_t bk = dtype == DC_F32 ? 32 : 64;
+  const bool f32 = dtype == DC_F32;
+  const int64_t bk = f32 ? 32 : 64;
+  // A stage alone in its compute unit takes `alone` at least (its loads'
+  // latency; fp32's matrix instructions hide less of it), and `held`
+  // workgroups of a tile share a unit.
+  const double alone = f32 ? 0.6 : 0.4;
   const int64_t stages = std::max<int64_t>(1, (k + bk - 1) / bk);
   Cut best{};
   double least = 0;
   for (const int32_t tile : {256, 128, 64}) {
+    const double held = tile == 256 ? 1 : tile == 128 ? 2 : 3, busy = stage_us(f32, tile);
     const int64_t tiles = std::max<int64_t>(1, ((m + tile - 1) / tile) * ((n + tile - 1) / tile));
     for (int64_t want = 1; want <= 64; ++want) {
       if (want > 1 && (want > stages / 4 || tiles * want > 4 * kComputeUnits)) break;
       const int64_t per = (stages + want - 1) / want, splits = (stages + per - 1) / per;
-      const int64_t rounds = (tiles * splits + kComputeUnits - 1) / kComputeUnits;
-      double us = rounds * per * stage_us(dtype == DC_F32, tile);
+      const double a_unit = (double)((tiles * splits + kComputeUnits - 1) / kComputeUnits);
+      const double full = std::floor(a_unit / held), rest = a_unit - full * held;
+      double us = per * (full * std::max(alone, held * busy) + (rest > 0 ? std::max(alone, rest * busy) : 0.0));
       // the sums written and read again, and a launch more
       if (splits > 1) us += 3.0 + splits * m * n * 8.0 / 4e6;
       if (best.tile == 0 || us < least) {
