@@ -140,9 +140,10 @@ __global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi
   P::each(
       acc, true, false,
       [&](int i, int j, f32x8 v) {
-        if (i >= a.rows || j >= b.rows) return;
+        if (i >= a.rows || j >= b.rows) return v;
         if (part) store_n<8>(part + (i0 + i) * g.ld_partial + j0 + j, v, 8);
         else epi(i0 + i, j0 + j, v);
+        return v;
       },
       [](int, int, f32x8) {});
 }
@@ -214,7 +215,7 @@ hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, in
                       c.k_per_split, partial, c.ld_partial};
   const bool direct = direct_operand<T>(a, ld_a, KCA ? k : m) && direct_operand<T>(b, ld_b, KCB ? k : n);
   const bool deep = deep_launch(g.tiles_m * g.tiles_n * g.splits);
-  if (c.tile == 256) launch_product<T, 256, 2, 4, 2, KCA, KCB>(g, direct, epi, stream);
+  if (c.tile == 256) launch_product<T, 256, 4, 2, 2, KCA, KCB>(g, direct, epi, stream);
   else if (c.tile == 128 && deep) launch_product<T, 128, 2, 4, 4, KCA, KCB>(g, direct, epi, stream);
   else if (c.tile == 128) launch_product<T, 128, 2, 4, 2, KCA, KCB>(g, direct, epi, stream);
   else if (deep) launch_product<T, 64, 2, 2, 8, KCA, KCB>(g, direct, epi, stream);

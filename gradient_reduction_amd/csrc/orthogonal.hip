@@ -285,21 +285,18 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
   const Operand<Held> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
   f32x4 acc[Tile::MI][Tile::NI] = {};
   held_product<Tile, P>(a, size, b, size, ld, acc);
-  // Columns m .. lda - 1 get zeros.  The mirrored tile adds the same beta A,
-  // read where it lies.
+  // Columns m .. lda - 1 get zeros; the mirrored tile gets the same values.
   Tile::each(
       acc, true, ti != tj,
       [&](int i, int j, f32x8 v) {
-        if (i >= a.rows || j0 + j >= sh.lda) return;
+        if (i >= a.rows || j0 + j >= sh.lda) return v;
         v *= alpha;
         if constexpr (POLY) v += beta * load_held<P, 8>(src, (i0 + i) * ld + j0 + j, size);
         store_held<P, 8>(dst, (i0 + i) * sh.lda + j0 + j, sh.a_size, v);
+        return v;
       },
       [&](int j, int i, f32x8 v) {
-        if (j >= b.rows || i >= a.rows) return;
-        v *= alpha;
-        if constexpr (POLY) v += beta * load_held<P, 8>(src, (j0 + j) * ld + i0 + i, size);
-        store_held<P, 8>(dst, (j0 + j) * sh.lda + i0 + i, sh.a_size, v);
+        if (j < b.rows && i < a.rows) store_held<P, 8>(dst, (j0 + j) * sh.lda + i0 + i, sh.a_size, v);
       });
 }
 
@@ -342,11 +339,12 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
   Tile::each(
       acc, !flip, flip,
       [&](int i, int j, f32x8 v) {
-        if (i >= a.rows || j >= b.rows) return;
+        if (i >= a.rows || j >= b.rows) return v;
         const int64_t at = (i0 + i) * sh.ldx + j0 + j;
         v = beta * v + a_coef * load_held<P, 8>(src, at, sh.x_size);
         if constexpr (LAST == kNsNext) store_held<P, 8>(dst, at, sh.x_size, v);
         else write(out + (i0 + i) * ld_out + j0 + j, v, sh.n - (j0 + j));
+        return v;
       },
       [&](int j, int i, f32x8 v) {
         if (j0 + j >= sh.n || i >= a.rows) return;
@@ -500,7 +498,7 @@ void launch_symmetric(const NsPlanes& tab, const NsTiles& tiles, int32_t n, int 
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, alpha, beta);
   };
   const bool deep = deep_launch(n);
-  if (tile == 256) launch(k_ns_symmetric<P, 256, 2, 4, 2, POLY>, 512);
+  if (tile == 256) launch(k_ns_symmetric<P, 256, 4, 2, 2, POLY>, 512);
   else if (tile == 128 && deep) launch(k_ns_symmetric<P, 128, 2, 4, 4, POLY>, 512);
   else if (tile == 128) launch(k_ns_symmetric<P, 128, 2, 4, 2, POLY>, 512);
   else if (deep) launch(k_ns_symmetric<P, 64, 2, 2, 8, POLY>, 256);
@@ -514,7 +512,7 @@ void launch_step(const Table& tab, const NsTiles& tiles, int32_t n, int tile, He
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, a_coef, beta, up);
   };
   const bool deep = deep_launch(n);
-  if (tile == 256) launch(k_ns_step<P, O, 256, 2, 4, 2, LAST, Table>, 512);
+  if (tile == 256) launch(k_ns_step<P, O, 256, 4, 2, 2, LAST, Table>, 512);
   else if (tile == 128 && deep) launch(k_ns_step<P, O, 128, 2, 4, 4, LAST, Table>, 512);
   else if (tile == 128) launch(k_ns_step<P, O, 128, 2, 4, 2, LAST, Table>, 512);
   else if (deep) launch(k_ns_step<P, O, 64, 2, 2, 8, LAST, Table>, 256);

@@ -245,9 +245,13 @@ struct TileProduct {
                                f32x4 (&acc)[MI][NI]) {
     u32x4 fa[MI], fb[NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) fa[i] = MapA::fragment(la, base_a, i, ks);
-#pragma unroll
     for (int j = 0; j < NI; ++j) fb[j] = MapB::fragment(lb, base_b, j, ks);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[i] = MapA::fragment(la, base_a, i, ks);
+    // All reads first: left to the compiler they trickle between the products,
+    // with fewer in flight (8192^3: 1115, 1270 and 1215 TFLOP/s for the three
+    // kinds of product; 1140, 1340 and 1310 so).
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -331,8 +335,9 @@ struct TileProduct {
   }
 
   // Hands the tile out eight values at a time: f(i, j, v) gets columns
-  // j .. j + 7 of row i when `rows` is set, ft(j, i, v) rows i .. i + 7 of
-  // column j when `cols` is, both inside the tile.  The accumulators go
+  // j .. j + 7 of row i when `rows` is set and returns what it made of them;
+  // ft(j, i, v) gets rows i .. i + 7 of column j when `cols` is (what f
+  // returned, if both are), all inside the tile.  The accumulators go
   // through the stages' memory, each wave by itself, so that a wave's accesses
   // to the result are runs of whole rows (or columns) and the code for eight
   // values exists once: with it in place for every accumulator, an epilogue
@@ -375,8 +380,14 @@ struct TileProduct {
           const int c = (lane % kLanes) * 2;
           const f32x4 lo = *(const __attribute__((address_space(3))) f32x4*)chunk(k, c);
           const f32x4 hi = *(const __attribute__((address_space(3))) f32x4*)chunk(k, c + 1);
-          f(row0 + p + k, col0 + c * 4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          const f32x8 v = f(row0 + p + k, col0 + c * 4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          if (cols) {
+            *(__attribute__((address_space(3))) f32x4*)chunk(k, c) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+            *(__attribute__((address_space(3))) f32x4*)chunk(k, c + 1) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+          }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
       if (cols) {
         constexpr int kLanes = RP / 8;
@@ -443,7 +454,7 @@ inline bool deep_launch(int64_t tiles) { return tiles <= kComputeUnits; }
 // held by the matrix cores' fp32 rate.
 inline double stage_us(bool f32, int tile) {
   if (f32) return tile == 256 ? 6.9 : tile == 128 ? 1.75 : 0.45;
-  return tile == 256 ? 1.65 : tile == 128 ? 0.54 : 0.25;
+  return tile == 256 ? 1.6 : tile == 128 ? 0.54 : 0.25;
 }
 
 // Workgroup b of n, with the workgroups of one XCD (b mod 8) on one run of
