@@ -218,7 +218,6 @@ hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, in
   if (c.tile == 256) launch_product<T, 256, 4, 2, 2, KCA, KCB>(g, direct, epi, stream);
   else if (c.tile == 128 && deep) launch_product<T, 128, 2, 4, 4, KCA, KCB>(g, direct, epi, stream);
   else if (c.tile == 128) launch_product<T, 128, 2, 4, 2, KCA, KCB>(g, direct, epi, stream);
-  else if (deep) launch_product<T, 64, 2, 2, 8, KCA, KCB>(g, direct, epi, stream);
   else launch_product<T, 64, 2, 2, 3, KCA, KCB>(g, direct, epi, stream);
   if (c.splits > 1) {
     const int64_t groups = m * ((n + 3) / 4);

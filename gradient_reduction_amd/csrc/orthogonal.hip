@@ -155,15 +155,8 @@ __global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsU
   if (threadIdx.x == 0) parts[(int64_t)(tab.first + e) * kNormParts + part] = sum[0] + sum[1] + sum[2] + sum[3];
 }
 
-// Eight (or four) held values at `at` of a plane; the second plane of a pair
-// lies `size` values on.
-template <int P, int N>
-__device__ __forceinline__ auto load_held(const Held* p, int64_t at, int64_t size) {
-  auto v = load_n<N>(p + at, N);
-  if constexpr (P == 2) v += load_n<N>(p + size + at, N);
-  return v;
-}
-
+// N held values at `at` of a plane; the second plane of a pair lies `size`
+// values on.
 template <int P, int N, class V>
 __device__ __forceinline__ void store_held(Held* p, int64_t at, int64_t size, V v) {
   store_n<N>(p + at, v, N);
@@ -238,19 +231,20 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
 }
 
 // The product of two operands that are pairs of planes, size_a and size_b
-// apart; the small products first.
-template <class Tile, int P, class Acc>
+// apart; the small products first.  hook is called with the stages that hold
+// B's own values (of each plane of it).
+template <class Tile, int P, class Acc, class Hook>
 __device__ __forceinline__ void held_product(Operand<Held> a, int64_t size_a, Operand<Held> b, int64_t size_b,
-                                             int64_t k, Acc& acc) {
+                                             int64_t k, Acc& acc, Hook&& hook) {
   if constexpr (P == 2) {
-    Operand<Held> low = b;
-    low.p += size_b;
-    Tile::run(a, low, 0, k, acc);
-    low = a;
+    Operand<Held> low = a;
     low.p += size_a;
     Tile::run(low, b, 0, k, acc);
+    low = b;
+    low.p += size_b;
+    Tile::run(a, low, 0, k, acc, hook);
   }
-  Tile::run(a, b, 0, k, acc);
+  Tile::run(a, b, 0, k, acc, hook);
 }
 
 // Tile t of the upper triangle of an nt x nt grid, by rows.
@@ -264,7 +258,7 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
   tj = row + left;
 }
 
-// A = alpha X XT (POLY false: src = X, dst = A), or B = beta A + alpha A A
+// A = alpha X XT (POLY false: src = X, dst = A), or B = alpha (beta A + A A)
 // (POLY true: src = A, dst = B; A is its own transpose).
 template <int P, int BT, int WM, int WN, int S, bool POLY>
 __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsTiles tiles, Held* planes, int32_t next,
@@ -284,14 +278,17 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
   const Operand<Held> a{src + i0 * ld, ld, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
   const Operand<Held> b{src + j0 * ld, ld, (int32_t)(sh.m - j0 < BT ? sh.m - j0 : BT)};
   f32x4 acc[Tile::MI][Tile::NI] = {};
-  held_product<Tile, P>(a, size, b, size, ld, acc);
+  // B: beta A, its own transpose, comes into the sums from the stages that
+  // hold it
+  held_product<Tile, P>(a, size, b, size, ld, acc, [&](LdsPtr la, int64_t k) {
+    if constexpr (POLY) Tile::add_b(la, k, i0, beta, acc);
+  });
   // Columns m .. lda - 1 get zeros; the mirrored tile gets the same values.
   Tile::each(
       acc, true, ti != tj,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j0 + j >= sh.lda) return v;
         v *= alpha;
-        if constexpr (POLY) v += beta * load_held<P, 8>(src, (i0 + i) * ld + j0 + j, size);
         store_held<P, 8>(dst, (i0 + i) * sh.lda + j0 + j, sh.a_size, v);
         return v;
       },
@@ -300,7 +297,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
       });
 }
 
-// X <- a X + beta B X into the other X plane, or out of it in the last step.
+// X <- beta (a X + B X) into the other X plane, or out of it in the last step.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
 template <int P, class O, int BT, int WM, int WN, int S, int LAST, class Table>
@@ -320,7 +317,10 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
   const Operand<Held> a{poly + i0 * sh.lda, sh.lda, (int32_t)(sh.m - i0 < BT ? sh.m - i0 : BT)};
   const Operand<Held> b{src + j0, sh.ldx, (int32_t)(sh.ldx - j0 < BT ? sh.ldx - j0 : BT)};
   f32x4 acc[Tile::MI][Tile::NI] = {};
-  held_product<Tile, P>(a, sh.a_size, b, sh.x_size, sh.m, acc);
+  // a X comes into the sums from the stages that hold it: with the tile read
+  // again after the sums, every unit waited for memory at once
+  held_product<Tile, P>(a, sh.a_size, b, sh.x_size, sh.m, acc,
+                        [&](LdsPtr la, int64_t k) { Tile::add_b(la, k, i0, a_coef, acc); });
   O* out = nullptr;
   int64_t ld_out = 0;
   float scale = 1.f, keep = 1.f;
@@ -340,23 +340,15 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
       acc, !flip, flip,
       [&](int i, int j, f32x8 v) {
         if (i >= a.rows || j >= b.rows) return v;
-        const int64_t at = (i0 + i) * sh.ldx + j0 + j;
-        v = beta * v + a_coef * load_held<P, 8>(src, at, sh.x_size);
-        if constexpr (LAST == kNsNext) store_held<P, 8>(dst, at, sh.x_size, v);
+        v *= beta;
+        if constexpr (LAST == kNsNext) store_held<P, 8>(dst, (i0 + i) * sh.ldx + j0 + j, sh.x_size, v);
         else write(out + (i0 + i) * ld_out + j0 + j, v, sh.n - (j0 + j));
         return v;
       },
       [&](int j, int i, f32x8 v) {
         if (j0 + j >= sh.n || i >= a.rows) return;
         const int64_t n = a.rows - i;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < n) {
-            const int64_t at = (i0 + i + k) * sh.ldx + j0 + j;
-            float old = (float)src[at];
-            if constexpr (P == 2) old += (float)src[sh.x_size + at];
-            v[k] = beta * v[k] + a_coef * old;
-          }
+        v *= beta;
         write(out + (j0 + j) * ld_out + i0 + i, v, n);
       });
 }
@@ -501,7 +493,6 @@ void launch_symmetric(const NsPlanes& tab, const NsTiles& tiles, int32_t n, int 
   if (tile == 256) launch(k_ns_symmetric<P, 256, 4, 2, 2, POLY>, 512);
   else if (tile == 128 && deep) launch(k_ns_symmetric<P, 128, 2, 4, 4, POLY>, 512);
   else if (tile == 128) launch(k_ns_symmetric<P, 128, 2, 4, 2, POLY>, 512);
-  else if (deep) launch(k_ns_symmetric<P, 64, 2, 2, 8, POLY>, 256);
   else launch(k_ns_symmetric<P, 64, 2, 2, 3, POLY>, 256);
 }
 
@@ -515,7 +506,6 @@ void launch_step(const Table& tab, const NsTiles& tiles, int32_t n, int tile, He
   if (tile == 256) launch(k_ns_step<P, O, 256, 4, 2, 2, LAST, Table>, 512);
   else if (tile == 128 && deep) launch(k_ns_step<P, O, 128, 2, 4, 4, LAST, Table>, 512);
   else if (tile == 128) launch(k_ns_step<P, O, 128, 2, 4, 2, LAST, Table>, 512);
-  else if (deep) launch(k_ns_step<P, O, 64, 2, 2, 8, LAST, Table>, 256);
   else launch(k_ns_step<P, O, 64, 2, 2, 3, LAST, Table>, 256);
 }
 
@@ -560,15 +550,18 @@ void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsSc
     const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
     const int32_t next = k & 1;
     launch_symmetric<P, false>(all, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
-    launch_symmetric<P, true>(all, poly, n_poly, poly_tile, planes, next, cc * (sc.b[k] / (sc.a * sc.a)),
-                              cb * (sc.b[k] / sc.a), stream);
+    // B = c (A A + b / c A): a c too small for fp32 to see beside b stands for
+    // zero
+    const double c = std::fabs(cc) < std::fabs(cb) * 0x1p-30 ? std::fabs(cb) * 0x1p-30 : cc;
+    launch_symmetric<P, true>(all, poly, n_poly, poly_tile, planes, next, (float)(c * sc.b[k] / ((double)sc.a * sc.a)),
+                              c != 0 ? (float)(cb * sc.a / c) : 0.f, stream);
     if (k + 1 < a.steps) {
-      launch_step<P, O, kNsNext>(all, step, n_step, step_tile, planes, next, ca, 1.f / sc.b[k], up, stream);
+      launch_step<P, O, kNsNext>(all, step, n_step, step_tile, planes, next, ca * sc.b[k], 1.f / sc.b[k], up, stream);
     } else {
       by_part([&](const NsTable& tab) {
         NsTiles last;
         const int32_t n = product_tiles(last, tab, kStep, last_tile);
-        launch_step<P, O, MOM ? kNsWeight : kNsOut>(tab, last, n, last_tile, planes, next, ca / sc.x,
+        launch_step<P, O, MOM ? kNsWeight : kNsOut>(tab, last, n, last_tile, planes, next, ca * sc.b[k],
                                                     1.f / (sc.b[k] * sc.x), up, stream);
       });
     }

@@ -258,9 +258,47 @@ struct TileProduct {
       for (int j = 0; j < NI; ++j) acc[i][j] = mma_slice(fb[j], fa[i], acc[i][j], T{});
   }
 
-  // acc += A B over k in [k0, k_end).
+  // acc(i, j) += coef B(j, i) for the rows i of the tile (its first row being k
+  // = i0) that the stage at k0 holds as its k: an operand that is also added
+  // to the result is taken from the stage in LDS, not read again.  A wave's
+  // rows are all in one stage.
+  __device__ static void add_b(LdsPtr la, int64_t k0, int64_t i0, float coef, f32x4 (&acc)[MI][NI]) {
+    static_assert(64 % (BM / WM) == 0 && sizeof(T) == 2, "stages hold whole waves' rows");
+    typedef T V __attribute__((ext_vector_type(4)));
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, r = lane & 15;
+    const int row_a = (wave / WN) * (BM / WM), row_b = (wave % WN) * (BN / WN);
+    if (k0 != i0 + row_a / BK * BK) return;
+    const LdsPtr lb = la + MapA::kBytes;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        V v;
+        if constexpr (KCB) {  // rows j in LDS: read transposed, lane r its column r
+          const int row = row_b + j * 16 + q * 4 + (r >> 2), k = row_a % BK + i * 16 + ((r & 3) << 2);
+          v = __builtin_bit_cast(V, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                        (__attribute__((address_space(3))) i16x4*)(
+                                            lb + row * 128 + (((k >> 3) ^ MapB::swizzle(row)) << 4) + ((k & 4) << 1))));
+        } else {
+          const int k = row_a % BK + i * 16 + r, col = row_b + j * 16 + q * 4;
+          v = *(const __attribute__((address_space(3))) V*)(
+              lb + k * (MapB::CPR * 16) + (((col >> 3) ^ MapB::swizzle(k)) << 4) + ((col & 4) << 1));
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(coef, (float)v[t], acc[i][j][t]);
+      }
+  }
+
+  struct NoHook {
+    __device__ void operator()(LdsPtr, int64_t) const {}
+  };
+
+  // acc += A B over k in [k0, k_end).  hook(la, k) is called when the stage of
+  // k .. k + 63 is at la (loads straight into LDS only).
+  template <class Hook = NoHook>
   __device__ static void run(const Operand<T>& a, const Operand<T>& b, int64_t k0, int64_t k_end,
-                             f32x4 (&acc)[MI][NI]) {
+                             f32x4 (&acc)[MI][NI], Hook&& hook = {}) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
     const uint32_t base_a = MapA::lane_base((wave / WN) * (BM / WM), q, r);
@@ -292,6 +330,7 @@ struct TileProduct {
         const LdsPtr la = (LdsPtr)cur;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) slice(la, la + MapA::kBytes, ks, base_a, base_b, acc);
+        hook(la, k0);
         k0 += BK;
       };
       each_index([&](auto i) { load(memory<i.value>(), k0 + i.value * BK); },
@@ -443,9 +482,11 @@ __device__ __forceinline__ void store_n(T* p, V v, int64_t n) {
 
 constexpr int64_t kComputeUnits = 256;
 
-// Stages in flight of a launch of `tiles` tiles: with no more tiles than
-// compute units each has a unit's memory for itself, and then as many stages
-// as fit hide the latency of what the launch before left in other caches.
+// Whether 128 tiles take four stages instead of two: with no more tiles than
+// compute units each has a unit's memory for itself (2048 x 1024 over 4096
+// bf16: 31.5 against 32.7 us forward, 26.5 against 28.2 us dw).  64 tiles keep
+// three: with eight, the longer code costs what the depth hides (one 1024 x
+// 1024 matrix orthogonalised: 173 us against 165).
 inline bool deep_launch(int64_t tiles) { return tiles <= kComputeUnits; }
 
 // Microseconds that a compute unit takes for a stage of a tile, as measured
