@@ -1183,6 +1183,11 @@ dc_status check_matrices(const dc_matrix* mats, int32_t num) {
   return DC_OK;
 }
 
+dc_status check_hold(int32_t hold) {
+  if (hold < DC_HOLD_AUTO || hold > DC_HOLD_PAIR) return fail(DC_ERR_ARG, "hold=%d", hold);
+  return DC_OK;
+}
+
 dc_status check_steps(int32_t steps, const float* coeffs, float eps) {
   if (steps < 1 || steps > DC_NS_MAX_STEPS)
     return fail(DC_ERR_ARG, "steps=%d outside [1, %d]", steps, DC_NS_MAX_STEPS);
@@ -1366,24 +1371,28 @@ dc_status dc_linear_backward(int32_t dtype, int64_t T, int64_t N, int64_t K, con
   return ok();
 }
 
-dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32_t num, int64_t* bytes) {
+dc_status dc_orthogonalize_workspace(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats,
+                                     int32_t num, int64_t* bytes) {
   dc_status st;
-  if ((st = check_dtype(dtype)) || (st = check_matrices(mats, num))) return st;
+  if ((st = check_dtype(dtype)) || (st = check_dtype(out_dtype)) || (st = check_hold(hold)) ||
+      (st = check_matrices(mats, num)))
+    return st;
   if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
-  *bytes = dc::ns_workspace(dtype, mats, num);
+  *bytes = dc::ns_workspace(dtype, out_dtype, hold, mats, num);
   return ok();
 }
 
-dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, int32_t steps,
-                           const float* coeffs, float eps, void* workspace,
+dc_status dc_orthogonalize(int32_t dtype, int32_t hold, const dc_matrix* mats, int32_t num,
+                           int32_t steps, const float* coeffs, float eps, void* workspace,
                            int64_t workspace_bytes, void* stream) {
   dc_status st;
-  if ((st = check_dtype(dtype)) || (st = check_steps(steps, coeffs, eps)) ||
+  if ((st = check_dtype(dtype)) || (st = check_hold(hold)) || (st = check_steps(steps, coeffs, eps)) ||
       (st = check_list(dtype, dtype, mats, num, false)) ||
-      (st = check_workspace(workspace, workspace_bytes, dc::ns_workspace(dtype, mats, num))))
+      (st = check_workspace(workspace, workspace_bytes, dc::ns_workspace(dtype, dtype, hold, mats, num))))
     return st;
   dc::NsLaunch a{};
   a.dtype = a.out_dtype = dtype;
+  a.hold = hold;
   a.mats = mats;
   a.num = num;
   a.steps = steps;
@@ -1393,13 +1402,14 @@ dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, in
   return hip_status(dc::launch_ns(a, static_cast<hipStream_t>(stream)), "orthogonalize launch");
 }
 
-dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, const dc_matrix* mats, int32_t num,
-                         float lr, const float* lr_scale, float mu, int32_t nesterov,
-                         float weight_decay, int32_t scale_mode, int32_t steps,
-                         const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
+dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, int32_t hold,
+                         const dc_matrix* mats, int32_t num, float lr, const float* lr_scale,
+                         float mu, int32_t nesterov, float weight_decay, int32_t scale_mode,
+                         int32_t steps, const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
                          void* stream) {
   dc_status st;
-  if ((st = check_dtype(dtype)) || (st = check_dtype(weight_dtype)) || (st = check_steps(steps, coeffs, eps)))
+  if ((st = check_dtype(dtype)) || (st = check_dtype(weight_dtype)) || (st = check_hold(hold)) ||
+      (st = check_steps(steps, coeffs, eps)))
     return st;
   if (!std::isfinite(lr) || !std::isfinite(mu) || !std::isfinite(weight_decay))
     return fail(DC_ERR_ARG, "lr=%g mu=%g weight_decay=%g", (double)lr, (double)mu, (double)weight_decay);
@@ -1407,11 +1417,12 @@ dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, const dc_matrix* m
   if (scale_mode < DC_SCALE_NONE || scale_mode > DC_SCALE_RMS) return fail(DC_ERR_ARG, "scale_mode=%d", scale_mode);
   if (reinterpret_cast<uintptr_t>(lr_scale) % 4 != 0) return fail(DC_ERR_ALIGN, "lr_scale is not aligned");
   if ((st = check_list(dtype, weight_dtype, mats, num, true)) ||
-      (st = check_workspace(workspace, workspace_bytes, dc::ns_workspace(dtype, mats, num))))
+      (st = check_workspace(workspace, workspace_bytes, dc::ns_workspace(dtype, weight_dtype, hold, mats, num))))
     return st;
   dc::NsLaunch a{};
   a.dtype = dtype;
   a.out_dtype = weight_dtype;
+  a.hold = hold;
   a.update = true;
   a.mats = mats;
   a.num = num;

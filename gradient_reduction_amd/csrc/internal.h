@@ -213,6 +213,7 @@ hipError_t launch_bias_act(int32_t dtype, int32_t grad_dtype, int64_t T, int64_t
 struct NsLaunch {
   int32_t dtype;      // of the gradients, and of `out` when update is false
   int32_t out_dtype;  // of the weights
+  int32_t hold;       // DC_HOLD_*
   bool update;
   const dc_matrix* mats;  // host
   int32_t num;
@@ -228,7 +229,7 @@ struct NsLaunch {
 float ns_factor(int32_t scale_mode, int32_t rows, int32_t cols);
 // Upper bound of every singular value at any step.
 double ns_largest(int32_t steps, const float* coeffs);
-int64_t ns_workspace(int32_t dtype, const dc_matrix* mats, int32_t num);
+int64_t ns_workspace(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats, int32_t num);
 hipError_t launch_ns(const NsLaunch& a, hipStream_t stream);
 
 }  // namespace dc

@@ -23,11 +23,17 @@ constexpr int kNsPart = 48;           // of them whose addresses fit one launch'
 constexpr int kNormParts = 256;       // partial sums of squares per matrix, at most
 constexpr int64_t kNormSpan = 16384;  // elements per partial sum, at least
 
-// What X, A and B are held in.  One fp16 (11 bits) for bf16 gradients; two for
-// fp32 ones, a value and what it leaves (22 bits), multiplied as high high +
-// high low + low high: three products of 16 bits take a fifth of one product
-// of fp32 on these matrix cores.
+// What X, A and B are held in: one fp16 (11 bits), or two, a value and what it
+// leaves (22 bits), multiplied as high high + high low + low high (three
+// products of 16 bits take a fifth of one product of fp32 on these matrix
+// cores).  One leaves 1.3e-3 to 1.6e-3 of |O|_F after five steps where the
+// smaller side is kPairUnder or more, less than the rounding of O to bf16; on
+// smaller matrices, whose few singular values do not average the roundings, it
+// left 8e-3 at worst, and there two cost little.  48 matrices of 1024 x 1024
+// to 4096 x 1024 with their momenta and weights take 2.9 ms with one, 6.8 with
+// two.
 using Held = _Float16;
+constexpr int32_t kPairUnder = 256;
 
 // One matrix of a chunk.  Its planes in the workspace, in values from the
 // planes' base: X [m][ldx], the next X [m][ldx], A [m][lda], B [m][lda]; with
@@ -406,24 +412,37 @@ NsScales ns_scales(int32_t steps, const float* coeffs) {
   return s;
 }
 
-// The next chunk of matrices from `first`: kNsChunk of them at most, and of
-// 2^22 64 x 64 tiles together unless it is one matrix (a grid holds 2^24).
-int32_t chunk_end(const dc_matrix* mats, int32_t n, int32_t first) {
-  int64_t tiles = 0;
-  int32_t k = first;
-  // what is left, in chunks of about one size
-  const int32_t left = n - first, even = (left + (left + kNsChunk - 1) / kNsChunk - 1) / ((left + kNsChunk - 1) / kNsChunk);
-  for (; k < n && k < first + even; ++k) {
-    tiles += ((int64_t)(mats[k].rows + 63) / 64) * ((mats[k].cols + 63) / 64);
-    if (k > first && tiles > ((int64_t)1 << 22)) break;
+// How many values hold one of a matrix's.
+struct Holding {
+  int32_t dtype, out_dtype, hold;
+  int values(const dc_matrix& m) const {
+    if (hold != DC_HOLD_AUTO) return hold == DC_HOLD_PAIR ? 2 : 1;
+    return dtype == DC_F32 || out_dtype == DC_F32 || std::min(m.rows, m.cols) < kPairUnder ? 2 : 1;
   }
-  return k;
-}
+};
 
-int64_t chunk_values(const dc_matrix* mats, int32_t first, int32_t last, int pair) {
-  int64_t v = 0;
-  for (int32_t k = first; k < last; ++k) v += NsShape(mats[k].rows, mats[k].cols).values(pair);
-  return v;
+// f(pair, indices, count) for every chunk: matrices held alike, kNsChunk of
+// them at most and of 2^22 64 x 64 tiles together unless it is one (a grid
+// holds 2^24), in chunks of about one size.
+template <class F>
+void each_chunk(const Holding& held, const dc_matrix* mats, int32_t num, F&& f) {
+  for (const int pair : {1, 2}) {
+    int32_t left = 0;
+    for (int32_t k = 0; k < num; ++k) left += held.values(mats[k]) == pair;
+    for (int32_t k = 0; left > 0;) {
+      const int32_t chunks = (left + kNsChunk - 1) / kNsChunk, most = (left + chunks - 1) / chunks;
+      int32_t at[kNsChunk], count = 0;
+      int64_t tiles = 0;
+      for (; k < num && count < most; ++k) {
+        if (held.values(mats[k]) != pair) continue;
+        tiles += ((int64_t)(mats[k].rows + 63) / 64) * ((mats[k].cols + 63) / 64);
+        if (count > 0 && tiles > ((int64_t)1 << 22)) break;
+        at[count++] = k;
+      }
+      f(pair, at, count);
+      left -= count;
+    }
+  }
 }
 
 constexpr int64_t kPartsBytes = (int64_t)kNsChunk * kNormParts * 8;
@@ -568,31 +587,32 @@ void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsSc
   }
 }
 
-template <int P, class G, class O, bool MOM>
+template <class G, class O, bool MOM>
 hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
   const NsScales sc = ns_scales(a.steps, a.coeffs);
   double* parts = static_cast<double*>(a.workspace);
   Held* planes = reinterpret_cast<Held*>(static_cast<char*>(a.workspace) + kPartsBytes);
   const NsUpdate up{a.mu, a.lr * a.weight_decay, a.nesterov, a.lr_scale};
-  for (int32_t first = 0, last; first < a.num; first = last) {
-    last = chunk_end(a.mats, a.num, first);
+  hipError_t status = hipSuccess;
+  each_chunk(Holding{a.dtype, a.out_dtype, a.hold}, a.mats, a.num, [&](int pair, const int32_t* at, int32_t count) {
+    if (status != hipSuccess) return;
     NsMatrix mats[kNsChunk];
     int64_t base = 0;
-    for (int32_t k = first; k < last; ++k) {
-      const dc_matrix& d = a.mats[k];
-      mats[k - first] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
-                                 a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
-      base += NsShape(d.rows, d.cols).values(P);
+    for (int32_t k = 0; k < count; ++k) {
+      const dc_matrix& d = a.mats[at[k]];
+      mats[k] = NsMatrix{d.grad, d.out, d.momentum, d.ld_grad, d.ld_out, base, d.rows, d.cols,
+                         a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
+      base += NsShape(d.rows, d.cols).values(pair);
     }
     // the longest sums first, so that short ones fill what they leave
-    std::sort(mats, mats + (last - first), [](const NsMatrix& x, const NsMatrix& y) {
+    std::sort(mats, mats + count, [](const NsMatrix& x, const NsMatrix& y) {
       return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
     });
-    ns_chunk<P, G, O, MOM>(mats, last - first, a, sc, up, parts, planes, stream);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+    if (pair == 2) ns_chunk<2, G, O, MOM>(mats, count, a, sc, up, parts, planes, stream);
+    else ns_chunk<1, G, O, MOM>(mats, count, a, sc, up, parts, planes, stream);
+    status = hipGetLastError();
+  });
+  return status;
 }
 
 }  // namespace
@@ -609,27 +629,28 @@ double ns_largest(int32_t steps, const float* coeffs) {
   return most;
 }
 
-int64_t ns_workspace(int32_t dtype, const dc_matrix* mats, int32_t num) {
+int64_t ns_workspace(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats, int32_t num) {
   int64_t most = 0;
-  for (int32_t first = 0, last; first < num; first = last) {
-    last = chunk_end(mats, num, first);
-    most = std::max(most, chunk_values(mats, first, last, dtype == DC_F32 ? 2 : 1));
-  }
+  each_chunk(Holding{dtype, out_dtype, hold}, mats, num, [&](int pair, const int32_t* at, int32_t count) {
+    int64_t v = 0;
+    for (int32_t k = 0; k < count; ++k) v += NsShape(mats[at[k]].rows, mats[at[k]].cols).values(pair);
+    most = std::max(most, v);
+  });
   return num ? kPartsBytes + most * (int64_t)sizeof(Held) : 0;
 }
 
 hipError_t launch_ns(const NsLaunch& a, hipStream_t stream) {
   if (a.num == 0) return hipSuccess;
   if (!a.update) {
-    if (a.dtype == DC_F32) return ns_run<2, float, float, false>(a, stream);
-    return ns_run<1, __bf16, __bf16, false>(a, stream);
+    if (a.dtype == DC_F32) return ns_run<float, float, false>(a, stream);
+    return ns_run<__bf16, __bf16, false>(a, stream);
   }
   if (a.dtype == DC_F32) {
-    if (a.out_dtype == DC_F32) return ns_run<2, float, float, true>(a, stream);
-    return ns_run<2, float, __bf16, true>(a, stream);
+    if (a.out_dtype == DC_F32) return ns_run<float, float, true>(a, stream);
+    return ns_run<float, __bf16, true>(a, stream);
   }
-  if (a.out_dtype == DC_F32) return ns_run<1, __bf16, float, true>(a, stream);
-  return ns_run<1, __bf16, __bf16, true>(a, stream);
+  if (a.out_dtype == DC_F32) return ns_run<__bf16, float, true>(a, stream);
+  return ns_run<__bf16, __bf16, true>(a, stream);
 }
 
 }  // namespace dc

@@ -25,6 +25,7 @@ DC_MAX_W, DC_MAX_GROUPS, DC_MAX_COMMS = 64, 64, 8
 
 DC_ACT_NONE, DC_ACT_RELU, DC_ACT_GELU, DC_ACT_SILU = 0, 1, 2, 3
 DC_SCALE_NONE, DC_SCALE_ASPECT, DC_SCALE_RMS = 0, 1, 2
+DC_HOLD_AUTO, DC_HOLD_ONE, DC_HOLD_PAIR = 0, 1, 2
 DC_NS_MAX_STEPS = 16
 
 TASK_DTYPE = np.dtype([("offset", "<i8"), ("numel", "<i8"), ("param", "<i4"),
@@ -106,9 +107,9 @@ _SIGS = {
                               _vp, _i64, _vp], _i32),
     "dc_linear_backward": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
                             _vp, _i64, _i32, _vp, _i64, _vp], _i32),
-    "dc_orthogonalize_workspace": ([_i32, _vp, _i32, _vp], _i32),
-    "dc_orthogonalize": ([_i32, _vp, _i32, _i32, _vp, _f32, _vp, _i64, _vp], _i32),
-    "dc_muon_update": ([_i32, _i32, _vp, _i32, _f32, _vp, _f32, _i32, _f32, _i32, _i32, _vp, _f32, _vp,
+    "dc_orthogonalize_workspace": ([_i32, _i32, _i32, _vp, _i32, _vp], _i32),
+    "dc_orthogonalize": ([_i32, _i32, _vp, _i32, _i32, _vp, _f32, _vp, _i64, _vp], _i32),
+    "dc_muon_update": ([_i32, _i32, _i32, _vp, _i32, _f32, _vp, _f32, _i32, _f32, _i32, _i32, _vp, _f32, _vp,
                         _i64, _vp], _i32),
     "dc_round_bf16": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_copy": ([_vp, _vp, _i64, _vp], _i32),
@@ -510,31 +511,32 @@ def dc_linear_backward(dtype, T, N, K, dz, ld_dz, w, ld_w, x, ld_x, dx, ld_dx, g
         _dev(dw), ld_dw, accumulate, _dev(workspace), workspace_bytes, _stream(stream)))
 
 
-def dc_orthogonalize_workspace(dtype, mats, num):
+def dc_orthogonalize_workspace(dtype, out_dtype, hold, mats, num):
     """Host only; mats: MATRIX_DTYPE records.  Bytes of workspace."""
     mp, _a = _host(mats, MATRIX_DTYPE)
     n = ctypes.c_int64(0)
-    _check("dc_orthogonalize_workspace", lib().dc_orthogonalize_workspace(dtype, mp, num,
-                                                                          ctypes.byref(n)))
+    _check("dc_orthogonalize_workspace", lib().dc_orthogonalize_workspace(
+        dtype, out_dtype, hold, mp, num, ctypes.byref(n)))
     return n.value
 
 
-def dc_orthogonalize(dtype, mats, num, steps, coeffs, eps, workspace, workspace_bytes, stream=None):
+def dc_orthogonalize(dtype, hold, mats, num, steps, coeffs, eps, workspace, workspace_bytes,
+                     stream=None):
     """mats: MATRIX_DTYPE records (host); coeffs: steps x 3."""
     mp, _a = _host(mats, MATRIX_DTYPE)
     cp, _b = _host(coeffs, np.float32)
     _check("dc_orthogonalize", lib().dc_orthogonalize(
-        dtype, mp, num, steps, cp, eps, _dev(workspace), workspace_bytes, _stream(stream)))
+        dtype, hold, mp, num, steps, cp, eps, _dev(workspace), workspace_bytes, _stream(stream)))
 
 
-def dc_muon_update(dtype, weight_dtype, mats, num, lr, lr_scale, mu, nesterov, weight_decay, scale_mode,
-                   steps, coeffs, eps, workspace, workspace_bytes, stream=None):
+def dc_muon_update(dtype, weight_dtype, hold, mats, num, lr, lr_scale, mu, nesterov, weight_decay,
+                   scale_mode, steps, coeffs, eps, workspace, workspace_bytes, stream=None):
     """mats: MATRIX_DTYPE records (host); coeffs: steps x 3; lr_scale: device
     float or None."""
     mp, _a = _host(mats, MATRIX_DTYPE)
     cp, _b = _host(coeffs, np.float32)
     _check("dc_muon_update", lib().dc_muon_update(
-        dtype, weight_dtype, mp, num, lr, _dev(lr_scale), mu, nesterov, weight_decay, scale_mode, steps,
+        dtype, weight_dtype, hold, mp, num, lr, _dev(lr_scale), mu, nesterov, weight_decay, scale_mode, steps,
         cp, eps, _dev(workspace), workspace_bytes, _stream(stream)))
 
 

@@ -427,26 +427,25 @@ class Zero1FlushExecutor:
         self.m_recs = recs
         self.m_wtype = dc.DC_F32 if torch.float32 in kinds else dc.DC_BF16
         self.m_keep = (dict(weights), dict(momenta))
-        self.m_bytes = dc.dc_orthogonalize_workspace(self.dtype, recs, len(recs))
 
     def muon_update(self, slab_out, ld_out: int, lr: float, mu: float = 0.95, nesterov: bool = True,
                     weight_decay: float = 0.0, scale: str = "rms", steps: int = 5, coeffs=None,
-                    eps: float = 1e-7, lr_scale=None, stream=None) -> None:
+                    eps: float = 1e-7, hold: str = "auto", lr_scale=None, stream=None) -> None:
         """Steps the registered matrices from the flushed slab (after flush()
         of every bucket into slab_out, on the same stream); arguments as in
         muon.update()."""
         from . import linear, muon
-        if scale not in muon.SCALES:
-            raise ValueError(f"scale {scale!r}: one of {sorted(muon.SCALES)}")
+        held, mode = muon._choice("hold", hold, muon.HOLDS), muon._choice("scale", scale, muon.SCALES)
         eb = 2 if self.dtype == dc.DC_BF16 else 4
         base = slab_out if isinstance(slab_out, int) else slab_out.data_ptr()
         recs = self.m_recs.copy()
         recs["grad"] = base + (self.m_rows * ld_out + self.m_cols) * eb
         table = muon._steps(steps, muon.COEFFS if coeffs is None else coeffs)
         with linear.on(self.d_owner.device, stream):
-            dc.dc_muon_update(self.dtype, self.m_wtype, recs, len(recs), lr, lr_scale, mu,
-                              1 if nesterov else 0, weight_decay, muon.SCALES[scale], steps, table, eps,
-                              linear.workspace(self.m_bytes, self.d_owner.device), self.m_bytes)
+            nbytes = dc.dc_orthogonalize_workspace(self.dtype, self.m_wtype, held, recs, len(recs))
+            dc.dc_muon_update(self.dtype, self.m_wtype, held, recs, len(recs), lr, lr_scale, mu,
+                              1 if nesterov else 0, weight_decay, mode, steps, table, eps,
+                              linear.workspace(nbytes, self.d_owner.device), nbytes)
 
     # -- one step as a HIP graph --------------------------------------------------
 

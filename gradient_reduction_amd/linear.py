@@ -7,7 +7,8 @@ workspaces come from torch's allocator, and everything runs in libdc.so
 (dc_linear, dc_bias_act_backward, dc_linear_backward) on `stream`, or on
 torch's current stream of the tensors' device.  Rows may have any stride of at
 least their length; columns are contiguous.  Tensors made on another stream
-are the caller's to order, as in torch.
+are the caller's to order, as in torch.  Nothing here is seen by autograd:
+backward() is called by hand.
 """
 import contextlib
 

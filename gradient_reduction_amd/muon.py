@@ -9,7 +9,8 @@ products and steps the weights; orthogonalize() is the middle part alone.
 A tensor [..., rows, cols] is a batch of matrices; one call takes a list of
 tensors of any shapes.  Marshalling only: everything runs in libdc.so
 (dc_orthogonalize, dc_muon_update) on `stream`, or on torch's current stream
-of the tensors' device; workspaces come from torch's allocator.
+of the tensors' device; workspaces come from torch's allocator.  Nothing here
+is seen by autograd.
 """
 import numpy as np
 import torch
@@ -20,6 +21,7 @@ from .linear import dtype_of, on, workspace
 # The quintic a s + b s^3 + c s^5 whose slope at 0 lifts small singular values
 # fastest while five steps bring all of them near 1.
 COEFFS = (3.4445, -4.7750, 2.0315)
+HOLDS = {"auto": dc.DC_HOLD_AUTO, "one": dc.DC_HOLD_ONE, "pair": dc.DC_HOLD_PAIR}
 SCALES = {"none": dc.DC_SCALE_NONE, "aspect": dc.DC_SCALE_ASPECT, "rms": dc.DC_SCALE_RMS}
 
 
@@ -69,16 +71,26 @@ def matrices(grads, outs, momenta=None):
     return np.concatenate(recs) if recs else np.zeros(0, dc.MATRIX_DTYPE)
 
 
+def _choice(name, value, table):
+    if value not in table:
+        raise ValueError(f"{name} {value!r}: one of {sorted(table)}")
+    return table[value]
+
+
 def _alike(name, ts, dtype, device):
     for k, t in enumerate(ts):
         if t.dtype != dtype or t.device != device:
             raise ValueError(f"{name} {k} is {t.dtype} on {t.device}, expected {dtype} on {device}")
 
 
-def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, out=None, stream=None):
+def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, hold="auto", out=None, stream=None):
     """Every matrix orthogonalised, in the gradients' dtype: a list of new
     tensors, or `out` (which may be the gradients).  `grads`: a list of
-    tensors, or one (then one comes back)."""
+    tensors, or one (then one comes back).  hold: "one" fp16 for each value of
+    the steps (1.5e-3 of the result on large matrices), a "pair" (5e-7, three
+    times the products), or "auto": pairs for float32 and for smaller sides
+    under 256."""
+    held = _choice("hold", hold, HOLDS)
     one = torch.is_tensor(grads)
     gs = [grads] if one else list(grads)
     if not gs:
@@ -95,27 +107,27 @@ def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, out=None, stream=None
                 raise ValueError(f"{len(outs)} outputs for {len(gs)} gradients")
             _alike("out", outs, dt, dev)
         mats = matrices(gs, outs)
-        nbytes = dc.dc_orthogonalize_workspace(dtype, mats, len(mats))
-        dc.dc_orthogonalize(dtype, mats, len(mats), steps, table, eps, workspace(nbytes, dev), nbytes)
+        nbytes = dc.dc_orthogonalize_workspace(dtype, dtype, held, mats, len(mats))
+        dc.dc_orthogonalize(dtype, held, mats, len(mats), steps, table, eps, workspace(nbytes, dev), nbytes)
     return outs[0] if one else outs
 
 
 def update(weights, grads, momentum, lr, mu=0.95, nesterov=True, weight_decay=0.0, scale="rms", steps=5,
-           coeffs=COEFFS, eps=1e-7, lr_scale=None, stream=None):
+           coeffs=COEFFS, eps=1e-7, hold="auto", lr_scale=None, stream=None):
     """One step of the weights and momenta, in place:
       m <- mu m + g;  u = mu m + g (nesterov) or m
       w <- (1 - l weight_decay) w - l s orthogonalize(u)
     with l = lr (times lr_scale, a device float32 read when the work runs) and
     s the shape's factor: "none", "aspect" sqrt(max(1, rows / cols)) or "rms"
     0.2 sqrt(max(rows, cols)).  Lists of tensors, or one of each; momenta are
-    float32, weights and gradients each bfloat16 or float32."""
+    float32, weights and gradients each bfloat16 or float32.  hold: as for
+    orthogonalize(); "auto" takes pairs for float32 weights too."""
+    held, mode = _choice("hold", hold, HOLDS), _choice("scale", scale, SCALES)
     if torch.is_tensor(weights):
         weights, grads, momentum = [weights], [grads], [momentum]
     ws, gs, ms = list(weights), list(grads), list(momentum)
     if not len(ws) == len(gs) == len(ms):
         raise ValueError(f"{len(ws)} weights, {len(gs)} gradients, {len(ms)} momenta")
-    if scale not in SCALES:
-        raise ValueError(f"scale {scale!r}: one of {sorted(SCALES)}")
     if not ws:
         return
     dev = gs[0].device
@@ -125,8 +137,10 @@ def update(weights, grads, momentum, lr, mu=0.95, nesterov=True, weight_decay=0.
     _alike("momentum", ms, torch.float32, dev)
     if lr_scale is not None:
         _alike("lr_scale", [lr_scale], torch.float32, dev)
+        if lr_scale.numel() != 1:
+            raise ValueError(f"lr_scale of {lr_scale.numel()} elements, one is needed")
     mats = matrices(gs, ws, ms)
     with on(dev, stream):
-        nbytes = dc.dc_orthogonalize_workspace(dtype, mats, len(mats))
-        dc.dc_muon_update(dtype, wtype, mats, len(mats), lr, lr_scale, mu, 1 if nesterov else 0,
-                          weight_decay, SCALES[scale], steps, table, eps, workspace(nbytes, dev), nbytes)
+        nbytes = dc.dc_orthogonalize_workspace(dtype, wtype, held, mats, len(mats))
+        dc.dc_muon_update(dtype, wtype, held, mats, len(mats), lr, lr_scale, mu, 1 if nesterov else 0,
+                          weight_decay, mode, steps, table, eps, workspace(nbytes, dev), nbytes)

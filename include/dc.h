@@ -96,6 +96,9 @@ typedef int32_t dc_status;
 #define DC_SCALE_NONE 0      /* shape factor of a matrix update: 1 */
 #define DC_SCALE_ASPECT 1    /* sqrt(max(1, rows / cols)) */
 #define DC_SCALE_RMS 2       /* 0.2 sqrt(max(rows, cols)) */
+#define DC_HOLD_AUTO 0       /* what Newton-Schulz steps hold a value in: by the types */
+#define DC_HOLD_ONE 1        /* one fp16 */
+#define DC_HOLD_PAIR 2       /* a pair of fp16 */
 #define DC_NS_MAX_STEPS 16   /* Newton-Schulz steps per call */
 
 #define DC_MAX_W 64          /* simulated ranks per slab */
@@ -872,10 +875,11 @@ dc_status dc_linear_backward(int32_t dtype, int64_t T, int64_t N, int64_t K, con
                              int32_t accumulate, void* workspace, int64_t workspace_bytes,
                              void* stream);
 
-/* Bytes of workspace of dc_orthogonalize and dc_muon_update for this list
- * (its rows and cols).  Host only. */
-dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32_t num,
-                                     int64_t* bytes);
+/* Bytes of workspace of dc_orthogonalize (out_dtype = dtype) and
+ * dc_muon_update (out_dtype = weight_dtype) for this list (its rows and
+ * cols).  Host only. */
+dc_status dc_orthogonalize_workspace(int32_t dtype, int32_t out_dtype, int32_t hold,
+                                     const dc_matrix* mats, int32_t num, int64_t* bytes);
 
 /* Every matrix orthogonalised by Newton-Schulz products.  With X the
  * gradient (its transpose where rows > cols):
@@ -884,9 +888,13 @@ dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32
  * and X (transposed back) is written to out: the singular vectors stay, the
  * singular values go through the odd polynomials a s + b s^3 + c s^5.
  * X, A and B are held in fp16, by powers of two that the polynomials' bounds
- * keep from overflowing, with fp32 sums: for DC_BF16 one fp16 (11 bits),
- * about 1.5e-3 of |out|_F before the rounding to bf16; for DC_F32 a pair (22
- * bits), about 5e-7.  |X|_F is summed in fp64.  A zero matrix gives zero (NaN when eps is 0); a NaN or
+ * keep from overflowing, with fp32 sums: a pair of them (22 bits), which leaves
+ * about 5e-7 of |out|_F, or one (11 bits), which leaves about 1.5e-3 on
+ * matrices of 256 and more a side, up to 1e-2 on small ones, and takes a third
+ * of the products.  hold DC_HOLD_AUTO takes pairs where the gradients or the
+ * output are fp32 or the smaller side is under 256, else one; DC_HOLD_ONE and
+ * DC_HOLD_PAIR are the caller's choice for the whole list.  |X|_F is summed in
+ * fp64.  A zero matrix gives zero (NaN when eps is 0); a NaN or
  * infinity anywhere gives NaN in the whole of its matrix and no other.
  *   mats, num       host dc_matrix[num], num <= 2^20; out has the dtype of the gradients
  *                   and may be the gradient itself (same ld), otherwise
@@ -895,8 +903,8 @@ dc_status dc_orthogonalize_workspace(int32_t dtype, const dc_matrix* mats, int32
  *                   bound on the singular values must stay under 64
  *                   (else DC_ERR_ARG: the steps diverge)
  *   eps             >= 0 */
-dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, int32_t steps,
-                           const float* coeffs, float eps, void* workspace,
+dc_status dc_orthogonalize(int32_t dtype, int32_t hold, const dc_matrix* mats, int32_t num,
+                           int32_t steps, const float* coeffs, float eps, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
 /* The owner's update of whole matrices from their reduced gradients ([DS]
@@ -904,7 +912,7 @@ dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, in
  * gradient).  For every matrix:
  *   m <- mu m + g                              (fp32, stored)
  *   u  = nesterov ? mu m + g : m
- *   O  = u orthogonalised, as dc_orthogonalize (in the precision of dtype)
+ *   O  = u orthogonalised, as dc_orthogonalize (held as hold says)
  *   w <- (1 - l weight_decay) w - l s O        (fp32, rounded to weight_dtype)
  * with l = lr, times *lr_scale when given (device float[1], read when the
  * work runs: a recorded graph follows a schedule through it), and s the
@@ -912,10 +920,10 @@ dc_status dc_orthogonalize(int32_t dtype, const dc_matrix* mats, int32_t num, in
  *   dtype         of the gradients; weight_dtype: of out, the weights
  *   mats, num     host dc_matrix[num]; weights and momenta overlap nothing
  * Other arguments as in dc_orthogonalize. */
-dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, const dc_matrix* mats, int32_t num,
-                         float lr, const float* lr_scale, float mu, int32_t nesterov,
-                         float weight_decay, int32_t scale_mode, int32_t steps,
-                         const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
+dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, int32_t hold,
+                         const dc_matrix* mats, int32_t num, float lr, const float* lr_scale,
+                         float mu, int32_t nesterov, float weight_decay, int32_t scale_mode,
+                         int32_t steps, const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
                          void* stream);
 
 #ifdef __cplusplus

@@ -2,7 +2,7 @@
 in 64 bits.
 
 The bound on |error|_F is carried through the steps.  With u the half step of
-what X, A and B are held in (fp16 2^-11 for bf16 gradients, fp32 2^-24) and
+what X, A and B are held in (one fp16 2^-11, a pair of them 2^-22) and
 g(k) = 2 k 2^-23 for a sum of k products:
   dA <= u |A| + g(n) |X|^2
   dB <= (|b| + 2 |c| |A|_2) dA + u |B| + g(m) |c| |A|^2 + 2^-21 (|b| |A| + |c| |A|^2)
@@ -47,7 +47,7 @@ def reference(u, steps, coeffs, eps, kind, u_err=0.0):
     """(O in 64 bits, bound on the error's Frobenius norm before the output's
     rounding) for one matrix U known to u_err |U|_F."""
     t = T()
-    hold = 2.0 ** -11 if kind == "bf16" else 2.0 ** -24
+    hold = 2.0 ** -11 if kind == "bf16" else 2.0 ** -22
     flip = u.shape[0] > u.shape[1]
     x = u.t() if flip else u
     x = x / (x.norm() + eps)
@@ -129,8 +129,10 @@ def test_large_tiles_with_odd_sizes(kind):
     gen = t.Generator().manual_seed(4)
     gs = [gradient(gen, 1100, 2090, dtype=dt(kind)), gradient(gen, 3001, 515, dtype=dt(kind)),
           gradient(gen, 7, 11, dtype=dt(kind))]
-    for g, o in zip(gs, muon.orthogonalize(gs)):
-        check(f"{tuple(g.shape)}", o, g.cpu().double(), kind, out_eps=half_step(dt(kind)))
+    for hold in ("auto", "one", "pair"):
+        held = {"auto": kind, "one": "bf16", "pair": "f32"}[hold]
+        for g, o in zip(gs, muon.orthogonalize(gs, hold=hold)):
+            check(f"{tuple(g.shape)} {hold}", o, g.cpu().double(), held, out_eps=half_step(dt(kind)))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
@@ -198,7 +200,8 @@ def test_other_steps(coeffs, kind):
 
 @pytest.mark.parametrize("kind, wkind", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("nesterov, scale", [(True, "rms"), (False, "aspect"), (True, "none")])
-def test_update(kind, wkind, nesterov, scale):
+@pytest.mark.parametrize("choice", ["auto", "one"])
+def test_update(kind, wkind, nesterov, scale, choice):
     t = T()
     gen = t.Generator().manual_seed(7)
     shapes = [(1, 1), (3, 40), (40, 3), (65, 130), (200, 120), (2, 66, 67)]
@@ -213,7 +216,7 @@ def test_update(kind, wkind, nesterov, scale):
     for step, scalar in ((0, None), (1, lrs)):
         w0, m0 = [w.cpu().double() for w in ws], [m.cpu().double() for m in ms]
         muon.update(ws, gs, ms, lr=float(lr), mu=float(mu), nesterov=nesterov, weight_decay=float(wd), scale=scale,
-                    lr_scale=scalar)
+                    hold=choice, lr_scale=scalar)
         rate = float(lr) * (0.5 if scalar is not None else 1.0)
         for k, s in enumerate(shapes):
             rows, cols = s[-2:]
@@ -227,7 +230,8 @@ def test_update(kind, wkind, nesterov, scale):
             for uu, ww, oo, gg, mm in zip(*flat):
                 # u: two fused multiply-adds, each off by half a step of its result
                 du = (2.0 ** -24 * (mm.norm() + uu.norm()) / uu.norm()).item()
-                o, bound = reference(uu, 5, np.tile(np.array(muon.COEFFS, np.float32), (5, 1)), 1e-7, kind, du)
+                held = "bf16" if choice == "one" or (kind == wkind == "bf16" and min(rows, cols) >= 256) else "f32"
+                o, bound = reference(uu, 5, np.tile(np.array(muon.COEFFS, np.float32), (5, 1)), 1e-7, held, du)
                 want = oo * (1 - rate * float(wd)) - rate * f * o
                 bound = (rate * f * bound + 6 * 2.0 ** -24 * (oo.norm() + rate * f * o.norm()).item()
                          + half_step(dt(wkind)) * want.norm().item()) * 1.01
@@ -335,7 +339,7 @@ def test_flush_then_owners_update(owners, dtype):
                 assert bool(((momenta[p].cpu().double() - m).abs() <= 2.0 ** -24 * m.abs() + 1e-40).all())
                 u = mu * m + g
                 du = (2.0 ** -24 * (m.norm() + u.norm()) / u.norm()).item()
-                o, bound = reference(u, 5, co, 1e-7, "bf16" if dtype == wl.DT_BF16 else "f32", du)
+                o, bound = reference(u, 5, co, 1e-7, "f32", du)     # fp32 weights: pairs
                 f = lr * 0.2 * max(sizes[p]) ** 0.5
                 want = old[p][0] * (1 - lr * wd) - f * o
                 bound = (f * bound + 7 * 2.0 ** -24 * (want.norm() + f * o.norm()).item()) * 1.01

@@ -93,17 +93,18 @@ BIG = 1 << 40
     (dc.DC_ERR_ARG, mats((3, 4), out=(0, at(0) + 2))),               # its own, shifted
 ])
 def test_list_refusals(code, m):
-    expect(code, dc.dc_orthogonalize, 0, m, len(m), 5, COEFFS, 1e-7, at(20), BIG, 0)
+    expect(code, dc.dc_orthogonalize, 0, 0, m, len(m), 5, COEFFS, 1e-7, at(20), BIG, 0)
     if not (len(m) == 1 and m["out"][0] == m["grad"][0] + 2):
-        expect(code, dc.dc_muon_update, 0, 0, m, len(m), 0.1, None, 0.9, 1, 0.0, 2, 5, COEFFS, 1e-7, at(20), BIG, 0)
+        expect(code, dc.dc_muon_update, 0, 0, 0, m, len(m), 0.1, None, 0.9, 1, 0.0, 2, 5, COEFFS, 1e-7, at(20), BIG, 0)
 
 
 def test_update_refusals():
-    def call(m=mats((3, 4)), dtype=0, wtype=1, num=1, lr=0.1, lrs=None, mu=0.9, nest=1, wd=0.0, mode=2, steps=5,
+    def call(m=mats((3, 4)), dtype=0, wtype=1, hold=0, num=1, lr=0.1, lrs=None, mu=0.9, nest=1, wd=0.0, mode=2, steps=5,
              co=COEFFS, eps=1e-7, ws=at(20), nbytes=BIG):
-        dc.dc_muon_update(dtype, wtype, m, num, lr, lrs, mu, nest, wd, mode, steps, co, eps, ws, nbytes, 0)
+        dc.dc_muon_update(dtype, wtype, hold, m, num, lr, lrs, mu, nest, wd, mode, steps, co, eps, ws, nbytes, 0)
 
     for code, change in [(dc.DC_ERR_DTYPE, dict(dtype=2)), (dc.DC_ERR_DTYPE, dict(wtype=-1)),
+                         (dc.DC_ERR_ARG, dict(hold=3)), (dc.DC_ERR_ARG, dict(hold=-1)),
                          (dc.DC_ERR_ARG, dict(lr=float("nan"))), (dc.DC_ERR_ARG, dict(mu=float("inf"))),
                          (dc.DC_ERR_ARG, dict(wd=float("nan"))), (dc.DC_ERR_ARG, dict(nest=2)),
                          (dc.DC_ERR_ARG, dict(mode=3)), (dc.DC_ERR_ARG, dict(steps=0)),
@@ -126,7 +127,7 @@ def test_update_refusals():
 ])
 def test_diverging_steps_are_refused(co):
     m = mats((3, 4))
-    expect(dc.DC_ERR_ARG, dc.dc_orthogonalize, 0, m, 1, len(co), co, 1e-7, at(20), BIG, 0)
+    expect(dc.DC_ERR_ARG, dc.dc_orthogonalize, 0, 0, m, 1, len(co), co, 1e-7, at(20), BIG, 0)
 
 
 def test_interleaved_columns_do_not_overlap():
@@ -135,20 +136,26 @@ def test_interleaved_columns_do_not_overlap():
     m = mats((8, 4), (8, 4))
     m["ld_out"] = 8
     m["out"] = at(1), at(1) + 8
-    expect(dc.DC_ERR_SHAPE, dc.dc_orthogonalize, 0, m, 2, 5, COEFFS, 1e-7, at(20), 16, 0)
+    expect(dc.DC_ERR_SHAPE, dc.dc_orthogonalize, 0, 0, m, 2, 5, COEFFS, 1e-7, at(20), 16, 0)
     m["out"][1] = at(1) + 6
-    expect(dc.DC_ERR_ARG, dc.dc_orthogonalize, 0, m, 2, 5, COEFFS, 1e-7, at(20), 16, 0)
+    expect(dc.DC_ERR_ARG, dc.dc_orthogonalize, 0, 0, m, 2, 5, COEFFS, 1e-7, at(20), 16, 0)
     m["out"][1] = at(1) + 10      # wraps into the next row's first column
-    expect(dc.DC_ERR_ARG, dc.dc_orthogonalize, 0, m, 2, 5, COEFFS, 1e-7, at(20), 16, 0)
+    expect(dc.DC_ERR_ARG, dc.dc_orthogonalize, 0, 0, m, 2, 5, COEFFS, 1e-7, at(20), 16, 0)
 
 
 def test_workspaces():
-    assert dc.dc_orthogonalize_workspace(0, mats(), 0) == 0
-    one = dc.dc_orthogonalize_workspace(0, mats((100, 300)), 1)
-    assert one >= 2 * (2 * 100 * 300 + 2 * 100 * 100)
-    assert dc.dc_orthogonalize_workspace(1, mats((100, 300)), 1) > one
-    many = np.concatenate([mats((100, 300))] * 1000)     # chunks reuse the workspace
-    assert dc.dc_orthogonalize_workspace(0, many, 1000) < 100 * one
+    assert dc.dc_orthogonalize_workspace(0, 0, 0, mats(), 0) == 0
+    one = dc.dc_orthogonalize_workspace(0, 0, 0, mats((400, 300)), 1)
+    assert one >= 2 * (2 * 400 * 300 + 2 * 300 * 300)
+    pair = dc.dc_orthogonalize_workspace(1, 1, 0, mats((400, 300)), 1)
+    assert pair > one and pair == dc.dc_orthogonalize_workspace(0, 1, 0, mats((400, 300)), 1)
+    assert pair == dc.dc_orthogonalize_workspace(0, 0, 2, mats((400, 300)), 1)
+    assert one == dc.dc_orthogonalize_workspace(1, 1, 1, mats((400, 300)), 1)
+    for bad in ((2, 0, 0), (0, 2, 0), (0, 0, 3)):
+        with pytest.raises(dc.DCError):
+            dc.dc_orthogonalize_workspace(*bad, mats((400, 300)), 1)
+    many = np.concatenate([mats((400, 300))] * 1000)     # chunks reuse the workspace
+    assert dc.dc_orthogonalize_workspace(0, 0, 0, many, 1000) < 200 * one
     assert dc.dc_linear_workspace(0, 8192, 8192, 64) == 0
     for T, N, K in [(1, 1, 1), (64, 64, 100000), (7, 300, 5000)]:
         assert dc.dc_linear_workspace(1, T, N, K) % 16 == 0
@@ -189,6 +196,8 @@ def test_python_refusals():
         muon.orthogonalize(g)
     with pytest.raises(ValueError):
         muon.orthogonalize([g, g.bfloat16()])
+    with pytest.raises(ValueError):
+        muon.orthogonalize(g, hold="two")
     with pytest.raises(ValueError):
         muon.orthogonalize(g, coeffs=[(1, 0, 0)])              # one triple for five steps
     with pytest.raises(ValueError):
