@@ -16,17 +16,22 @@ namespace {
 // rounded division the elementwise backward was bound by its arithmetic (129
 // us on 8192 x 11008 bf16 where its bytes take 84).
 
-// exp(x), x <= 88 taken: 2^(x log2 e) with what the product rounds off.
+// exp(x), x taken into [-150, 88] (zero from -104 on; outside, what the
+// product rounds off would be infinite less infinite): 2^(x log2 e) with what
+// the product rounds off.
 __device__ __forceinline__ float exp_fast(float x) {
-  x = fminf(x, 88.f);
+  x = __builtin_amdgcn_fmed3f(x, -150.f, 88.f);
   const float t = x * 1.44269504f;
   const float r = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e, r * 0.693147181f, e);
 }
 
-// 1 / (1 + exp(-v)).
-__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + exp_fast(-v)); }
+// 1 / (1 + exp(-v)); under -87 zero, so that a v of any size times it is
+// within 2e-36 of its limit.
+__device__ __forceinline__ float sigmoid(float v) {
+  return v < -87.f ? 0.f : __builtin_amdgcn_rcpf(1.f + exp_fast(-v));
+}
 
 // Phi(v), the normal distribution's, and e = exp(-v^2 / 2).  With z = |v| /
 // sqrt 2 and t = 1 / (1 + z / 2), erfc(z) exp(z^2) / t is a smooth function of
@@ -317,6 +322,9 @@ __global__ void __launch_bounds__(512) k_linear_few(const T* x, int64_t ld_x, co
 
 constexpr int64_t kFewRows = 64;
 
+// (A grid holds 2^32 threads; 2^26 outputs take 2^31.)
+bool is_few(int64_t rows, int64_t n) { return rows <= kFewRows && n <= ((int64_t)1 << 26); }
+
 template <class T, bool DIRECT, class Epi>
 hipError_t few_rows(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int64_t rows, int64_t n, int64_t k,
                     const Epi& epi, hipStream_t stream) {
@@ -465,7 +473,7 @@ hipError_t bias_act(int32_t dtype, int64_t rows, int64_t n, const void* dy, int6
 }  // namespace
 
 int64_t linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K) {
-  if (T <= kFewRows) return 0;
+  if (is_few(T, N)) return 0;
   return cut(dtype, T, N, K).partial_bytes(T);
 }
 
@@ -481,7 +489,7 @@ int64_t bias_act_workspace(int32_t dtype, int64_t T, int64_t N) {
 hipError_t launch_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x, const void* w,
                          int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  if (T <= kFewRows) {
+  if (is_few(T, N)) {
     auto few = [&](auto type) {
       using E = decltype(type);
       const LinearEpilogue<E> epi{o, N};

@@ -258,6 +258,44 @@ def test_gradients_match_differences(act):
             assert abs(got.cpu().view(-1)[i].item() - d.item()) < (1e-7 + 2.0 ** -18) * size
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_values_of_any_size(rows, act, kind):
+    """Activations and slopes where exp(-v), exp(-v^2 / 2) or v^2 leave fp32's
+    range.  Those values are exact: v or 0, and slopes 1 or 0 (within 1e-35 from
+    |v| = 100 on); infinity gives infinity, NaN NaN."""
+    t = T()
+    sizes = t.tensor([100.0, 2.0 ** 10, 2.0 ** 40, 2.0 ** 63, 2.0 ** 64, 2.0 ** 65, 2.0 ** 100, 2.0 ** 127, 3.3e38],
+                     dtype=t.float32)
+    v = t.cat([sizes, -sizes]).to(dt(kind))
+    n = v.numel()
+    x = t.ones(rows, 1, dtype=dt(kind), device="cuda")
+    y = linear.forward(x, v.view(n, 1).cuda(), act=act)
+    want = t.where(v > 0, v, t.zeros_like(v)).double().expand(rows, n)
+    assert (host(y)[0] - want).abs().max() <= 1e-35
+    pre = v.expand(rows, n).contiguous().cuda()
+    dz, _ = linear.bias_act_backward(t.ones_like(pre), pre, act=act)
+    assert (host(dz)[0] - (v > 0).double().expand(rows, n)).abs().max() <= 1e-35
+    odd = t.tensor([[float("inf")], [float("nan")]], dtype=dt(kind), device="cuda")
+    y = host(linear.forward(x, odd, act=act))[0]
+    assert (y[:, 0] == float("inf")).all() and y[:, 1].isnan().all()
+
+
+def test_few_rows_of_many_outputs():
+    """More outputs than the few-row kernel's grid takes: small whole numbers,
+    so the sums are exact in any order."""
+    t = T()
+    n, k = 2 ** 26 + 24, 8
+    w = t.randint(-4, 5, (n, k), dtype=t.int8, device="cuda").bfloat16()
+    x = t.randint(-4, 5, (2, k), dtype=t.int8, device="cuda").bfloat16()
+    y = linear.forward(x, w)
+    for at in range(0, n, 2 ** 24):
+        part = w[at:at + 2 ** 24].float()
+        for i in range(2):
+            assert t.equal(y[i, at:at + 2 ** 24].float(), (part * x[i].float()).sum(1))
+
+
 def layer(t, gen, rows, n, k, kind):
     h = dt(kind)
     return (randn(gen, rows, k, dtype=h), randn(gen, n, k, scale=k ** -0.5, dtype=h), randn(gen, n, dtype=h),
