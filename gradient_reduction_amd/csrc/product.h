@@ -124,6 +124,10 @@ struct StageMap {
 // Loads through registers: any address and any size.  A chunk wholly inside
 // is one 16-byte load (unaligned where the operand is); one that crosses the
 // operand's end is read value by value, and what is outside counts as zero.
+// A whole stage is loaded with no condition for each chunk: rows (columns, of
+// a KS operand) outside only make sums that nobody writes, so they get the
+// values of a row inside, and a KS chunk across a row's end takes in the next
+// row's beginning, which exists in all stages but the last.
 template <class T, int ROWS, bool KC, int NT>
 struct RegisterLoader {
   using Map = StageMap<T, ROWS, KC>;
@@ -132,6 +136,18 @@ struct RegisterLoader {
   u32x4 v[kPer];
 
   __device__ void load(const Operand<T>& op, int64_t k0, int64_t k_end, int tid) {
+    if (KC ? k0 + Map::BK <= k_end : k0 + Map::BK < k_end && op.ld >= Map::EPC) {
+      const T* base = op.p + (KC ? k0 : k0 * op.ld);
+#pragma unroll
+      for (int s = 0; s < kPer; ++s) {
+        const int c = s * NT + tid;
+        const int line = c / Map::CPR, chunk = (c % Map::CPR) ^ Map::swizzle(line);
+        const int row = KC && line >= op.rows ? 0 : line;
+        const int at = !KC && chunk * Map::EPC >= op.rows ? 0 : chunk * Map::EPC;
+        __builtin_memcpy(&v[s], base + row * op.ld + at, 16);
+      }
+      return;
+    }
 #pragma unroll
     for (int s = 0; s < kPer; ++s) {
       const int c = s * NT + tid;
