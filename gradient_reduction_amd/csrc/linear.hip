@@ -124,6 +124,14 @@ struct ProductArgs {
   int64_t ld_partial;
 };
 
+// One tile of C = A B (product.h) and its epilogue; y = x wT, dx = dz w and dw
+// = dzT x are its three kinds.  Bound by the matrix cores where the tiles fill
+// the chip: 8192 x 11008 over 4096 bf16 takes 690 us with silu and pre kept
+// (1.07 PFLOP/s), dx 585 (1.26) and dw added to fp32 about 695 (1.06: 688 tiles
+// of 256 are 2.7 rounds over the units, paid as 3).  Tiles are walked in bands
+// of eight rows, one XCD's workgroups on neighbours, so that an L2 serves what
+// they share.  Odd fp32 rows go through registers: 777 x 1003 over 515 takes
+// 23 us, bound by the latency of a tile's 17 stages.
 template <class T, int BM, int BN, int WM, int WN, bool KCA, bool KCB, int S, class Epi>
 __global__ void __launch_bounds__(WM * WN * 64) k_product(ProductArgs g, Epi epi) {
   using P = TileProduct<T, BM, BN, WM, WN, KCA, KCB, S>;
@@ -344,9 +352,10 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 // dz = dy act'(pre) and the column sums of dz, in strips of `strip` rows: one
 // workgroup per 64 chunks of 16 bytes of columns and strip, a wave to a row
 // and two rows in flight per wave.  dy and pre are read past the caches, dz
-// is left in them for the products that read it next (8192 x 11008 bf16: 103
-// us so, 155 us with ordinary loads, 109 us with the stores past them too).
-// Bound by those bytes.  The strips' sums go to partial[strip][n] and are added in order by
+// is left in them for the products that read it next (8192 x 11008 bf16 when it
+// was chosen: 103 us so, 155 us with ordinary loads, 109 us with the stores past
+// them too).  Bound by those bytes: 541 MB in 109 us, 5.0 TB/s, with silu.  The
+// strips' sums go to partial[strip][n] and are added in order by
 // k_column_join, or straight to db when there is one strip.
 template <class T, class G, int ACT>
 __global__ void __launch_bounds__(256) k_bias_act(int64_t rows, int64_t n, const T* dy, int64_t ld_dy, const T* pre,
@@ -420,6 +429,8 @@ __global__ void __launch_bounds__(256) k_bias_act(int64_t rows, int64_t n, const
   }
 }
 
+// db from the strips' sums, eight lanes to a column, in a fixed order.  A few
+// hundred KB: bound by latency, 3 to 5 us.
 template <class G>
 __global__ void __launch_bounds__(256) k_column_join(const float* partial, int32_t strips, int64_t n, G* db,
                                                      int accumulate) {

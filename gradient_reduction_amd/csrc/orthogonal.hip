@@ -118,7 +118,8 @@ struct NsUpdate {
 };
 
 // |U|_F^2 in parts, in fp64 (fp32 gradients of 1e-30 and 1e30 both have a
-// square there), and the momentum's step: m <- mu m + g.
+// square there), and the momentum's step: m <- mu m + g.  Bound by its bytes:
+// 100 M elements of bf16 gradients and fp32 momenta, 1 GB, take 190 us.
 template <class G, bool MOM>
 __global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsUpdate up, double* parts) {
   const int e = find_matrix(tiles, tab.count, (int32_t)blockIdx.x);
@@ -174,7 +175,8 @@ __device__ __forceinline__ void store_held(Held* p, int64_t at, int64_t size, V 
 }
 
 // X = U scale / (|U|_F + eps), transposed where rows > cols, 64 x 64 at a
-// time; columns n .. ldx - 1 of X are zero.
+// time; columns n .. ldx - 1 of X are zero.  Bound by its bytes: the same 100 M
+// elements into pairs, 1 GB, take 214 us.
 template <int P, class G, bool MOM>
 __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsUpdate up, const double* parts,
                                                  float eps, float scale, Held* planes) {
@@ -265,7 +267,11 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
 }
 
 // A = alpha X XT (POLY false: src = X, dst = A), or B = alpha (beta A + A A)
-// (POLY true: src = A, dst = B; A is its own transpose).
+// (POLY true: src = A, dst = B; A is its own transpose).  Bound by the matrix
+// cores: the four 4096 x 4096 and three 4096 x 11008 matrices of a 7B layer take
+// 787 us for A and 484 us for B, 1.12 and 1.05 PFLOP/s of the tiles that are
+// computed, half of the whole product; 952 tiles of 256 are 3.7 rounds.  One
+// 1024 x 1024 matrix takes 10 us each, a tile's latency.
 template <int P, int BT, int WM, int WN, int S, bool POLY>
 __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsTiles tiles, Held* planes, int32_t next,
                                                                float alpha, float beta) {
@@ -304,6 +310,9 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
 }
 
 // X <- beta (a X + B X) into the other X plane, or out of it in the last step.
+// The same 7B layer takes 1528 us, 1.09 PFLOP/s; 48 matrices of 1024 x 1024 to
+// 4096 x 1024 in pairs 623 us, 0.99 (a tile's beginning and end are a fifth of
+// its 48 stages), their last step with the weights 795 us.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
 template <int P, class O, int BT, int WM, int WN, int S, int LAST, class Table>

@@ -81,6 +81,7 @@ class Zero1FlushExecutor:
         raw = torch.from_numpy(allt.view(np.uint8).copy())
         self.d_tasks = raw.to(dev) if len(allt) else torch.empty(32, dtype=torch.uint8, device=dev)
         self.h_owner: Optional[np.ndarray] = None
+        self.m_recs: Optional[np.ndarray] = None    # register_matrices()
         self.d_tiles = None        # flush plans (plan()), one table for all buckets
         self.tile_begin = None
         self.root_tiles = None
@@ -436,9 +437,21 @@ class Zero1FlushExecutor:
         muon.update()."""
         from . import linear, muon
         held, mode = muon._choice("hold", hold, muon.HOLDS), muon._choice("scale", scale, muon.SCALES)
+        if self.m_recs is None:
+            raise RuntimeError("muon_update() before register_matrices()")
+        muon._check_lr_scale(lr_scale, self.d_owner.device)
         eb = 2 if self.dtype == dc.DC_BF16 else 4
-        base = slab_out if isinstance(slab_out, int) else slab_out.data_ptr()
         recs = self.m_recs.copy()
+        base = slab_out
+        if not isinstance(slab_out, int):
+            base = slab_out.data_ptr()
+            sizes = recs["rows"].astype(np.int64) * recs["cols"]
+            ends = self.m_rows * ld_out + self.m_cols + sizes
+            have = slab_out.untyped_storage().nbytes() // eb - slab_out.storage_offset()
+            if slab_out.element_size() != eb or slab_out.device != self.d_owner.device or \
+                    (len(recs) and int(ends.max()) > have):
+                raise ValueError(f"slab_out {tuple(slab_out.shape)} of {slab_out.dtype} on {slab_out.device} "
+                                 f"with ld_out={ld_out} does not hold every matrix")
         recs["grad"] = base + (self.m_rows * ld_out + self.m_cols) * eb
         table = muon._steps(steps, muon.COEFFS if coeffs is None else coeffs)
         with linear.on(self.d_owner.device, stream):

@@ -165,12 +165,7 @@ def backward(dy, x, w, pre=None, act="none", dw=None, db=None, accumulate=False,
     if accumulate and need_dw and dw is None:
         raise ValueError("accumulate needs dw")
     with on(dev, stream):
-        if act != "none" or db is not None:
-            dz, db = bias_act_backward(dy, pre, act, db=db, accumulate=accumulate and db is not None)
-        else:
-            dz = dy
-        dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
-        dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
+        # a call that is refused for its dw leaves db as it was
         ld_dw, dw_type = 0, dc.DC_F32
         if need_dw:
             if dw is None:
@@ -181,6 +176,12 @@ def backward(dy, x, w, pre=None, act="none", dw=None, db=None, accumulate=False,
             dw_type = dtype_of(dw)
         else:
             dw = None
+        if act != "none" or db is not None:
+            dz, db = bias_act_backward(dy, pre, act, db=db, accumulate=accumulate and db is not None)
+        else:
+            dz = dy
+        dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
+        dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
         if (need_dx and T) or need_dw:
             nbytes = dc.dc_linear_backward_workspace(dtype, T, N, K)
             dc.dc_linear_backward(dtype, T, N, K, dz, ld_dz, w, ld_w, x, ld_x, dx, K, dw_type, dw, ld_dw,

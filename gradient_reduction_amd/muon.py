@@ -83,6 +83,13 @@ def _alike(name, ts, dtype, device):
             raise ValueError(f"{name} {k} is {t.dtype} on {t.device}, expected {dtype} on {device}")
 
 
+def _check_lr_scale(t, device):
+    if t is not None:
+        _alike("lr_scale", [t], torch.float32, device)
+        if t.numel() != 1:
+            raise ValueError(f"lr_scale of {t.numel()} elements, one is needed")
+
+
 def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, hold="auto", out=None, stream=None):
     """Every matrix orthogonalised, in the gradients' dtype: a list of new
     tensors, or `out` (which may be the gradients).  `grads`: a list of
@@ -135,10 +142,7 @@ def update(weights, grads, momentum, lr, mu=0.95, nesterov=True, weight_decay=0.
     _alike("gradient", gs, gs[0].dtype, dev)
     _alike("weight", ws, ws[0].dtype, dev)
     _alike("momentum", ms, torch.float32, dev)
-    if lr_scale is not None:
-        _alike("lr_scale", [lr_scale], torch.float32, dev)
-        if lr_scale.numel() != 1:
-            raise ValueError(f"lr_scale of {lr_scale.numel()} elements, one is needed")
+    _check_lr_scale(lr_scale, dev)
     mats = matrices(gs, ws, ms)
     with on(dev, stream):
         nbytes = dc.dc_orthogonalize_workspace(dtype, wtype, held, mats, len(mats))

@@ -421,3 +421,13 @@ def test_layers_into_the_deferred_reduction():
         bound = (2 * rows + 16) * STEP * size
         inside("reduced", out[0, :M], want, bound)
         inside("slabs", other[0, :M], want, bound)
+
+
+def test_refused_backward_leaves_db():
+    t = T()
+    dy, x, w = (t.ones(s, device="cuda") for s in ((4, 5), (4, 6), (5, 6)))
+    for dw in (t.zeros(5, 7, device="cuda"), t.zeros(5, 6), t.zeros(5, 6, device="cuda").double()):
+        db = t.zeros(5, device="cuda")
+        with pytest.raises(ValueError):
+            linear.backward(dy, x, w, dw=dw, db=db, accumulate=True)
+        assert not db.any()

@@ -351,3 +351,26 @@ def test_flush_then_owners_update(owners, dtype):
         ex.register_matrices({1: t.zeros(7, 12, device="cuda")}, {1: t.zeros(7, 12, device="cuda")})
     with pytest.raises(ValueError):
         ex.register_matrices(weights, {})
+
+
+def test_owners_update_refusals():
+    """Refused on the host: an update of nothing, a slab that does not hold
+    every matrix, a rate that is not one element."""
+    t = T()
+    w = wl.custom_flush("update", 2, wl.DT_F32, [12 * 8, 77], capacity=9000, pre_div=1, value_seed=3)
+    slab = t.zeros(w.W, w.ld, device="cuda")
+    ex = executor.from_workload(w, reduce_to_owner=True)
+    ex.build_owner_map()
+    with pytest.raises(RuntimeError):
+        ex.muon_update(slab, w.ld, lr=0.02)
+    weights, momenta = {0: t.ones(12, 8, device="cuda")}, {0: t.ones(12, 8, device="cuda")}
+    ex.register_matrices(weights, momenta)
+    for bad in (slab.bfloat16(), slab.cpu(), slab[:, :50].contiguous()[:1]):
+        with pytest.raises(ValueError):
+            ex.muon_update(bad, w.ld, lr=0.02)
+    for rate in (t.ones(2, device="cuda"), t.ones(1), t.ones(1, device="cuda").double()):
+        with pytest.raises(ValueError):
+            ex.muon_update(slab, w.ld, lr=0.02, lr_scale=rate)
+        with pytest.raises(ValueError):
+            muon.update(weights[0], slab[0, :96].view(12, 8), momenta[0], lr=0.02, lr_scale=rate)
+    assert bool((weights[0] == 1).all()) and bool((momenta[0] == 1).all())
