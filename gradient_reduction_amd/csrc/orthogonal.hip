@@ -163,9 +163,19 @@ __global__ void __launch_bounds__(256) k_ns_norm(NsTable tab, NsTiles tiles, NsU
 }
 
 // N held values at `at` of a plane; the second plane of a pair lies `size`
-// values on.
+// values on.  v is settled first: a multiplication that made it is otherwise
+// folded into one of its two conversions (v_fma_mixlo_f16 rounds the product
+// once, v_cvt_pk_f16_f32 the product's fp32), and the low half then belongs to
+// another high half than the stored one.  That left up to 6e-5 of |O|_F
+// instead of 1e-6.
 template <int P, int N, class V>
 __device__ __forceinline__ void store_held(Held* p, int64_t at, int64_t size, V v) {
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    float settled = v[t];
+    asm("" : "+v"(settled));
+    v[t] = settled;
+  }
   store_n<N>(p + at, v, N);
   if constexpr (P == 2) {
 #pragma unroll

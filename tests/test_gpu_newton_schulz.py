@@ -1,0 +1,42 @@
+"""Orthogonalised matrices and updates on the GPU, held to the bounds of
+newton_schulz_model (which zeros, -O, a step less or a lost low half break:
+tests/test_newton_schulz_bounds.py)."""
+import pytest
+import torch
+
+from gradient_reduction_amd import dc, muon
+from tests import newton_schulz_model as ns
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    dc.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def dt(name):
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def close(name, got, u, hold, coeffs=ns.COEFFS, eps=1e-7):
+    got = got.cpu()
+    assert bool(torch.isfinite(got).all()), f"{name}: not finite"
+    off = ns.beyond(got, ns.exact(u, coeffs, eps), torch.finfo(got.dtype).eps / 2)
+    most = 1.01 * ns.bound(hold, tuple(u.shape))
+    assert off <= most, f"{name}: off by {off:.3g} |O| beyond the output's rounding, bound {most:.3g}"
+
+
+@pytest.mark.parametrize("shape", [(768, 130), (1024, 1024)], ids=str)
+def test_halves_are_of_one_number(shape):
+    """Ten matrices held in pairs: a low half that belongs to another rounding
+    than the stored high half shows in some of them."""
+    us = torch.stack([ns.gradient(torch.Generator().manual_seed(s), *shape, dtype=torch.float32)
+                      for s in range(10)])
+    got = muon.orthogonalize(us.cuda(), hold="pair")
+    off = [ns.beyond(g, ns.exact(u, ns.COEFFS, 1e-7), 2.0 ** -24) for g, u in zip(got.cpu(), us)]
+    print("beyond the output's rounding, |O|:", " ".join(f"{v:.2g}" for v in off), flush=True)
+    assert max(off) <= 1.01 * ns.PAIR_BOUND
