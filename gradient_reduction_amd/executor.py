@@ -431,7 +431,7 @@ class Zero1FlushExecutor:
 
     def muon_update(self, slab_out, ld_out: int, lr: float, mu: float = 0.95, nesterov: bool = True,
                     weight_decay: float = 0.0, scale: str = "rms", steps: int = 5, coeffs=None,
-                    eps: float = 1e-7, hold: str = "auto", lr_scale=None, stream=None) -> None:
+                    eps: float = 1e-7, hold: str = "pair", lr_scale=None, stream=None) -> None:
         """Steps the registered matrices from the flushed slab (after flush()
         of every bucket into slab_out, on the same stream); arguments as in
         muon.update()."""

@@ -90,13 +90,13 @@ def _check_lr_scale(t, device):
             raise ValueError(f"lr_scale of {t.numel()} elements, one is needed")
 
 
-def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, hold="auto", out=None, stream=None):
+def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, hold="pair", out=None, stream=None):
     """Every matrix orthogonalised, in the gradients' dtype: a list of new
     tensors, or `out` (which may be the gradients).  `grads`: a list of
-    tensors, or one (then one comes back).  hold: "one" fp16 for each value of
-    the steps (1.5e-3 of the result on large matrices), a "pair" (5e-7, three
-    times the products), or "auto": pairs for float32 and for smaller sides
-    under 256."""
+    tensors, or one (then one comes back).  hold: a "pair" of fp16 for each
+    value of the steps (about 1e-6 of the result), "one" (1.5e-3 on large
+    matrices, a third of the products), or "auto": pairs for float32 and for
+    smaller sides under 256, else one."""
     held = _choice("hold", hold, HOLDS)
     one = torch.is_tensor(grads)
     gs = [grads] if one else list(grads)
@@ -120,7 +120,7 @@ def orthogonalize(grads, steps=5, coeffs=COEFFS, eps=1e-7, hold="auto", out=None
 
 
 def update(weights, grads, momentum, lr, mu=0.95, nesterov=True, weight_decay=0.0, scale="rms", steps=5,
-           coeffs=COEFFS, eps=1e-7, hold="auto", lr_scale=None, stream=None):
+           coeffs=COEFFS, eps=1e-7, hold="pair", lr_scale=None, stream=None):
     """One step of the weights and momenta, in place:
       m <- mu m + g;  u = mu m + g (nesterov) or m
       w <- (1 - l weight_decay) w - l s orthogonalize(u)

@@ -40,3 +40,17 @@ def test_halves_are_of_one_number(shape):
     off = [ns.beyond(g, ns.exact(u, ns.COEFFS, 1e-7), 2.0 ** -24) for g, u in zip(got.cpu(), us)]
     print("beyond the output's rounding, |O|:", " ".join(f"{v:.2g}" for v in off), flush=True)
     assert max(off) <= 1.01 * ns.PAIR_BOUND
+
+
+@pytest.mark.parametrize("shape", [(300, 260), (257, 1025), (1024, 1024)], ids=str)
+def test_fewer_bits_are_the_callers_choice(shape):
+    """A caller who says nothing gets pairs: on bf16 matrices too, nothing is
+    lost beyond the output's own rounding."""
+    u = ns.gradient(torch.Generator().manual_seed(3), *shape, dtype=torch.bfloat16)
+    close("orthogonalize", muon.orthogonalize(u.cuda()), u, "pair")
+    close("one", muon.orthogonalize(u.cuda(), hold="one"), u, "one")
+    w = torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")
+    m = torch.zeros(*shape, device="cuda")
+    # from zero weights and momenta, w = -O
+    muon.update(w, u.cuda(), m, lr=1.0, mu=0.0, nesterov=False, scale="none")
+    close("update", -w, u, "pair")
