@@ -409,8 +409,9 @@ class Zero1FlushExecutor:
         kinds = {w.dtype for w in weights.values()}
         if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
             raise ValueError(f"weights are {sorted(map(str, kinds))}: all bfloat16 or all float32 are needed")
+        # a refused call leaves the registration before it as it was
         recs = np.zeros(len(weights), dc.MATRIX_DTYPE)
-        self.m_rows, self.m_cols = np.zeros(len(weights), np.int64), np.zeros(len(weights), np.int64)
+        rows, cols = np.zeros(len(weights), np.int64), np.zeros(len(weights), np.int64)
         for k, p in enumerate(sorted(weights)):
             w, m = weights[p], momenta[p]
             if p not in place or len(place[p]) != 1 or place[p][0][2] != 0:
@@ -424,8 +425,8 @@ class Zero1FlushExecutor:
                 raise ValueError(f"param {p} is not on {self.d_owner.device}")
             recs[k] = (0, w.data_ptr(), m.data_ptr(), w.shape[1], w.shape[1], w.shape[0], w.shape[1])
             owner = int(self.h_owner[p]) if self.reduce_to_owner else -1
-            self.m_rows[k], self.m_cols[k] = max(owner, 0), col
-        self.m_recs = recs
+            rows[k], cols[k] = max(owner, 0), col
+        self.m_recs, self.m_rows, self.m_cols = recs, rows, cols
         self.m_wtype = dc.DC_F32 if torch.float32 in kinds else dc.DC_BF16
         self.m_keep = (dict(weights), dict(momenta))
 

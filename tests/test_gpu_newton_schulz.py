@@ -4,7 +4,8 @@ tests/test_newton_schulz_bounds.py)."""
 import pytest
 import torch
 
-from gradient_reduction_amd import dc, muon
+from gradient_reduction_amd import dc, executor, muon
+from synth import workloads as wl
 from tests import newton_schulz_model as ns
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +55,29 @@ def test_fewer_bits_are_the_callers_choice(shape):
     # from zero weights and momenta, w = -O
     muon.update(w, u.cuda(), m, lr=1.0, mu=0.0, nesterov=False, scale="none")
     close("update", -w, u, "pair")
+
+
+def test_update_after_a_refused_registration():
+    """The executor's update after a registration that was refused steps the
+    matrices that were registered before, from their own gradients."""
+    sizes = [(40, 30), (64, 64), (7, 200)]
+    w = wl.custom_flush("update", 4, wl.DT_F32, [a * b for a, b in sizes], capacity=9000, pre_div=1, value_seed=3)
+    gen = torch.Generator().manual_seed(12)
+    slab = (torch.randn(w.W, w.ld, generator=gen) * 1e-3).cuda()
+    out = torch.zeros_like(slab)
+    ex = executor.from_workload(w, reduce_to_owner=True)
+    ex.build_owner_map()
+    weights = {p: torch.zeros(*s, device="cuda") for p, s in enumerate(sizes)}
+    ex.register_matrices(weights, {p: torch.zeros_like(v) for p, v in weights.items()})
+    with pytest.raises(ValueError):
+        ex.register_matrices({0: torch.zeros(40, 31, device="cuda")}, {0: torch.zeros(40, 31, device="cuda")})
+    for b in range(len(w.buckets)):
+        ex.flush(b, slab, w.ld, out, w.ld)
+    ex.muon_update(out, w.ld, lr=1.0, mu=0.0, nesterov=False, scale="none")
+    for bk in w.buckets:
+        for t in bk.tasks:
+            u = slab[:, bk.col + t.offset:bk.col + t.offset + t.numel].cpu().double().mean(0)
+            # the flushed fp32 sum of four rows is off by 3 roundings of 2^-24 at
+            # most, which the steps' slopes (10 on the average) make 2e-6
+            want = ns.exact(u.view(*sizes[t.param]), ns.COEFFS, 1e-7)
+            assert ns.error(-weights[t.param].cpu().double(), want) <= ns.PAIR_BOUND + 2e-6 + 2.0 ** -24
