@@ -81,6 +81,7 @@ class Zero1FlushExecutor:
         raw = torch.from_numpy(allt.view(np.uint8).copy())
         self.d_tasks = raw.to(dev) if len(allt) else torch.empty(32, dtype=torch.uint8, device=dev)
         self.h_owner: Optional[np.ndarray] = None
+        self.map_built = False
         self.m_recs: Optional[np.ndarray] = None    # register_matrices()
         self.d_tiles = None        # flush plans (plan()), one table for all buckets
         self.tile_begin = None
@@ -99,6 +100,7 @@ class Zero1FlushExecutor:
         dc.dc_build_owner_map(self.W, self.P, self.d_pid_off, self.d_pids, self.pids_capacity,
                               self.G, self.group_begin, self.group_comm_size,
                               self.group_rank_to_global, self.d_owner, self.d_counts, stream)
+        self.map_built = True
         if self.zero2:
             dc.dc_param_part_size(self.W, self.P, self.G, self.group_begin, self.group_comm_size,
                                   self.group_rank_to_global, self.d_part_size, self.d_psize,
@@ -394,7 +396,8 @@ class Zero1FlushExecutor:
         needs its whole reduced gradient in one row: the owner's, or row 0
         where it is AllReduced (every row has it).  ZeRO-2 spreads a param
         over rows and a sub-communicator's blocks hold different sums, so
-        both are refused.  Synchronizes (the owner map is read back)."""
+        both are refused.  Comes after build_owner_map, and synchronizes (the
+        owner map is read back)."""
         torch = self.torch
         if self.zero2:
             raise ValueError("register_matrices: ZeRO-2 leaves no row with a whole parameter")
@@ -404,7 +407,9 @@ class Zero1FlushExecutor:
         for bk in self.buckets:
             for off, numel, param, comm in bk.tasks:
                 place.setdefault(param, []).append((bk.col + off, numel, comm))
-        if self.h_owner is None:
+        if self.reduce_to_owner and self.h_owner is None:
+            if not self.map_built:
+                raise RuntimeError("register_matrices() before build_owner_map()")
             self.fetch_metadata()
         kinds = {w.dtype for w in weights.values()}
         if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:

@@ -66,3 +66,25 @@ def test_a_new_registration_replaces_the_old(launched):
     ex.register_matrices(*tensors())
     ex.register_matrices(*tensors([2]))
     assert elements(ex, slab, w.ld, launched) == [place[2]]
+
+
+def test_registration_needs_the_owner_map(monkeypatch):
+    """Before build_owner_map the device map holds nothing: reading it would
+    take any row for the owner's."""
+    w, ex, place = made()
+    ex.h_owner = None
+    with pytest.raises(RuntimeError, match="build_owner_map"):
+        ex.register_matrices(*tensors())
+    assert ex.h_owner is None and ex.m_recs is None
+    # with the map built (its launches replaced), it is read back
+    monkeypatch.setattr(dc, "dc_partition_ids", lambda *a: None)
+    monkeypatch.setattr(dc, "dc_build_owner_map", lambda *a: None)
+    ex.build_owner_map()
+    ex.d_owner.copy_(torch.tensor([1, -1, 0]))
+    ex.d_pid_off.zero_()
+    ex.register_matrices(*tensors())
+    assert ex.m_rows.tolist() == [1, 0]
+    # every row has an AllReduced gradient: no map is needed
+    ex = executor.from_workload(w, reduce_to_owner=False, device="cpu")
+    ex.register_matrices(*tensors())
+    assert ex.m_rows.tolist() == [0, 0]
