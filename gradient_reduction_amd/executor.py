@@ -449,10 +449,12 @@ class Zero1FlushExecutor:
         eb = 2 if self.dtype == dc.DC_BF16 else 4
         recs = self.m_recs.copy()
         base = slab_out
+        ends = self.m_cols + recs["rows"].astype(np.int64) * recs["cols"]    # in a row
+        if len(recs) and ld_out < int(ends.max()):
+            raise ValueError(f"ld_out={ld_out} is less than a row with every matrix ({int(ends.max())})")
         if not isinstance(slab_out, int):
             base = slab_out.data_ptr()
-            sizes = recs["rows"].astype(np.int64) * recs["cols"]
-            ends = self.m_rows * ld_out + self.m_cols + sizes
+            ends = self.m_rows * ld_out + ends
             have = slab_out.untyped_storage().nbytes() // eb - slab_out.storage_offset()
             if slab_out.element_size() != eb or slab_out.device != self.d_owner.device or \
                     (len(recs) and int(ends.max()) > have):

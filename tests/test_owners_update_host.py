@@ -88,3 +88,20 @@ def test_registration_needs_the_owner_map(monkeypatch):
     ex = executor.from_workload(w, reduce_to_owner=False, device="cpu")
     ex.register_matrices(*tensors())
     assert ex.m_rows.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("as_address", [False, True])
+def test_ld_out_is_a_rows_length(launched, as_address):
+    """A stride under the row's matrices (or a negative one, which reads before
+    the slab) is refused, for a tensor and for an address."""
+    w, ex, place = made()
+    slab = torch.zeros(w.W, w.ld)
+    ex.register_matrices(*tensors())
+    least = max(place[0] + 64, place[2] + 76)
+    where = slab.data_ptr() if as_address else slab
+    for ld in (-w.ld, -1, 0, least - 1):
+        with pytest.raises(ValueError, match="ld_out"):
+            ex.muon_update(where, ld, lr=0.1)
+    assert not launched
+    ex.muon_update(where, least, lr=0.1)
+    assert ((launched["mats"]["grad"] - slab.data_ptr()) // 4).tolist() == [least + place[0], place[2]]
