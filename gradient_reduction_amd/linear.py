@@ -109,12 +109,35 @@ def forward(x, w, bias=None, residual=None, act="none", save_pre=False, out=None
     return out if pre is None else (out, pre)
 
 
-def bias_act_backward(dy, pre=None, act="none", dz=None, db=None, accumulate=False, need_dz=True,
-                      need_db=False, grad_dtype=torch.float32, stream=None):
-    """(dz, db): dz = dy act'(pre) and the bias gradient, its column sums
-    (added to `db` with accumulate).  db is returned when it is given or
-    need_db is set; dz when need_dz is set, and is dy itself without an
-    activation."""
+def _share(a, ld_a, b, ld_b):
+    """Whether two operands (vectors, or matrices with their row strides)
+    share an element; column ranges of rows with one stride may interleave."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    ea, eb, pa, pb = a.element_size(), b.element_size(), a.data_ptr(), b.data_ptr()
+    ca, cb = a.shape[-1] * ea, b.shape[-1] * eb
+    ra, rb = a.numel() // a.shape[-1], b.numel() // b.shape[-1]
+    step = ld_a * ea
+    if pa >= pb + (rb - 1) * ld_b * eb + cb or pb >= pa + (ra - 1) * step + ca:
+        return False
+    if step != ld_b * eb:
+        return True
+    d = (pb - pa) % step
+    return d < ca or d + cb > step
+
+
+def _apart(outs, ins):
+    """Refuses a written operand that shares an element with another one;
+    entries are (name, tensor, row stride)."""
+    for k, (name, o, ld) in enumerate(outs):
+        for other, t, ld_t in outs[:k] + ins:
+            if _share(o, ld, t, ld_t):
+                raise ValueError(f"{name} and {other} overlap")
+
+
+def _bias_act(dy, pre, act, dz, db, accumulate, need_dz, need_db, grad_dtype):
+    """bias_act_backward's checks and allocations, in the caller's on():
+    (dz, db, what launches it)."""
     if dy.dim() != 2:
         raise ValueError(f"dy {tuple(dy.shape)} must be a matrix")
     T, N = dy.shape
@@ -132,21 +155,37 @@ def bias_act_backward(dy, pre=None, act="none", dz=None, db=None, accumulate=Fal
             dz, need_dz = dy, False
     if accumulate and db is None:
         raise ValueError("accumulate needs db")
-    with on(dev, stream):
-        if need_dz and dz is None:
-            dz = torch.empty((T, N), dtype=dt, device=dev)
-        if db is None and need_db:
-            db = torch.empty(N, dtype=grad_dtype, device=dev)
-        if db is not None:
-            _vector("db", db, N, (torch.float32, dt), dev)
-        ld_dz = 0
-        if need_dz:
-            dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
-        if (need_dz and T) or db is not None:
-            nbytes = dc.dc_bias_act_workspace(dtype, T, N) if db is not None else 0
-            dc.dc_bias_act_backward(dtype, T, N, dy, ld_dy, pre, ld_pre, code, dz if need_dz else None,
-                                    ld_dz, dtype_of(db) if db is not None else dc.DC_F32, db,
-                                    1 if accumulate else 0, workspace(nbytes, dev), nbytes)
+    if need_dz and dz is None:
+        dz = torch.empty((T, N), dtype=dt, device=dev)
+    if db is None and need_db:
+        db = torch.empty(N, dtype=grad_dtype, device=dev)
+    if db is not None:
+        _vector("db", db, N, (torch.float32, dt), dev)
+    ld_dz = 0
+    if need_dz:
+        dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
+    if not ((need_dz and T) or db is not None):
+        return dz, db, lambda: None
+    nbytes = dc.dc_bias_act_workspace(dtype, T, N) if db is not None else 0
+    ws = workspace(nbytes, dev)
+
+    def launch():
+        dc.dc_bias_act_backward(dtype, T, N, dy, ld_dy, pre, ld_pre, code, dz if need_dz else None,
+                                ld_dz, dtype_of(db) if db is not None else dc.DC_F32, db,
+                                1 if accumulate else 0, ws, nbytes)
+
+    return dz, db, launch
+
+
+def bias_act_backward(dy, pre=None, act="none", dz=None, db=None, accumulate=False, need_dz=True,
+                      need_db=False, grad_dtype=torch.float32, stream=None):
+    """(dz, db): dz = dy act'(pre) and the bias gradient, its column sums
+    (added to `db` with accumulate).  db is returned when it is given or
+    need_db is set; dz when need_dz is set, and is dy itself without an
+    activation."""
+    with on(dy.device, stream):
+        dz, db, launch = _bias_act(dy, pre, act, dz, db, accumulate, need_dz, need_db, grad_dtype)
+        launch()
     return dz, db
 
 
@@ -154,36 +193,62 @@ def backward(dy, x, w, pre=None, act="none", dw=None, db=None, accumulate=False,
              need_dw=True, grad_dtype=torch.float32, stream=None):
     """(dx, dw, db) of forward() from dy, the gradient of y; the residual's
     gradient is dy.  dw [N, K] and db [N] are float32 or x's dtype; given ones
-    are written, or added to with accumulate; db only when given.  dz = dy
-    act'(pre) is rounded once to x's dtype on its way into the products."""
+    are written, or added to with accumulate; db only when given.  They may
+    share no element with each other or with what is read.  dz = dy act'(pre)
+    is rounded once to x's dtype on its way into the products.  A call that is
+    refused has changed nothing."""
+    with on(x.device, stream):
+        dx, dw, db, launch = _backward(dy, x, w, pre, act, dw, db, accumulate, need_dx, need_dw, grad_dtype)
+        launch()
+    return dx, dw, db
+
+
+def _backward(dy, x, w, pre, act, dw, db, accumulate, need_dx, need_dw, grad_dtype=torch.float32):
+    """backward()'s checks and allocations, in the caller's on(): (dx, dw, db,
+    what launches it).  Nothing is refused after the first launch."""
     T, N, K = _sizes(x, w)
     dt, dev = x.dtype, x.device
     dtype = dtype_of(x)
     x, ld_x = _rows("x", x, T, K, dt, dev)
     w, ld_w = _rows("w", w, N, K, dt, dev)
-    _rows("dy", dy, T, N, dt, dev)
+    dy, ld_dy = _rows("dy", dy, T, N, dt, dev)
     if accumulate and need_dw and dw is None:
         raise ValueError("accumulate needs dw")
-    with on(dev, stream):
-        # a call that is refused for its dw leaves db as it was
-        ld_dw, dw_type = 0, dc.DC_F32
+    ld_dw, dw_type, given = 0, dc.DC_F32, dw is not None and need_dw
+    if need_dw:
+        if dw is None:
+            dw = torch.empty((N, K), dtype=grad_dtype, device=dev)
+        if dw.dtype not in (torch.float32, dt):
+            raise ValueError(f"dw is {dw.dtype}, expected float32 or {dt}")
+        dw, ld_dw = _rows("dw", dw, N, K, dw.dtype, dev)
+        dw_type = dtype_of(dw)
+    else:
+        dw = None
+    elementwise = lambda: None                                           # noqa: E731
+    dz = dy
+    if act != "none" or db is not None:
+        dz, db, elementwise = _bias_act(dy, pre, act, None, db, accumulate and db is not None, True, False,
+                                        grad_dtype)
+    outs = ([("dw", dw, ld_dw)] if given else []) + ([("db", db, N)] if db is not None else [])
+    if outs:
+        ins = [("dy", dy, ld_dy)]
+        if act != "none":
+            ins.append(("pre", pre, pre.stride(0) if T > 1 else N))
         if need_dw:
-            if dw is None:
-                dw = torch.empty((N, K), dtype=grad_dtype, device=dev)
-            if dw.dtype not in (torch.float32, dt):
-                raise ValueError(f"dw is {dw.dtype}, expected float32 or {dt}")
-            dw, ld_dw = _rows("dw", dw, N, K, dw.dtype, dev)
-            dw_type = dtype_of(dw)
-        else:
-            dw = None
-        if act != "none" or db is not None:
-            dz, db = bias_act_backward(dy, pre, act, db=db, accumulate=accumulate and db is not None)
-        else:
-            dz = dy
-        dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
-        dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
-        if (need_dx and T) or need_dw:
-            nbytes = dc.dc_linear_backward_workspace(dtype, T, N, K)
+            ins.append(("x", x, ld_x))
+        if need_dx:
+            ins.append(("w", w, ld_w))
+        _apart(outs, ins)
+    dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
+    dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
+    products = (need_dx and T) or need_dw
+    nbytes = dc.dc_linear_backward_workspace(dtype, T, N, K) if products else 0
+    ws = workspace(nbytes, dev)
+
+    def launch():
+        elementwise()
+        if products:
             dc.dc_linear_backward(dtype, T, N, K, dz, ld_dz, w, ld_w, x, ld_x, dx, K, dw_type, dw, ld_dw,
-                                  1 if accumulate else 0, workspace(nbytes, dev), nbytes)
-    return dx, dw, db
+                                  1 if accumulate else 0, ws, nbytes)
+
+    return dx, dw, db, launch

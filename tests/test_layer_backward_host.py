@@ -1,0 +1,103 @@
+"""What a layer's backward refuses, and when (no GPU): launches are replaced
+by a record of them, and every refusal comes before the first."""
+import contextlib
+
+import pytest
+import torch
+
+from gradient_reduction_amd import dc, linear
+
+T, N, K = 3, 4, 5
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    seen = []
+    monkeypatch.setattr(linear, "on", lambda device, stream: contextlib.nullcontext())
+    for name in ("dc_bias_act_backward", "dc_linear_backward"):
+        monkeypatch.setattr(dc, name, lambda *a, name=name: seen.append(name))
+    return seen
+
+
+def operands():
+    return {"dy": torch.zeros(T, N), "x": torch.zeros(T, K), "w": torch.zeros(N, K), "pre": torch.zeros(T, N)}
+
+
+def call(o, act="gelu", **kw):
+    return linear.backward(o["dy"], o["x"], o["w"], o["pre"], act, accumulate=True, **kw)
+
+
+def inside(t, at, *shape):
+    """A tensor of `shape` over the elements of t's storage from `at` on."""
+    n = 1
+    for s in shape:
+        n *= s
+    return torch.as_strided(t, shape, (shape[-1], 1) if len(shape) == 2 else (1,), at) if n + at <= t.numel() else None
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("name", ["dy", "x", "w", "pre", "dw"])
+def test_a_bias_gradient_over_another_operand(launches, name, act):
+    if (name, act) == ("pre", "none"):
+        return                # not read
+    o = operands()
+    dw = torch.zeros(N, K)
+    over = dw if name == "dw" else o[name]
+    for at in (0, over.numel() - N):
+        with pytest.raises(ValueError, match="db"):
+            call(o, act=act, dw=dw, db=inside(over, at, N))
+        assert not launches
+        if name in ("dy", "w", "pre"):     # without a weight gradient too: then x is not read
+            with pytest.raises(ValueError, match="db"):
+                call(o, act=act, db=inside(over, at, N), need_dw=False)
+            assert not launches
+
+
+@pytest.mark.parametrize("name", ["dy", "x", "w", "pre"])
+def test_a_weight_gradient_over_another_operand(launches, name):
+    flat = torch.zeros(100)
+    o = operands()
+    rows, cols = o[name].shape
+    o[name] = flat[30:30 + rows * cols].view(rows, cols)
+    for at in (30, 30 + rows * cols - 1, 31 - N * K):
+        with pytest.raises(ValueError, match="dw"):
+            call(o, dw=flat[at:at + N * K].view(N, K), db=torch.zeros(N))
+        assert not launches
+    # next to it
+    for at in (30 + rows * cols, 30 - N * K):
+        call(o, dw=flat[at:at + N * K].view(N, K), db=torch.zeros(N))
+    assert launches == ["dc_bias_act_backward", "dc_linear_backward"] * 2
+
+
+def test_interleaved_columns_are_apart(launches):
+    wide = torch.zeros(N, 2 * K + 1)
+    o = operands()
+    o["w"] = wide[:, :K]
+    call(o, dw=wide[:, K:2 * K], db=torch.zeros(N))
+    assert len(launches) == 2
+    with pytest.raises(ValueError, match="dw"):
+        call(o, dw=wide[:, K - 1:2 * K - 1], db=torch.zeros(N))
+    assert len(launches) == 2
+
+
+def test_refusals_of_any_kind_come_first(launches, monkeypatch):
+    o = operands()
+    db, dw = torch.zeros(N), torch.zeros(N, K)
+    for change, kw in [({"pre": None}, {}), ({"pre": torch.zeros(T, N + 1)}, {}), ({"pre": torch.zeros(T + 1, N)}, {}),
+                       ({"dy": torch.zeros(T, N + 1)}, {}), ({"x": torch.zeros(T, 0), "w": torch.zeros(N, 0)}, {}),
+                       ({}, {"db": torch.zeros(N + 1)}), ({}, {"db": torch.zeros(N).double()}),
+                       ({}, {"dw": torch.zeros(N, K).double()}), ({}, {"dw": torch.zeros(K, N)}), ({}, {"act": "tanh"})]:
+        args = {"db": db, "dw": dw, **kw}
+        if "x" in change:
+            args["dw"] = torch.zeros(N, 0)
+        with pytest.raises((ValueError, dc.DCError)):
+            call({**o, **change}, **args)
+        assert not launches, (change, kw)
+
+    def full(*a, **k):
+        raise MemoryError
+
+    monkeypatch.setattr(linear, "workspace", full)       # no memory is left
+    with pytest.raises(MemoryError):
+        call(o, db=db, dw=dw)
+    assert not launches
