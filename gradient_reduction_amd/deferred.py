@@ -66,9 +66,10 @@ class DeferredReducer:
         if bias_offset is not None and bias_offset < offset + n * k and offset < bias_offset + n:
             raise ValueError("the weight's and the bias's elements overlap")
         with linear.on(self.acc.device, stream):
-            if self.micro_batches == 0 and not self.open:
+            dx, _, _, launch = linear._backward(dy, x, w, pre, act, dw, db, True, need_dx, True)
+            if self.micro_batches == 0 and not self.open:     # the layer is accepted
                 self.acc.zero_()
-            dx, _, _ = linear.backward(dy, x, w, pre, act, dw=dw, db=db, accumulate=True, need_dx=need_dx)
+            launch()
         self.open = True
         return dx
 

@@ -5,7 +5,7 @@ import contextlib
 import pytest
 import torch
 
-from gradient_reduction_amd import dc, linear
+from gradient_reduction_amd import dc, deferred, linear
 
 T, N, K = 3, 4, 5
 
@@ -101,3 +101,20 @@ def test_refusals_of_any_kind_come_first(launches, monkeypatch):
     with pytest.raises(MemoryError):
         call(o, db=db, dw=dw)
     assert not launches
+
+
+def test_a_refused_layer_leaves_the_accumulators(launches):
+    """What reduce(keep_acc=True) or anything else left in them stays until a
+    layer is accepted."""
+    red = deferred.DeferredReducer(2, 40, device="cpu")
+    red.acc.fill_(7.0)
+    o = operands()
+    for change, kw in [({"pre": None}, {}), ({"pre": torch.zeros(T, N + 1)}, {}), ({"dy": torch.zeros(T, N + 1)}, {}),
+                       ({"x": torch.zeros(T, K).double()}, {}), ({}, {"act": "tanh"}),
+                       ({"x": red.acc[0, :T * K].view(T, K)}, {}), ({"dy": red.acc[0, 20:20 + T * N].view(T, N)}, {})]:
+        a = {**o, **change}
+        with pytest.raises(ValueError):
+            red.accumulate_linear(0, 0, a["dy"], a["x"], a["w"], a["pre"], **{"act": "gelu", "bias_offset": 20, **kw})
+        assert not launches and not red.open and bool((red.acc == 7).all()), change
+    red.accumulate_linear(0, 0, o["dy"], o["x"], o["w"], o["pre"], act="gelu", bias_offset=20)
+    assert launches and red.open and bool((red.acc[0] == 0).all())
