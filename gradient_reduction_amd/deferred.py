@@ -32,11 +32,13 @@ class DeferredReducer:
         self.acc = torch.empty((W, self.ld), dtype=torch.float32, device=device)
         self.micro_batches = 0
         self.open = False          # a micro-batch is being added layer by layer
+        self.stale = set()         # rows that still hold what was there before this step
 
     def accumulate(self, x, ld_x: int, stream=None) -> None:
         """Add one micro-batch: acc[r] += x[r] on every replica row (the first
         micro-batch of a step starts from +0)."""
         self._closed("accumulate()")
+        self._clear_stale(stream)
         dc.dc_accumulate(self.W, x, ld_x, self.acc, self.ld, self.M, 1 if self.micro_batches == 0 else 0,
                          stream)
         self.micro_batches += 1
@@ -44,6 +46,15 @@ class DeferredReducer:
     def _closed(self, what):
         if self.open:
             raise RuntimeError(f"{what} inside a micro-batch: call end_micro_batch() first")
+
+    def _clear_stale(self, stream=None):
+        """Rows of a step's replicas that had no layer yet."""
+        if self.stale:
+            from . import linear
+            with linear.on(self.acc.device, stream):
+                for r in sorted(self.stale):
+                    self.acc[r].zero_()
+            self.stale = set()
 
     def _place(self, row, offset, n):
         if not 0 <= row < self.W:
@@ -58,7 +69,10 @@ class DeferredReducer:
         its weight gradient [N, K] is added at elements offset .. offset + N K
         of the row and its bias gradient at bias_offset, if given; returns dx
         (None without need_dx).  A parameter used by several layers is given
-        once for each.  The first call of a step clears the accumulator."""
+        once for each.  A replica's first call of a step clears its row, on
+        that call's stream, and no call touches another replica's: replicas may
+        be on streams of their own.  The caller orders calls of one row, and
+        what uses all rows (reduce, accumulate, state_dict) after them."""
         from . import linear
         n, k = w.shape
         dw = self._place(row, offset, n * k).view(n, k)
@@ -67,9 +81,11 @@ class DeferredReducer:
             raise ValueError("the weight's and the bias's elements overlap")
         with linear.on(self.acc.device, stream):
             dx, _, _, launch = linear._backward(dy, x, w, pre, act, dw, db, True, need_dx, True)
-            if self.micro_batches == 0 and not self.open:     # the layer is accepted
-                self.acc.zero_()
+            stale = self.stale if self.open or self.micro_batches else set(range(self.W))
+            if row in stale:                                  # the layer is accepted
+                self.acc[row].zero_()
             launch()
+        self.stale = stale - {row}
         self.open = True
         return dx
 
@@ -88,9 +104,10 @@ class DeferredReducer:
         (dc_accumulate_reduce); keep_acc also writes it to the accumulator.
         The next accumulate() starts a new step."""
         self._closed("reduce()")
+        if last is None and self.micro_batches == 0:
+            raise RuntimeError("reduce() before any accumulate() in this step")
+        self._clear_stale(stream)
         if last is None:
-            if self.micro_batches == 0:
-                raise RuntimeError("reduce() before any accumulate() in this step")
             dc.dc_deferred_reduce(self.W, self.acc, self.ld, out, ld_out, self.M, out_rows, stream)
         else:
             dc.dc_accumulate_reduce(self.W, last, ld_last, self.acc, self.ld,
@@ -102,6 +119,7 @@ class DeferredReducer:
         """The accumulator's state mid-step: a copy of the slab's M columns
         and the micro-batch count."""
         self._closed("state_dict()")
+        self._clear_stale()
         return {"acc": self.acc[:, :self.M].clone(), "micro_batches": self.micro_batches}
 
     def load_state_dict(self, state: dict) -> None:
@@ -110,4 +128,5 @@ class DeferredReducer:
             raise ValueError(f"accumulator of shape {tuple(acc.shape)}, expected {(self.W, self.M)}")
         self.acc[:, :self.M].copy_(acc)
         self.open = False
+        self.stale = set()
         self.micro_batches = int(state["micro_batches"])

@@ -118,3 +118,55 @@ def test_a_refused_layer_leaves_the_accumulators(launches):
         assert not launches and not red.open and bool((red.acc == 7).all()), change
     red.accumulate_linear(0, 0, o["dy"], o["x"], o["w"], o["pre"], act="gelu", bias_offset=20)
     assert launches and red.open and bool((red.acc[0] == 0).all())
+
+
+def test_a_layer_touches_its_own_replicas_accumulators_only(launches, monkeypatch):
+    """Replicas may be on streams of their own, so a layer of one may not clear
+    another's row: each row is cleared by its replica's first layer of the step,
+    and one without any before the row is next used."""
+    red = deferred.DeferredReducer(3, 40, device="cpu")
+    o = operands()
+
+    def add(row):
+        red.accumulate_linear(row, 0, o["dy"], o["x"], o["w"])
+        red.acc[row, 3] += 1.0          # as the product would
+
+    def rows():
+        return [red.acc[r, 3].item() for r in range(3)]
+
+    monkeypatch.setattr(dc, "dc_deferred_reduce", lambda *a: None)
+    monkeypatch.setattr(dc, "dc_accumulate", lambda *a: red.acc.add_(10.0) if a[-2] == 0 else red.acc.fill_(10.0))
+    red.acc.fill_(7.0)
+    add(1)
+    assert rows() == [7, 1, 7]
+    add(0)
+    add(1)
+    assert rows() == [1, 2, 7]
+    red.end_micro_batch()
+    add(0)
+    red.end_micro_batch()
+    assert rows() == [2, 2, 7]
+    assert red.state_dict()["acc"][:, 3].tolist() == [2, 2, 0] and rows() == [2, 2, 0]
+    red.reduce(None, 0)
+    # a step whose second micro-batch comes whole
+    red.acc.fill_(7.0)
+    add(2)
+    red.end_micro_batch()
+    red.accumulate(None, 0)
+    assert rows() == [10, 10, 11]
+    red.reduce(None, 0)
+    # one that is reduced with rows without layers
+    red.acc.fill_(7.0)
+    add(0)
+    red.end_micro_batch()
+    red.reduce(None, 0)
+    assert rows() == [1, 0, 0]
+    # one that is replaced by a saved state, and one of whole micro-batches
+    add(0)
+    red.load_state_dict({"acc": torch.full((3, 40), 5.0), "micro_batches": 1})
+    add(1)
+    assert rows() == [5, 6, 5]
+    red.end_micro_batch()
+    red.reduce(None, 0)
+    red.accumulate(None, 0)
+    assert rows() == [10, 10, 10]
