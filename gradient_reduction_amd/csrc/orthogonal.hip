@@ -20,6 +20,9 @@ namespace {
 
 constexpr int kNsChunk = 128;         // matrices whose products share launches
 constexpr int kNsPart = 48;           // of them whose addresses fit one launch's arguments
+// Planes of a chunk: the workspace does not grow with a model's layers.  A
+// 7B-class layer takes 2.4 GiB in pairs and has 12 rounds of tiles a product.
+constexpr int64_t kNsBytes = (int64_t)4 << 30;
 constexpr int kNormParts = 256;       // partial sums of squares per matrix, at most
 constexpr int64_t kNormSpan = 16384;  // elements per partial sum, at least
 
@@ -441,8 +444,8 @@ struct Holding {
 };
 
 // f(pair, indices, count) for every chunk: matrices held alike, kNsChunk of
-// them at most and of 2^22 64 x 64 tiles together unless it is one (a grid
-// holds 2^24), in chunks of about one size.
+// them at most, and of 2^22 64 x 64 tiles (a grid holds 2^24) and kNsBytes of
+// planes together unless it is one, in chunks of about one size.
 template <class F>
 void each_chunk(const Holding& held, const dc_matrix* mats, int32_t num, F&& f) {
   for (const int pair : {1, 2}) {
@@ -451,11 +454,12 @@ void each_chunk(const Holding& held, const dc_matrix* mats, int32_t num, F&& f) 
     for (int32_t k = 0; left > 0;) {
       const int32_t chunks = (left + kNsChunk - 1) / kNsChunk, most = (left + chunks - 1) / chunks;
       int32_t at[kNsChunk], count = 0;
-      int64_t tiles = 0;
+      int64_t tiles = 0, bytes = 0;
       for (; k < num && count < most; ++k) {
         if (held.values(mats[k]) != pair) continue;
         tiles += ((int64_t)(mats[k].rows + 63) / 64) * ((mats[k].cols + 63) / 64);
-        if (count > 0 && tiles > ((int64_t)1 << 22)) break;
+        bytes += NsShape(mats[k].rows, mats[k].cols).values(pair) * (int64_t)sizeof(Held);
+        if (count > 0 && (tiles > ((int64_t)1 << 22) || bytes > kNsBytes)) break;
         at[count++] = k;
       }
       f(pair, at, count);

@@ -877,7 +877,8 @@ dc_status dc_linear_backward(int32_t dtype, int64_t T, int64_t N, int64_t K, con
 
 /* Bytes of workspace of dc_orthogonalize (out_dtype = dtype) and
  * dc_muon_update (out_dtype = weight_dtype) for this list (its rows and
- * cols).  Host only. */
+ * cols): at most 4 GiB and 256 KiB, or what its largest matrix needs, as
+ * longer lists are worked off in parts.  Host only. */
 dc_status dc_orthogonalize_workspace(int32_t dtype, int32_t out_dtype, int32_t hold,
                                      const dc_matrix* mats, int32_t num, int64_t* bytes);
 

@@ -26,7 +26,7 @@ def dt(name):
 def close(name, got, u, hold, coeffs=ns.COEFFS, eps=1e-7):
     got = got.cpu()
     assert bool(torch.isfinite(got).all()), f"{name}: not finite"
-    off = ns.beyond(got, ns.exact(u, coeffs, eps), torch.finfo(got.dtype).eps / 2)
+    off = ns.beyond(got, ns.exact(u, coeffs, eps).cpu(), torch.finfo(got.dtype).eps / 2)
     most = 1.01 * ns.bound(hold, tuple(u.shape))
     assert off <= most, f"{name}: off by {off:.3g} |O| beyond the output's rounding, bound {most:.3g}"
 
@@ -81,3 +81,16 @@ def test_update_after_a_refused_registration():
             # most, which the steps' slopes (10 on the average) make 2e-6
             want = ns.exact(u.view(*sizes[t.param]), ns.COEFFS, 1e-7)
             assert ns.error(-weights[t.param].cpu().double(), want) <= ns.PAIR_BOUND + 2e-6 + 2.0 ** -24
+
+
+@pytest.mark.parametrize("hold", ["one", "pair"])
+def test_a_list_of_more_than_one_workspace(hold):
+    """Matrices whose planes do not fit the workspace together: those at the
+    beginning, the end and the middle, the first of a new chunk among them."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    us = [(torch.randn(*s, generator=gen, device="cuda") * 1e-3).bfloat16()
+          for s in [(4096, 4096)] * 9 + [(600, 270), (5000, 4100), (4096, 4096), (4096, 11008)] + [(4096, 4096)] * 24]
+    got = muon.orthogonalize(us, hold=hold)
+    # 16 of the pairs fit 4 GiB, 32 held once
+    for k in (0, 8, 9, 10, 12, 15, 16, 17, 31, 32, 36):
+        close(k, got[k], us[k], hold)

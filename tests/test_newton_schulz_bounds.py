@@ -1,9 +1,11 @@
 """The bounds that the GPU's orthogonalised matrices are held to can fail: the
 kernels' roundings stay under half of them, and wrong outputs do not (on the
 CPU; see newton_schulz_model)."""
+import numpy as np
 import pytest
 import torch
 
+from gradient_reduction_amd import dc
 from tests import newton_schulz_model as ns
 
 SHAPES = [(1, 1), (1, 333), (333, 1), (3, 5), (8, 8), (16, 64), (63, 65), (128, 128), (300, 130), (257, 513),
@@ -49,3 +51,25 @@ def test_halves_of_two_roundings_are_seen(shape):
         if seed < 2:
             assert ns.error(ns.model(u, ns.COEFFS, 1e-7, "pair"), want) <= ns.PAIR_BOUND / 2
     assert worst > ns.PAIR_BOUND
+
+
+def layer_7b():
+    return [(4096, 4096)] * 4 + [(11008, 4096)] * 2 + [(4096, 11008)]
+
+
+@pytest.mark.parametrize("hold", [dc.DC_HOLD_ONE, dc.DC_HOLD_PAIR])
+def test_the_workspace_does_not_grow_with_the_model(hold):
+    """A list's matrices share one workspace of a few GiB (or of the largest
+    matrix), however many there are."""
+    def need(shapes):
+        m = np.zeros(len(shapes), dc.MATRIX_DTYPE)
+        m["rows"], m["cols"] = [s[0] for s in shapes], [s[1] for s in shapes]
+        return dc.dc_orthogonalize_workspace(dc.DC_BF16, dc.DC_F32, hold, m, len(m))
+
+    parts = 1 << 20
+    for shapes in (layer_7b() * 32, [(8192, 8192)] * 100, [(1 << 20, 512)] * 9, layer_7b()[::-1] * 5):
+        assert need(shapes) <= max((4 << 30) + parts, max(need([s]) for s in set(shapes)))
+    # what fits is not cut: one layer, and 128 small matrices
+    one = 2 * hold * 2
+    assert need(layer_7b()) >= one * sum(a * b + min(a, b) ** 2 for a, b in layer_7b())
+    assert need([(1024, 1024)] * 128) >= one * 128 * 2 * 1024 * 1024
