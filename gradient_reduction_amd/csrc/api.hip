@@ -1286,6 +1286,16 @@ dc_status dc_bias_act_workspace(int32_t dtype, int64_t T, int64_t N, int64_t* by
   return ok();
 }
 
+dc_status dc_linear_form(int32_t dtype, int32_t product, int64_t T, int64_t N, int64_t K, int32_t* out) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, N, K))) return st;
+  if (product < DC_PRODUCT_FORWARD || product > DC_PRODUCT_DW) return fail(DC_ERR_ARG, "product=%d", product);
+  if (out == nullptr) return fail(DC_ERR_NULL, "out is NULL");
+  const dc::LaunchForm f = dc::linear_form(dtype, product, T, N, K);
+  out[0] = f.tile, out[1] = f.stages, out[2] = f.splits;
+  return ok();
+}
+
 dc_status dc_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x,
                     const void* w, int64_t ld_w, const void* bias, const void* residual,
                     int64_t ld_res, int32_t act, void* pre, int64_t ld_pre, void* y, int64_t ld_y,
@@ -1379,6 +1389,21 @@ dc_status dc_orthogonalize_workspace(int32_t dtype, int32_t out_dtype, int32_t h
     return st;
   if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
   *bytes = dc::ns_workspace(dtype, out_dtype, hold, mats, num);
+  return ok();
+}
+
+dc_status dc_orthogonalize_form(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats,
+                                int32_t num, int32_t update, int32_t index, int32_t* out) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_dtype(out_dtype)) || (st = check_hold(hold)) ||
+      (st = check_matrices(mats, num)))
+    return st;
+  if (update != 0 && update != 1) return fail(DC_ERR_ARG, "update=%d", update);
+  if (index < 0 || index >= num) return fail(DC_ERR_ARG, "index=%d of %d matrices", index, num);
+  if (out == nullptr) return fail(DC_ERR_NULL, "out is NULL");
+  dc::LaunchForm f[4];
+  dc::ns_forms(dtype, out_dtype, hold, mats, num, update == 1, index, f);
+  for (int k = 0; k < 4; ++k) out[3 * k] = f[k].tile, out[3 * k + 1] = f[k].stages, out[3 * k + 2] = f[k].splits;
   return ok();
 }
 

@@ -194,6 +194,14 @@ int64_t linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K);
 int64_t linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K);
 int64_t bias_act_workspace(int32_t dtype, int64_t T, int64_t N);
 
+// The kernel that a product runs on: its tile (0: the few-row kernel), the
+// stages of 128 bytes of k that it keeps (aligned operands) and the splits of k.
+struct LaunchForm {
+  int32_t tile, stages, splits;
+};
+// kind: 0 forward, 1 dx, 2 dw.
+LaunchForm linear_form(int32_t dtype, int32_t kind, int64_t T, int64_t N, int64_t K);
+
 hipError_t launch_linear(int32_t dtype, int64_t T, int64_t N, int64_t K, const void* x, int64_t ld_x, const void* w,
                          int64_t ld_w, const LinearOut& o, void* workspace, hipStream_t stream);
 
@@ -230,6 +238,9 @@ float ns_factor(int32_t scale_mode, int32_t rows, int32_t cols);
 // Upper bound of every singular value at any step.
 double ns_largest(int32_t steps, const float* coeffs);
 int64_t ns_workspace(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats, int32_t num);
+// Of the products of matrix `index` of the list: A, B, a step and the last one.
+void ns_forms(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats, int32_t num, bool update,
+              int32_t index, LaunchForm forms[4]);
 hipError_t launch_ns(const NsLaunch& a, hipStream_t stream);
 
 }  // namespace dc

@@ -227,9 +227,9 @@ hipError_t product(int32_t dtype, const void* a, int64_t ld_a, const void* b, in
   const ProductArgs g{a, b, ld_a, ld_b, m, n, k, (m + c.tile - 1) / c.tile, (n + c.tile - 1) / c.tile, c.splits,
                       c.k_per_split, partial, c.ld_partial};
   const bool direct = direct_operand<T>(a, ld_a, KCA ? k : m) && direct_operand<T>(b, ld_b, KCB ? k : n);
-  const bool deep = deep_launch(g.tiles_m * g.tiles_n * g.splits);
+  const int32_t stages = launch_stages(c.tile, g.tiles_m * g.tiles_n * g.splits);
   if (c.tile == 256) launch_product<T, 256, 4, 2, 2, KCA, KCB>(g, direct, epi, stream);
-  else if (c.tile == 128 && deep) launch_product<T, 128, 2, 4, 4, KCA, KCB>(g, direct, epi, stream);
+  else if (c.tile == 128 && stages == 4) launch_product<T, 128, 2, 4, 4, KCA, KCB>(g, direct, epi, stream);
   else if (c.tile == 128) launch_product<T, 128, 2, 4, 2, KCA, KCB>(g, direct, epi, stream);
   else launch_product<T, 64, 2, 2, 3, KCA, KCB>(g, direct, epi, stream);
   if (c.splits > 1) {
@@ -490,6 +490,14 @@ int64_t linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K) {
 
 int64_t linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K) {
   return std::max(cut(dtype, T, K, N).partial_bytes(T), cut(dtype, N, K, T).partial_bytes(N));
+}
+
+LaunchForm linear_form(int32_t dtype, int32_t kind, int64_t T, int64_t N, int64_t K) {
+  if (kind == 0 && is_few(T, N)) return {};
+  const int64_t m = kind == 2 ? N : T, n = kind == 0 ? N : K;
+  const Cut c = cut(dtype, m, n, kind == 0 ? K : kind == 1 ? N : T);
+  const int64_t tiles = ((m + c.tile - 1) / c.tile) * ((n + c.tile - 1) / c.tile);
+  return {c.tile, launch_stages(c.tile, tiles * c.splits), c.splits};
 }
 
 int64_t bias_act_workspace(int32_t dtype, int64_t T, int64_t N) {

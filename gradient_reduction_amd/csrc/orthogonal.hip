@@ -516,6 +516,20 @@ int ns_tile(const NsPlanes& tab, Product p, int pair) {
   return best;
 }
 
+// The tiles of a chunk's products.
+struct NsCut {
+  int gram, poly, step, last;
+};
+
+NsCut ns_cut(const NsPlanes& tab, int pair, bool update) {
+  NsCut c{ns_tile(tab, kGram, pair), ns_tile(tab, kPoly, pair), ns_tile(tab, kStep, pair), 0};
+  // The last step of an update also reads and writes the weights: two 128
+  // tiles in a compute unit overlap that with products (40 matrices of 1024 x
+  // 1024 and 4096 x 1024, fp32 weights: 295 us against 356 us of one 256 tile).
+  c.last = update && c.step == 256 ? 128 : c.step;
+  return c;
+}
+
 // The first tiles of a product's launch; returns their number.
 template <class Table>
 int32_t product_tiles(NsTiles& tiles, const Table& tab, Product p, int tile) {
@@ -531,7 +545,7 @@ void launch_symmetric(const NsPlanes& tab, const NsTiles& tiles, int32_t n, int 
   auto launch = [&](auto kernel, int threads) {
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, alpha, beta);
   };
-  const bool deep = deep_launch(n);
+  const bool deep = launch_stages(tile, n) == 4;
   if (tile == 256) launch(k_ns_symmetric<P, 256, 4, 2, 2, POLY>, 512);
   else if (tile == 128 && deep) launch(k_ns_symmetric<P, 128, 2, 4, 4, POLY>, 512);
   else if (tile == 128) launch(k_ns_symmetric<P, 128, 2, 4, 2, POLY>, 512);
@@ -544,7 +558,7 @@ void launch_step(const Table& tab, const NsTiles& tiles, int32_t n, int tile, He
   auto launch = [&](auto kernel, int threads) {
     kernel<<<n, threads, 0, stream>>>(tab, tiles, planes, next, a_coef, beta, up);
   };
-  const bool deep = deep_launch(n);
+  const bool deep = launch_stages(tile, n) == 4;
   if (tile == 256) launch(k_ns_step<P, O, 256, 4, 2, 2, LAST, Table>, 512);
   else if (tile == 128 && deep) launch(k_ns_step<P, O, 128, 2, 4, 4, LAST, Table>, 512);
   else if (tile == 128) launch(k_ns_step<P, O, 128, 2, 4, 2, LAST, Table>, 512);
@@ -580,34 +594,38 @@ void ns_chunk(const NsMatrix* mats, int32_t count, const NsLaunch& a, const NsSc
   NsPlanes all;
   all.count = count;
   for (int32_t k = 0; k < count; ++k) all.m[k] = {mats[k].base, mats[k].rows, mats[k].cols};
-  const int gram_tile = ns_tile(all, kGram, P), poly_tile = ns_tile(all, kPoly, P), step_tile = ns_tile(all, kStep, P);
-  // The last step of an update also reads and writes the weights: two 128
-  // tiles in a compute unit overlap that with products (40 matrices of 1024 x
-  // 1024 and 4096 x 1024, fp32 weights: 295 us against 356 us of one 256 tile).
-  const int last_tile = MOM && step_tile == 256 ? 128 : step_tile;
+  const NsCut cut = ns_cut(all, P, MOM);
   NsTiles gram, poly, step;
-  const int32_t n_gram = product_tiles(gram, all, kGram, gram_tile), n_poly = product_tiles(poly, all, kPoly, poly_tile),
-                n_step = product_tiles(step, all, kStep, step_tile);
+  const int32_t n_gram = product_tiles(gram, all, kGram, cut.gram), n_poly = product_tiles(poly, all, kPoly, cut.poly),
+                n_step = product_tiles(step, all, kStep, cut.step);
   for (int32_t k = 0; k < a.steps; ++k) {
     const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
     const int32_t next = k & 1;
-    launch_symmetric<P, false>(all, gram, n_gram, gram_tile, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
+    launch_symmetric<P, false>(all, gram, n_gram, cut.gram, planes, next, sc.a / (sc.x * sc.x), 0.f, stream);
     // B = c (A A + b / c A): a c too small for fp32 to see beside b stands for
     // zero
     const double c = std::fabs(cc) < std::fabs(cb) * 0x1p-30 ? std::fabs(cb) * 0x1p-30 : cc;
-    launch_symmetric<P, true>(all, poly, n_poly, poly_tile, planes, next, (float)(c * sc.b[k] / ((double)sc.a * sc.a)),
+    launch_symmetric<P, true>(all, poly, n_poly, cut.poly, planes, next, (float)(c * sc.b[k] / ((double)sc.a * sc.a)),
                               c != 0 ? (float)(cb * sc.a / c) : 0.f, stream);
     if (k + 1 < a.steps) {
-      launch_step<P, O, kNsNext>(all, step, n_step, step_tile, planes, next, ca * sc.b[k], 1.f / sc.b[k], up, stream);
+      launch_step<P, O, kNsNext>(all, step, n_step, cut.step, planes, next, ca * sc.b[k], 1.f / sc.b[k], up, stream);
     } else {
       by_part([&](const NsTable& tab) {
         NsTiles last;
-        const int32_t n = product_tiles(last, tab, kStep, last_tile);
-        launch_step<P, O, MOM ? kNsWeight : kNsOut>(tab, last, n, last_tile, planes, next, ca * sc.b[k],
+        const int32_t n = product_tiles(last, tab, kStep, cut.last);
+        launch_step<P, O, MOM ? kNsWeight : kNsOut>(tab, last, n, cut.last, planes, next, ca * sc.b[k],
                                                     1.f / (sc.b[k] * sc.x), up, stream);
       });
     }
   }
+}
+
+// A chunk's matrices, the longest sums first, so that short ones fill what they
+// leave.
+void sort_chunk(NsMatrix* mats, int32_t count) {
+  std::sort(mats, mats + count, [](const NsMatrix& x, const NsMatrix& y) {
+    return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
+  });
 }
 
 template <class G, class O, bool MOM>
@@ -627,10 +645,7 @@ hipError_t ns_run(const NsLaunch& a, hipStream_t stream) {
                          a.lr * ns_factor(a.scale_mode, d.rows, d.cols)};
       base += NsShape(d.rows, d.cols).values(pair);
     }
-    // the longest sums first, so that short ones fill what they leave
-    std::sort(mats, mats + count, [](const NsMatrix& x, const NsMatrix& y) {
-      return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
-    });
+    sort_chunk(mats, count);
     if (pair == 2) ns_chunk<2, G, O, MOM>(mats, count, a, sc, up, parts, planes, stream);
     else ns_chunk<1, G, O, MOM>(mats, count, a, sc, up, parts, planes, stream);
     status = hipGetLastError();
@@ -660,6 +675,40 @@ int64_t ns_workspace(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_ma
     most = std::max(most, v);
   });
   return num ? kPartsBytes + most * (int64_t)sizeof(Held) : 0;
+}
+
+void ns_forms(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats, int32_t num, bool update,
+              int32_t index, LaunchForm forms[4]) {
+  each_chunk(Holding{dtype, out_dtype, hold}, mats, num, [&](int pair, const int32_t* at, int32_t count) {
+    const int32_t* own = std::find(at, at + count, index);
+    if (own == at + count) return;
+    NsMatrix sorted[kNsChunk];
+    for (int32_t k = 0; k < count; ++k) {
+      sorted[k] = NsMatrix{};
+      sorted[k].rows = mats[at[k]].rows;
+      sorted[k].cols = mats[at[k]].cols;
+    }
+    sort_chunk(sorted, count);
+    NsPlanes all;
+    all.count = count;
+    for (int32_t k = 0; k < count; ++k) all.m[k] = {0, sorted[k].rows, sorted[k].cols};
+    const NsCut cut = ns_cut(all, pair, update);
+    NsTiles tiles;
+    auto form = [&](Product p, int tile) {
+      return LaunchForm{tile, launch_stages(tile, product_tiles(tiles, all, p, tile)), 1};
+    };
+    forms[0] = form(kGram, cut.gram);
+    forms[1] = form(kPoly, cut.poly);
+    forms[2] = form(kStep, cut.step);
+    // the last step goes by parts of kNsPart matrices
+    const dc_matrix& m = mats[*own];
+    int32_t k = 0;
+    while (sorted[k].rows != m.rows || sorted[k].cols != m.cols) ++k;
+    NsPlanes part;
+    part.count = std::min(kNsPart, count - k / kNsPart * kNsPart);
+    std::copy(all.m + k / kNsPart * kNsPart, all.m + k / kNsPart * kNsPart + part.count, part.m);
+    forms[3] = LaunchForm{cut.last, launch_stages(cut.last, product_tiles(tiles, part, kStep, cut.last)), 1};
+  });
 }
 
 hipError_t launch_ns(const NsLaunch& a, hipStream_t stream) {

@@ -505,6 +505,12 @@ constexpr int64_t kComputeUnits = 256;
 // 1024 matrix orthogonalised: 173 us against 165).
 inline bool deep_launch(int64_t tiles) { return tiles <= kComputeUnits; }
 
+// Stages of a launch of `tiles` tiles whose operands are loaded straight into
+// LDS.
+inline int32_t launch_stages(int32_t tile, int64_t tiles) {
+  return tile == 256 ? 2 : tile == 64 ? 3 : deep_launch(tiles) ? 4 : 2;
+}
+
 // Microseconds that a compute unit takes for a stage of a tile, as measured
 // with the unit busy (one 256 tile, two of 128, three of 64 resident): 2
 // tile^2 64 operations at 1.26, 1.0 and 0.55 PFLOP/s over the chip; fp32 is

@@ -24,6 +24,7 @@ DC_SCHED_RING, DC_SCHED_BIDIR, DC_SCHED_RD = 0, 1, 2
 DC_MAX_W, DC_MAX_GROUPS, DC_MAX_COMMS = 64, 64, 8
 
 DC_ACT_NONE, DC_ACT_RELU, DC_ACT_GELU, DC_ACT_SILU = 0, 1, 2, 3
+DC_PRODUCT_FORWARD, DC_PRODUCT_DX, DC_PRODUCT_DW = 0, 1, 2
 DC_SCALE_NONE, DC_SCALE_ASPECT, DC_SCALE_RMS = 0, 1, 2
 DC_HOLD_AUTO, DC_HOLD_ONE, DC_HOLD_PAIR = 0, 1, 2
 DC_NS_MAX_STEPS = 16
@@ -101,6 +102,8 @@ _SIGS = {
     "dc_linear_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
     "dc_linear_backward_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
     "dc_bias_act_workspace": ([_i32, _i64, _i64, _vp], _i32),
+    "dc_linear_form": ([_i32, _i32, _i64, _i64, _i64, _vp], _i32),
+    "dc_orthogonalize_form": ([_i32, _i32, _i32, _vp, _i32, _i32, _i32, _vp], _i32),
     "dc_linear": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp,
                    _i64, _vp, _i64, _vp], _i32),
     "dc_bias_act_backward": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i32,
@@ -490,6 +493,13 @@ def dc_bias_act_workspace(dtype, T, N):
     return n.value
 
 
+def dc_linear_form(dtype, product, T, N, K):
+    """Host only; (tile, stages, splits) of a product's kernel."""
+    out = (ctypes.c_int32 * 3)()
+    _check("dc_linear_form", lib().dc_linear_form(dtype, product, T, N, K, out))
+    return tuple(out)
+
+
 def dc_linear(dtype, T, N, K, x, ld_x, w, ld_w, bias, residual, ld_res, act, pre, ld_pre, y, ld_y,
               workspace, workspace_bytes, stream=None):
     _check("dc_linear", lib().dc_linear(
@@ -518,6 +528,16 @@ def dc_orthogonalize_workspace(dtype, out_dtype, hold, mats, num):
     _check("dc_orthogonalize_workspace", lib().dc_orthogonalize_workspace(
         dtype, out_dtype, hold, mp, num, ctypes.byref(n)))
     return n.value
+
+
+def dc_orthogonalize_form(dtype, out_dtype, hold, mats, num, update, index):
+    """Host only; mats: MATRIX_DTYPE records.  (tile, stages, splits) for A, B,
+    a step and the last step of matrix `index`."""
+    mp, _a = _host(mats, MATRIX_DTYPE)
+    out = (ctypes.c_int32 * 12)()
+    _check("dc_orthogonalize_form", lib().dc_orthogonalize_form(
+        dtype, out_dtype, hold, mp, num, update, index, out))
+    return [tuple(out[k:k + 3]) for k in range(0, 12, 3)]
 
 
 def dc_orthogonalize(dtype, hold, mats, num, steps, coeffs, eps, workspace, workspace_bytes,

@@ -93,6 +93,10 @@ typedef int32_t dc_status;
 #define DC_ACT_GELU 2        /* v Phi(v), Phi the normal distribution's */
 #define DC_ACT_SILU 3        /* v / (1 + exp(-v)) */
 
+#define DC_PRODUCT_FORWARD 0 /* products of the linear layer */
+#define DC_PRODUCT_DX 1
+#define DC_PRODUCT_DW 2
+
 #define DC_SCALE_NONE 0      /* shape factor of a matrix update: 1 */
 #define DC_SCALE_ASPECT 1    /* sqrt(max(1, rows / cols)) */
 #define DC_SCALE_RMS 2       /* 0.2 sqrt(max(rows, cols)) */
@@ -822,6 +826,16 @@ dc_status dc_linear_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, in
 dc_status dc_linear_backward_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t* bytes);
 dc_status dc_bias_act_workspace(int32_t dtype, int64_t T, int64_t N, int64_t* bytes);
 
+/* The kernel that a product runs on, as the library chooses it from types and
+ * sizes: out[0] its square tile (256, 128 or 64; 0: the kernel for up to 64
+ * rows), out[1] the stages of its loads (where operands and strides are whole
+ * 16 bytes; others go through registers), out[2] the parts that its sum is cut
+ * into.  For profiles and tests; nothing depends on it.  Host only.
+ *   product   DC_PRODUCT_FORWARD (dc_linear), DC_PRODUCT_DX or DC_PRODUCT_DW
+ *             (dc_linear_backward)
+ *   out       host int32[3] */
+dc_status dc_linear_form(int32_t dtype, int32_t product, int64_t T, int64_t N, int64_t K, int32_t* out);
+
 /* Linear layer on T rows (tokens), N outputs, K inputs:
  *   pre[t][n] = sum_k x[t][k] w[n][k] + bias[n]
  *   y[t][n]   = act(pre[t][n]) + residual[t][n]
@@ -881,6 +895,13 @@ dc_status dc_linear_backward(int32_t dtype, int64_t T, int64_t N, int64_t K, con
  * longer lists are worked off in parts.  Host only. */
 dc_status dc_orthogonalize_workspace(int32_t dtype, int32_t out_dtype, int32_t hold,
                                      const dc_matrix* mats, int32_t num, int64_t* bytes);
+
+/* The same for the products of matrix `index` of a list: out[3 k ..] for A (k =
+ * 0), B (1), a step's X (2) and the last step's (3).
+ *   update  1: dc_muon_update, 0: dc_orthogonalize
+ *   out     host int32[12] */
+dc_status dc_orthogonalize_form(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* mats,
+                                int32_t num, int32_t update, int32_t index, int32_t* out);
 
 /* Every matrix orthogonalised by Newton-Schulz products.  With X the
  * gradient (its transpose where rows > cols):
