@@ -7,6 +7,7 @@ import torch
 from gradient_reduction_amd import dc, executor, muon
 from synth import workloads as wl
 from tests import newton_schulz_model as ns
+from tests import product_forms as pf
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +95,62 @@ def test_a_list_of_more_than_one_workspace(hold):
     # 16 of the pairs fit 4 GiB, 32 held once
     for k in (0, 8, 9, 10, 12, 15, 16, 17, 31, 32, 36):
         close(k, got[k], us[k], hold)
+
+
+def made(shapes, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    some = [ns.gradient(gen, *s, dtype=dtype) for s in sorted(set(shapes))]
+    # matrices of one shape differ by a shift of their columns
+    return [some[sorted(set(shapes)).index(s)].roll(k, 1).cuda().contiguous() for k, s in enumerate(shapes)]
+
+
+@pytest.mark.parametrize("hold", ["one", "pair"])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("shapes", pf.ORTHOGONAL, ids=lambda v: f"{len(v)}x{v[0]}".replace(" ", ""))
+def test_every_form_of_the_products(shapes, kind, hold):
+    us = made(shapes, dt(kind), 5)
+    got = muon.orthogonalize(us, hold=hold)
+    for k in {0, len(shapes) // 2, len(shapes) - 1}:
+        close(k, got[k], us[k], hold)
+
+
+@pytest.mark.parametrize("hold", ["one", "pair"])
+@pytest.mark.parametrize("kind, wkind", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("shapes", pf.ORTHOGONAL, ids=lambda v: f"{len(v)}x{v[0]}".replace(" ", ""))
+def test_every_form_of_the_update(shapes, kind, wkind, hold):
+    """w <- (1 - lr wd) w - lr O(mu m + g).  The look-ahead is rounded twice to
+    fp32 (2^-24 of it each), which the steps make ten times as much on the
+    average; the weight takes six roundings of its terms besides the output's."""
+    gs = made(shapes, dt(kind), 6)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    ms = [torch.randn(*s, generator=gen, device="cuda") * 1e-3 for s in shapes]
+    ws = [(torch.randn(*s, generator=gen, device="cuda") * 0.05).to(dt(wkind)) for s in shapes]
+    some = sorted({0, len(shapes) // 2, len(shapes) - 1})
+    old = {k: (ws[k].double(), ms[k].double()) for k in some}
+    lr, mu, wd = 0.5, 0.9375, 0.125                     # exact in fp32
+    muon.update(ws, gs, ms, lr=lr, mu=mu, nesterov=True, weight_decay=wd, scale="none", hold=hold)
+    for k in some:
+        w, m = old[k]
+        new = mu * m + gs[k].double()
+        assert bool(((ms[k].double() - new).abs() <= 2.0 ** -24 * new.abs() + 1e-40).all())
+        o = lr * ns.exact(mu * new + gs[k].double(), ns.COEFFS, 1e-7)
+        want = (1 - lr * wd) * w - o
+        half = torch.finfo(ws[k].dtype).eps / 2
+        off = (ws[k].double() - want).abs() - half * want.abs() - 6 * 2.0 ** -24 * (w.abs() + o.abs())
+        most = 1.02 * (ns.bound(hold, shapes[k]) + 20 * 2.0 ** -24)
+        assert (off.clamp(min=0).norm() / o.norm()).item() <= most, k
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 2), (2, 1), (1, 333), (333, 1), (3, 5), (5, 3), (8, 8), (16, 64), (63, 65),
+                                   (64, 64), (65, 64), (129, 127), (300, 130), (257, 513), (200, 1000)], ids=str)
+def test_every_shape(shape, kind):
+    u = ns.gradient(torch.Generator().manual_seed(8), *shape, dtype=dt(kind))
+    close("pair", muon.orthogonalize(u.cuda()), u, "pair")
+    close("one", muon.orthogonalize(u.cuda(), hold="one"), u, "one")
+    close("four steps", muon.orthogonalize(u.cuda(), steps=4), u, "pair", coeffs=ns.COEFFS[:4])
+    # another gradient's size, and eps that counts beside it
+    v = (u.double() * 1e4).to(u.dtype)
+    close("large", muon.orthogonalize(v.cuda()), v, "pair")
+    eps = float(torch.tensor(u.double().norm().item() / 4).float())
+    close("eps", muon.orthogonalize(u.cuda(), eps=eps), u, "pair", eps=eps)
