@@ -254,7 +254,18 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
 // The product of two operands that are pairs of planes, size_a and size_b
 // apart; the small products first.  hook is called with the stages that hold
 // B's own values (of each plane of it).
-template <class Tile, int P, class Acc, class Hook>
+//
+// An instruction rounds the sum it adds to four times (once for eight of its 32
+// products), so a long sum collects roundings of its whole size: with A's sums
+// in one piece 20 x 2000, 4000 x 24 and 48 x 4096 were off by 1.9e-6, 2.9e-6
+// and 1.6e-6 of |O|_F, with sums of kFold stages that are added up apart (FOLD)
+// by 1.4e-6, 1.5e-6 and 1.4e-6; one 1024 x 1024 matrix takes 284 us so, 278
+// without.  (Most of the rest is that the eight products are cut off at 2^-24 of
+// the largest.)  The other products' sums are as short as the smaller side: 308
+// us with all of them so.  A 256 tile has no registers for it.
+constexpr int kFold = 4;
+
+template <class Tile, int P, bool FOLD, class Acc, class Hook>
 __device__ __forceinline__ void held_product(Operand<Held> a, int64_t size_a, Operand<Held> b, int64_t size_b,
                                              int64_t k, Acc& acc, Hook&& hook) {
   if constexpr (P == 2) {
@@ -265,7 +276,29 @@ __device__ __forceinline__ void held_product(Operand<Held> a, int64_t size_a, Op
     low.p += size_b;
     Tile::run(a, low, 0, k, acc, hook);
   }
-  Tile::run(a, b, 0, k, acc, hook);
+  if constexpr (P == 2 && FOLD) {
+    f32x4 total[Tile::MI][Tile::NI] = {};
+    auto fold = [&] {
+#pragma unroll
+      for (int i = 0; i < Tile::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile::NI; ++j) {
+          total[i][j] += acc[i][j];
+          acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    };
+    fold();
+    Tile::run(a, b, 0, k, acc, [&](LdsPtr la, int64_t k0) {
+      hook(la, k0);
+      if ((k0 / Tile::BK) % kFold == kFold - 1) fold();
+    });
+#pragma unroll
+    for (int i = 0; i < Tile::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < Tile::NI; ++j) acc[i][j] += total[i][j];
+  } else {
+    Tile::run(a, b, 0, k, acc, hook);
+  }
 }
 
 // Tile t of the upper triangle of an nt x nt grid, by rows.
@@ -305,7 +338,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
   f32x4 acc[Tile::MI][Tile::NI] = {};
   // B: beta A, its own transpose, comes into the sums from the stages that
   // hold it
-  held_product<Tile, P>(a, size, b, size, ld, acc, [&](LdsPtr la, int64_t k) {
+  held_product<Tile, P, !POLY && BT <= 128>(a, size, b, size, ld, acc, [&](LdsPtr la, int64_t k) {
     if constexpr (POLY) Tile::add_b(la, k, i0, beta, acc);
   });
   // Columns m .. lda - 1 get zeros; the mirrored tile gets the same values.
@@ -347,7 +380,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
   f32x4 acc[Tile::MI][Tile::NI] = {};
   // a X comes into the sums from the stages that hold it: with the tile read
   // again after the sums, every unit waited for memory at once
-  held_product<Tile, P>(a, sh.a_size, b, sh.x_size, sh.m, acc,
+  held_product<Tile, P, false>(a, sh.a_size, b, sh.x_size, sh.m, acc,
                         [&](LdsPtr la, int64_t k) { Tile::add_b(la, k, i0, a_coef, acc); });
   O* out = nullptr;
   int64_t ld_out = 0;

@@ -8,7 +8,7 @@ product of pairs leaves out low x low (2^-24), and sums round to 24 bits: about
 2^-22 of a value in all, once in each of A, B and X per step.  A rounding in X
 grows by the slopes of the steps that follow: 3.45^5 = 485 where all five meet a
 vanishing singular value, about ten on the average over a random matrix's.
-model() carries exactly these roundings through and gives 4e-7 to 6e-7 at sides
+model() carries exactly these roundings through and, with sums rounded once, gives 4e-7 to 6e-7 at sides
 of 16 and more, up to 2e-6 on a few elements, and 1.2e-3 to 1.8e-3 (up to 4.5e-3)
 with one fp16.  The bounds are twice the largest of these;
 tests/test_newton_schulz_bounds.py checks that, and that wrong outputs break
@@ -62,14 +62,34 @@ def _held(v, hold, fault):
     return high.double(), low.double()
 
 
-def _product(a, b):
-    """Of (high, low) pairs, summed in fp32 (rounded once here)."""
-    return (a[0] @ b[0] + a[0] @ b[1] + a[1] @ b[0]).float().double()
+def _instructions(a, b, acc, fold):
+    """acc + a b as the matrix instructions add it up: eight products at a time,
+    each cut off at 2^-24 of the largest one's power of two, and their sum
+    rounded into the fp32 sum; after `fold` of these a sum begins anew, and the
+    sums are added up apart (0: never)."""
+    part = torch.zeros_like(acc) if fold else acc
+    for i, k in enumerate(range(0, a.shape[1], 8)):
+        p = a[:, k:k + 8, None] * b[None, k:k + 8, :]
+        unit = torch.exp2(torch.floor(torch.log2(p.abs().amax(1, keepdim=True).clamp(min=1e-300))) - 24)
+        part = (part + (torch.trunc(p / unit) * unit).sum(1)).float().double()
+        if fold and (i + 1) % fold == 0:
+            acc, part = (acc + part).float().double(), torch.zeros_like(acc)
+    return (acc + part).float().double() if fold else part
 
 
-def model(u, coeffs, eps, hold, fault=None):
-    """O as the kernels round it (before the output's rounding).  fault:
-    "no low half", or "folded" (the low half taken from another rounding of
+def _product(a, b, fold=None):
+    """Of (high, low) pairs, summed in fp32: rounded once, or with `fold` as the
+    instructions do it (the small products first)."""
+    if fold is None:
+        return (a[0] @ b[0] + a[0] @ b[1] + a[1] @ b[0]).float().double()
+    acc = torch.zeros(a[0].shape[0], b[0].shape[1], dtype=torch.float64)
+    acc = _instructions(a[0], b[1], _instructions(a[1], b[0], acc, 0), 0)
+    return _instructions(a[0], b[0], acc, fold)
+
+
+def model(u, coeffs, eps, hold, fault=None, fold=None):
+    """O as the kernels round it (before the output's rounding).  fold: sums as
+    _product gives them.  fault: "no low half", or "folded" (the low half taken from another rounding of
     the value than the one that is stored, in B)."""
     x = u.double()
     flip = u.shape[0] > u.shape[1]
@@ -80,13 +100,13 @@ def model(u, coeffs, eps, hold, fault=None):
     for k, (a, b, c) in enumerate(coeffs):
         a, b, c = float(a), float(b), float(c)
         # A by a power of two
-        g = _held((_product(p, (p[0].t(), p[1].t())) * (2.0 ** 12 / scale ** 2)), hold, own)
+        g = _held((_product(p, (p[0].t(), p[1].t()), fold) * (2.0 ** 12 / scale ** 2)), hold, own)
         # B = alpha (beta A + A A), alpha no power of two
         alpha = torch.tensor(c * 2.0 ** 11 / 2.0 ** 24).float().double()
         beta = torch.tensor(b * 2.0 ** 12 / c).float().double()
-        s = (g[0] @ g[0] + g[0] @ g[1] + g[1] @ g[0] + beta * (g[0] + g[1])).float().double()
+        s = (_product(g, g, fold) + beta * (g[0] + g[1])).float().double()
         q = _held((alpha * s).contiguous(), hold, fault)
-        new = (a * 2.0 ** 11 * (p[0] + p[1]) + _product(q, p)).float().double() * 2.0 ** -11
+        new = (a * 2.0 ** 11 * (p[0] + p[1]) + _product(q, p, fold)).float().double() * 2.0 ** -11
         if k + 1 < len(coeffs):
             p = _held(new, hold, own)
     out = new / scale

@@ -154,3 +154,20 @@ def test_every_shape(shape, kind):
     close("large", muon.orthogonalize(v.cuda()), v, "pair")
     eps = float(torch.tensor(u.double().norm().item() / 4).float())
     close("eps", muon.orthogonalize(u.cuda(), eps=eps), u, "pair", eps=eps)
+
+
+@pytest.mark.parametrize("shape", [(20, 2000), (4000, 24), (48, 4096)], ids=str)
+def test_long_sums(shape):
+    """Sums of thousands of products are added up in parts of 256 (32 times
+    eight): off by what the model of that gives.  One matrix's error scatters by
+    a third about it, the mean of eight by an eighth; twice that is allowed.
+    Sums in one piece are off by 1.6, 2 and 1.15 times as much."""
+    us = [ns.gradient(torch.Generator().manual_seed(s), *shape, dtype=torch.float32) for s in range(8)]
+    got = muon.orthogonalize(torch.stack(us).cuda(), hold="pair").cpu()
+    here = there = 0.0
+    for g, u in zip(got, us):
+        want = ns.exact(u, ns.COEFFS, 1e-7)
+        here += ns.error(g.double(), want) / len(us)
+        there += ns.error(ns.model(u, ns.COEFFS, 1e-7, "pair", fold=32), want) / len(us)
+    print(f"{shape}: {here:.3g}, the model {there:.3g}", flush=True)
+    assert here <= 1.25 * there
