@@ -265,12 +265,26 @@ __global__ void __launch_bounds__(256) k_ns_load(NsTable tab, NsTiles tiles, NsU
 // us with all of them so.  A 256 tile has no registers for it.
 constexpr int kFold = 4;
 
+// Up to kFew singular values do not average what is left out: their products
+// of the low halves (2^-24 of a value, of one sign on A's diagonal) are taken
+// too (64 tiles).  Without them 1 x 300 was off by 6.9e-7 of |O|_F and 4 x 1000
+// by 1.3e-6, with them by 5.5e-7 and 9.8e-7; nine odd matrices, three of them
+// with few, take 231.7 us so, 230.3 without.
+constexpr int kFew = 64;
+
 template <class Tile, int P, bool FOLD, class Acc, class Hook>
 __device__ __forceinline__ void held_product(Operand<Held> a, int64_t size_a, Operand<Held> b, int64_t size_b,
-                                             int64_t k, Acc& acc, Hook&& hook) {
+                                             int64_t k, bool few, Acc& acc, Hook&& hook) {
   if constexpr (P == 2) {
     Operand<Held> low = a;
     low.p += size_a;
+    if constexpr (Tile::MI * Tile::NI <= 4) {  // 64 tiles
+      if (few) {
+        Operand<Held> lows = b;
+        lows.p += size_b;
+        Tile::run(low, lows, 0, k, acc);
+      }
+    }
     Tile::run(low, b, 0, k, acc);
     low = b;
     low.p += size_b;
@@ -338,7 +352,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
   f32x4 acc[Tile::MI][Tile::NI] = {};
   // B: beta A, its own transpose, comes into the sums from the stages that
   // hold it
-  held_product<Tile, P, !POLY && BT <= 128>(a, size, b, size, ld, acc, [&](LdsPtr la, int64_t k) {
+  held_product<Tile, P, !POLY && BT <= 128>(a, size, b, size, ld, sh.m <= kFew, acc, [&](LdsPtr la, int64_t k) {
     if constexpr (POLY) Tile::add_b(la, k, i0, beta, acc);
   });
   // Columns m .. lda - 1 get zeros; the mirrored tile gets the same values.
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_step(Table tab, NsTiles til
   f32x4 acc[Tile::MI][Tile::NI] = {};
   // a X comes into the sums from the stages that hold it: with the tile read
   // again after the sums, every unit waited for memory at once
-  held_product<Tile, P, false>(a, sh.a_size, b, sh.x_size, sh.m, acc,
+  held_product<Tile, P, false>(a, sh.a_size, b, sh.x_size, sh.m, sh.m <= kFew, acc,
                         [&](LdsPtr la, int64_t k) { Tile::add_b(la, k, i0, a_coef, acc); });
   O* out = nullptr;
   int64_t ld_out = 0;

@@ -77,19 +77,21 @@ def _instructions(a, b, acc, fold):
     return (acc + part).float().double() if fold else part
 
 
-def _product(a, b, fold=None):
+def _product(a, b, fold=None, lows=False):
     """Of (high, low) pairs, summed in fp32: rounded once, or with `fold` as the
-    instructions do it (the small products first)."""
+    instructions do it (the small products first); low x low with `lows`."""
     if fold is None:
         return (a[0] @ b[0] + a[0] @ b[1] + a[1] @ b[0]).float().double()
     acc = torch.zeros(a[0].shape[0], b[0].shape[1], dtype=torch.float64)
+    if lows:
+        acc = _instructions(a[1], b[1], acc, 0)
     acc = _instructions(a[0], b[1], _instructions(a[1], b[0], acc, 0), 0)
     return _instructions(a[0], b[0], acc, fold)
 
 
-def model(u, coeffs, eps, hold, fault=None, fold=None):
-    """O as the kernels round it (before the output's rounding).  fold: sums as
-    _product gives them.  fault: "no low half", or "folded" (the low half taken from another rounding of
+def model(u, coeffs, eps, hold, fault=None, fold=None, lows=False):
+    """O as the kernels round it (before the output's rounding).  fold, lows:
+    products as _product gives them.  fault: "no low half", or "folded" (the low half taken from another rounding of
     the value than the one that is stored, in B)."""
     x = u.double()
     flip = u.shape[0] > u.shape[1]
@@ -100,13 +102,13 @@ def model(u, coeffs, eps, hold, fault=None, fold=None):
     for k, (a, b, c) in enumerate(coeffs):
         a, b, c = float(a), float(b), float(c)
         # A by a power of two
-        g = _held((_product(p, (p[0].t(), p[1].t()), fold) * (2.0 ** 12 / scale ** 2)), hold, own)
+        g = _held((_product(p, (p[0].t(), p[1].t()), fold, lows) * (2.0 ** 12 / scale ** 2)), hold, own)
         # B = alpha (beta A + A A), alpha no power of two
         alpha = torch.tensor(c * 2.0 ** 11 / 2.0 ** 24).float().double()
         beta = torch.tensor(b * 2.0 ** 12 / c).float().double()
-        s = (_product(g, g, fold) + beta * (g[0] + g[1])).float().double()
+        s = (_product(g, g, fold, lows) + beta * (g[0] + g[1])).float().double()
         q = _held((alpha * s).contiguous(), hold, fault)
-        new = (a * 2.0 ** 11 * (p[0] + p[1]) + _product(q, p, fold)).float().double() * 2.0 ** -11
+        new = (a * 2.0 ** 11 * (p[0] + p[1]) + _product(q, p, fold, lows)).float().double() * 2.0 ** -11
         if k + 1 < len(coeffs):
             p = _held(new, hold, own)
     out = new / scale
