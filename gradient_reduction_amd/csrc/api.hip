@@ -1115,14 +1115,15 @@ dc_status check_rows(const Rows& m) {
   return DC_OK;
 }
 
-// Whether the matrices share an element.  Column ranges of rows with one
-// stride interleave without sharing any.
+// Whether the matrices share an element.  Between rows of one stride there may
+// be others' columns, or a single row.
 bool share(const Rows& a, const Rows& b) {
   if (a.p == nullptr || b.p == nullptr || a.rows <= 0 || b.rows <= 0) return false;
   const int64_t na = ((a.rows - 1) * a.ld + a.cols) * a.bytes, nb = ((b.rows - 1) * b.ld + b.cols) * b.bytes;
   if (!overlaps(a.p, na, b.p, nb)) return false;
-  const uint64_t step = (uint64_t)a.ld * a.bytes;
-  if (step != (uint64_t)b.ld * b.bytes) return true;
+  const uint64_t step_a = (uint64_t)a.ld * a.bytes, step_b = (uint64_t)b.ld * b.bytes;
+  if (a.rows > 1 && b.rows > 1 && step_a != step_b) return true;
+  const uint64_t step = b.rows == 1 ? step_a : step_b;
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
   const uint64_t d = pb >= pa ? (pb - pa) % step : (step - (pa - pb) % step) % step;
   return d < (uint64_t)a.cols * a.bytes || d + (uint64_t)b.cols * b.bytes > step;

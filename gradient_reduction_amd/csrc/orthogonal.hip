@@ -268,7 +268,7 @@ constexpr int kFold = 4;
 // Up to kFew singular values do not average what is left out: their products
 // of the low halves (2^-24 of a value, of one sign on A's diagonal) are taken
 // too (64 tiles).  Without them 1 x 300 was off by 6.9e-7 of |O|_F and 4 x 1000
-// by 1.3e-6, with them by 5.5e-7 and 9.8e-7; nine odd matrices, three of them
+// by 1.3e-6, with them by 5.5e-7 and 9.8e-7; nine odd matrices, two of them
 // with few, take 231.7 us so, 230.3 without.
 constexpr int kFew = 64;
 

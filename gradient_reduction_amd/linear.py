@@ -111,28 +111,29 @@ def forward(x, w, bias=None, residual=None, act="none", save_pre=False, out=None
 
 def _share(a, ld_a, b, ld_b):
     """Whether two operands (vectors, or matrices with their row strides)
-    share an element; column ranges of rows with one stride may interleave."""
+    share an element.  Between rows of one stride there may be others' columns,
+    or a vector."""
     if a.numel() == 0 or b.numel() == 0:
         return False
     ea, eb, pa, pb = a.element_size(), b.element_size(), a.data_ptr(), b.data_ptr()
     ca, cb = a.shape[-1] * ea, b.shape[-1] * eb
     ra, rb = a.numel() // a.shape[-1], b.numel() // b.shape[-1]
-    step = ld_a * ea
-    if pa >= pb + (rb - 1) * ld_b * eb + cb or pb >= pa + (ra - 1) * step + ca:
+    step_a, step_b = ld_a * ea, ld_b * eb
+    if pa >= pb + (rb - 1) * step_b + cb or pb >= pa + (ra - 1) * step_a + ca:
         return False
-    if step != ld_b * eb:
+    step = step_a if rb == 1 else step_b
+    if ra > 1 and rb > 1 and step_a != step_b:
         return True
     d = (pb - pa) % step
     return d < ca or d + cb > step
 
 
-def _apart(outs, ins):
-    """Refuses a written operand that shares an element with another one;
-    entries are (name, tensor, row stride)."""
-    for k, (name, o, ld) in enumerate(outs):
-        for other, t, ld_t in outs[:k] + ins:
-            if _share(o, ld, t, ld_t):
-                raise ValueError(f"{name} and {other} overlap")
+def _apart(out, ins):
+    """Refuses a written operand that shares an element with one of the others;
+    each is (name, tensor, row stride)."""
+    for other, t, ld in ins:
+        if _share(out[1], out[2], t, ld):
+            raise ValueError(f"{out[0]} and {other} overlap")
 
 
 def _bias_act(dy, pre, act, dz, db, accumulate, need_dz, need_db, grad_dtype):
@@ -194,7 +195,7 @@ def backward(dy, x, w, pre=None, act="none", dw=None, db=None, accumulate=False,
     """(dx, dw, db) of forward() from dy, the gradient of y; the residual's
     gradient is dy.  dw [N, K] and db [N] are float32 or x's dtype; given ones
     are written, or added to with accumulate; db only when given.  They may
-    share no element with each other or with what is read.  dz = dy act'(pre)
+    share no element with each other, x or w, nor db with dy or pre.  dz = dy act'(pre)
     is rounded once to x's dtype on its way into the products.  A call that is
     refused has changed nothing."""
     with on(x.device, stream):
@@ -229,25 +230,21 @@ def _backward(dy, x, w, pre, act, dw, db, accumulate, need_dx, need_dw, grad_dty
     if act != "none" or db is not None:
         dz, db, elementwise = _bias_act(dy, pre, act, None, db, accumulate and db is not None, True, False,
                                         grad_dtype)
-    outs = ([("dw", dw, ld_dw)] if given else []) + ([("db", db, N)] if db is not None else [])
-    if outs:
-        ins = [("dy", dy, ld_dy)]
-        if act != "none":
-            ins.append(("pre", pre, pre.stride(0) if T > 1 else N))
-        if need_dw:
-            ins.append(("x", x, ld_x))
-        if need_dx:
-            ins.append(("w", w, ld_w))
-        _apart(outs, ins)
+    products = ([("x", x, ld_x)] if need_dw else []) + ([("w", w, ld_w)] if need_dx else [])
+    if given:       # dy and pre are read before it is written, unless dy is dz
+        _apart(("dw", dw, ld_dw), products + ([("dy", dy, ld_dy)] if act == "none" else []))
+    if db is not None:
+        _apart(("db", db, N), products + [("dy", dy, ld_dy)] + ([("dw", dw, ld_dw)] if given else [])
+               + ([("pre", pre, pre.stride(0) if T > 1 else N)] if act != "none" else []))
     dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
     dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
-    products = (need_dx and T) or need_dw
-    nbytes = dc.dc_linear_backward_workspace(dtype, T, N, K) if products else 0
+    any_product = (need_dx and T) or need_dw
+    nbytes = dc.dc_linear_backward_workspace(dtype, T, N, K) if any_product else 0
     ws = workspace(nbytes, dev)
 
     def launch():
         elementwise()
-        if products:
+        if any_product:
             dc.dc_linear_backward(dtype, T, N, K, dz, ld_dz, w, ld_w, x, ld_x, dx, K, dw_type, dw, ld_dw,
                                   1 if accumulate else 0, ws, nbytes)
 

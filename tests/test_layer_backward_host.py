@@ -1,7 +1,9 @@
 """What a layer's backward refuses, and when (no GPU): launches are replaced
 by a record of them, and every refusal comes before the first."""
 import contextlib
+import random
 
+import numpy as np
 import pytest
 import torch
 
@@ -53,19 +55,19 @@ def test_a_bias_gradient_over_another_operand(launches, name, act):
             assert not launches
 
 
-@pytest.mark.parametrize("name", ["dy", "x", "w", "pre"])
-def test_a_weight_gradient_over_another_operand(launches, name):
+@pytest.mark.parametrize("act, name", [("gelu", "x"), ("gelu", "w"), ("none", "dy"), ("none", "x")])
+def test_a_weight_gradient_over_another_operand(launches, act, name):
     flat = torch.zeros(100)
     o = operands()
     rows, cols = o[name].shape
     o[name] = flat[30:30 + rows * cols].view(rows, cols)
     for at in (30, 30 + rows * cols - 1, 31 - N * K):
         with pytest.raises(ValueError, match="dw"):
-            call(o, dw=flat[at:at + N * K].view(N, K), db=torch.zeros(N))
+            call(o, act=act, dw=flat[at:at + N * K].view(N, K), db=torch.zeros(N))
         assert not launches
     # next to it
     for at in (30 + rows * cols, 30 - N * K):
-        call(o, dw=flat[at:at + N * K].view(N, K), db=torch.zeros(N))
+        call(o, act=act, dw=flat[at:at + N * K].view(N, K), db=torch.zeros(N))
     assert launches == ["dc_bias_act_backward", "dc_linear_backward"] * 2
 
 
@@ -78,6 +80,26 @@ def test_interleaved_columns_are_apart(launches):
     with pytest.raises(ValueError, match="dw"):
         call(o, dw=wide[:, K - 1:2 * K - 1], db=torch.zeros(N))
     assert len(launches) == 2
+
+
+def test_gradients_where_nothing_is_read_any_more(launches):
+    """Between another operand's rows; over dy and pre, which the elementwise
+    part has read; over x or w, where the other gradient alone is made."""
+    o = operands()
+    wide = torch.zeros(N, K + N)
+    call(o, dw=wide[:, :K], db=wide[0, K:])
+    call(o, dw=wide[:, :K], db=wide[N - 2, K:])
+    for at in (K - 1, K + 1):       # wide's elements K - 1 and K + N
+        with pytest.raises(ValueError, match="db"):
+            call(o, dw=wide[:, :K], db=wide.view(-1)[at:at + N])
+    flat = torch.zeros(100)
+    o["dy"], o["pre"] = flat[:T * N].view(T, N), flat[50:50 + T * N].view(T, N)
+    call(o, dw=flat[:N * K].view(N, K))
+    call(o, dw=flat[45:45 + N * K].view(N, K))
+    o = operands()
+    call(o, dw=o["w"], need_dx=False)
+    call(o, db=o["x"].view(-1)[:N], need_dw=False)
+    assert launches.count("dc_linear_backward") == 6
 
 
 def test_refusals_of_any_kind_come_first(launches, monkeypatch):
@@ -170,3 +192,38 @@ def test_a_layer_touches_its_own_replicas_accumulators_only(launches, monkeypatc
     red.reduce(None, 0)
     red.accumulate(None, 0)
     assert rows() == [10, 10, 10]
+
+
+def elements(at, rows, cols, ld):
+    return {at + r * ld + c for r in range(rows) for c in range(cols)}
+
+
+def test_overlap_is_found_exactly():
+    """The library's check and the one before it against the elements
+    themselves: exact for rows of one stride and for a single row; matrices of
+    different strides may not interleave."""
+    rng = random.Random(5)
+    flat = torch.zeros(400)
+    base, far = 1 << 32, 1 << 40
+    coeffs = np.tile(np.array([3.4445, -4.775, 2.0315], np.float32), (5, 1))
+    seen = set()
+    for _ in range(4000):
+        a, b = [(rng.randrange(60), rng.choice([1, 1, 2, 3, 4]), rng.randint(1, 6)) for _ in range(2)]
+        ld = [v[2] + rng.randrange(9) for v in (a, b)]
+        if rng.random() < 0.5:
+            ld = [max(ld)] * 2
+        ea, eb = elements(*a, ld[0]), elements(*b, ld[1])
+        want = bool(ea & eb)
+        if a[1] > 1 and b[1] > 1 and ld[0] != ld[1]:
+            want = max(ea) >= min(eb) and max(eb) >= min(ea)
+        views = [torch.as_strided(flat, v[1:], (d, 1), v[0]) for v, d in ((a, ld[0]), (b, ld[1]))]
+        assert linear._share(views[0], ld[0], views[1], ld[1]) == want, (a, b, ld)
+        m = np.zeros(2, dc.MATRIX_DTYPE)
+        m["rows"], m["cols"] = (a[1], b[1]), (a[2], b[2])
+        m["out"], m["ld_out"] = (base + 4 * a[0], far), (ld[0], b[2])
+        m["grad"], m["ld_grad"] = (2 * far, base + 4 * b[0]), (a[2], ld[1])
+        with pytest.raises(dc.DCError) as e:       # the workspace is too small
+            dc.dc_orthogonalize(dc.DC_F32, 0, m, 2, 5, coeffs, 1e-7, 3 * far, 16, 0)
+        assert ("overlap" in str(e.value)) == want, (a, b, ld, e.value)
+        seen.add((want, a[1] == 1, b[1] == 1, ld[0] == ld[1]))
+    assert len(seen) == 16
