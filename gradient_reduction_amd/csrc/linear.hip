@@ -11,8 +11,11 @@
 namespace dc {
 namespace {
 
-// Activations and their slopes in fp32, to about 2^-21 of the result, from
-// the hardware's 2^x and 1/x: with the library's exp, erfc and correctly
+// Activations and their slopes in fp32 from the hardware's 2^x and 1/x:
+// activations to 2^-22 of the larger of argument and result, slopes to 2^-20
+// (over -15 .. 15).  GELU's negative tail is off by about 2^-20 of itself at -5,
+// 2^-19 at -9 and 2^-18 at -13, from the rounding of v^2; slopes have no such
+// bound near their zeros.  With the library's exp, erfc and correctly
 // rounded division the elementwise backward was bound by its arithmetic (129
 // us on 8192 x 11008 bf16 where its bytes take 84).
 
@@ -126,9 +129,10 @@ struct ProductArgs {
 
 // One tile of C = A B (product.h) and its epilogue; y = x wT, dx = dz w and dw
 // = dzT x are its three kinds.  Bound by the matrix cores where the tiles fill
-// the chip: 8192 x 11008 over 4096 bf16 takes 690 us with silu and pre kept
-// (1.07 PFLOP/s), dx 585 (1.26) and dw added to fp32 about 695 (1.06: 688 tiles
-// of 256 are 2.7 rounds over the units, paid as 3).  Tiles are walked in bands
+// the chip: 8192 x 11008 over 4096 bf16 takes 690 to 715 us with silu and pre
+// kept (1.05 PFLOP/s), dx 565 (1.31) and dw added to fp32 680 (1.09: 688 tiles of
+// 256 are 2.7 rounds over the units, paid as 3), the first calls after idling a
+// quarter more.  Tiles are walked in bands
 // of eight rows, one XCD's workgroups on neighbours, so that an L2 serves what
 // they share.  Odd fp32 rows go through registers: 777 x 1003 over 515 takes
 // 23 us, bound by the latency of a tile's 17 stages.
@@ -353,8 +357,9 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 // workgroup per 64 chunks of 16 bytes of columns and strip, a wave to a row
 // and two rows in flight per wave.  dy and pre are read past the caches, dz
 // is left in them for the products that read it next (8192 x 11008 bf16 when it
-// was chosen: 103 us so, 155 us with ordinary loads, 109 us with the stores past
-// them too).  Bound by those bytes: 541 MB in 109 us, 5.0 TB/s, with silu.  The
+// was chosen, before the activations' ranges were widened: 103 us so, 155 us with
+// ordinary loads, 109 us with the stores past them too).  Bound by those bytes:
+// 541 MB in 110 to 115 us, 4.7 to 4.9 TB/s, with silu.  The
 // strips' sums go to partial[strip][n] and are added in order by
 // k_column_join, or straight to db when there is one strip.
 template <class T, class G, int ACT>

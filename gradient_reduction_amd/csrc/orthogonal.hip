@@ -29,12 +29,13 @@ constexpr int64_t kNormSpan = 16384;  // elements per partial sum, at least
 // What X, A and B are held in: one fp16 (11 bits), or two, a value and what it
 // leaves (22 bits), multiplied as high high + high low + low high (three
 // products of 16 bits take a fifth of one product of fp32 on these matrix
-// cores).  One leaves 1.3e-3 to 1.6e-3 of |O|_F after five steps where the
-// smaller side is kPairUnder or more, less than the rounding of O to bf16; on
-// smaller matrices, whose few singular values do not average the roundings, it
-// left 8e-3 at worst, and there two cost little.  48 matrices of 1024 x 1024
-// to 4096 x 1024 with their momenta and fp32 weights take 2.9 ms with one, 6.9
-// with two, and the weights are off by 3.2e-6 and 1.3e-7.
+// cores).  Two leave about 1e-6 of |O|_F after five steps (0.5e-6 to 1.6e-6, single
+// small matrices up to 2e-6); the same steps in fp32 leave 0.3e-6 to 3.6e-6.  One leaves 1.3e-3 to 1.6e-3 where the smaller
+// side is kPairUnder or more, less than the rounding of O to bf16; on smaller
+// matrices, whose few singular values do not average the roundings, it left 8e-3
+// at worst, and there two cost little.  48 matrices of 1024 x 1024 to 4096 x 1024
+// with their momenta and fp32 weights take 2.9 ms with one, 6.8 with two, and the
+// weights are off by 3.2e-6 and 4.1e-8.
 using Held = _Float16;
 constexpr int32_t kPairUnder = 256;
 
@@ -329,9 +330,10 @@ __device__ __forceinline__ void triangle_tile(int32_t t, int32_t nt, int32_t& ti
 // A = alpha X XT (POLY false: src = X, dst = A), or B = alpha (beta A + A A)
 // (POLY true: src = A, dst = B; A is its own transpose).  Bound by the matrix
 // cores: the four 4096 x 4096 and three 4096 x 11008 matrices of a 7B layer take
-// 787 us for A and 484 us for B, 1.12 and 1.05 PFLOP/s of the tiles that are
-// computed, half of the whole product; 952 tiles of 256 are 3.7 rounds.  One
-// 1024 x 1024 matrix takes 10 us each, a tile's latency.
+// 787 us for A and 484 us for B with one fp16, 1.12 and 1.05 PFLOP/s of the tiles
+// that are computed, half of the whole product, and 2250 and 1410 us with pairs,
+// 1.17 and 1.08; 952 tiles of 256 are 3.7 rounds.  One 1024 x 1024 matrix takes 10
+// us each, 18 with pairs, a tile's latency.
 template <int P, int BT, int WM, int WN, int S, bool POLY>
 __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsTiles tiles, Held* planes, int32_t next,
                                                                float alpha, float beta) {
@@ -370,9 +372,10 @@ __global__ void __launch_bounds__(WM * WN * 64) k_ns_symmetric(NsPlanes tab, NsT
 }
 
 // X <- beta (a X + B X) into the other X plane, or out of it in the last step.
-// The same 7B layer takes 1528 us, 1.09 PFLOP/s; 48 matrices of 1024 x 1024 to
-// 4096 x 1024 in pairs 623 us, 0.99 (a tile's beginning and end are a fifth of
-// its 48 stages), their last step with the weights 795 us.
+// The same 7B layer takes 1528 us with one fp16, 1.09 PFLOP/s, and 4430 with
+// pairs, 1.12; 48 matrices of 1024 x 1024 to 4096 x 1024 in pairs 621 us, 0.99 (a
+// tile's beginning and end are a fifth of its 48 stages), their last step with
+// the weights 792 us.
 enum : int { kNsNext = 0, kNsOut = 1, kNsWeight = 2 };
 
 template <int P, class O, int BT, int WM, int WN, int S, int LAST, class Table>

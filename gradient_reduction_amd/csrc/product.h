@@ -265,8 +265,8 @@ struct TileProduct {
 #pragma unroll
     for (int i = 0; i < MI; ++i) fa[i] = MapA::fragment(la, base_a, i, ks);
     // All reads first: left to the compiler they trickle between the products,
-    // with fewer in flight (8192^3: 1115, 1270 and 1215 TFLOP/s for the three
-    // kinds of product; 1140, 1340 and 1310 so).
+    // with fewer in flight (8192^3 when it was chosen: 1115, 1270 and 1215
+    // TFLOP/s for the three kinds of product; 1140, 1340 and 1310 so).
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < MI; ++i)

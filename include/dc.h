@@ -911,9 +911,9 @@ dc_status dc_orthogonalize_form(int32_t dtype, int32_t out_dtype, int32_t hold, 
  * singular values go through the odd polynomials a s + b s^3 + c s^5.
  * X, A and B are held in fp16, by powers of two that the polynomials' bounds
  * keep from overflowing, with fp32 sums: a pair of them (22 bits), which leaves
- * about 5e-7 of |out|_F, or one (11 bits), which leaves about 1.5e-3 on
- * matrices of 256 and more a side, up to 1e-2 on small ones, and takes a third
- * of the products.  hold DC_HOLD_AUTO takes pairs where the gradients or the
+ * about 1e-6 of |out|_F (up to 2e-6; the same steps in fp32 leave 0.3e-6 to
+ * 3.6e-6), or one (11 bits), which leaves about 1.5e-3 on matrices of 256 and more a side, up
+ * to 1e-2 on small ones, and takes a third of the products.  hold DC_HOLD_AUTO takes pairs where the gradients or the
  * output are fp32 or the smaller side is under 256, else one; DC_HOLD_ONE and
  * DC_HOLD_PAIR are the caller's choice for the whole list.  |X|_F is summed in
  * fp64.  A zero matrix gives zero (NaN when eps is 0); a NaN or
