@@ -107,8 +107,11 @@ class Zero1FlushExecutor:
                                   stream)
 
     def fetch_metadata(self) -> None:
-        """Copy the owner map and partition lists to the host (synchronizes);
-        the probe and the ratio report use them."""
+        """Copy the owner map and partition lists to the host (synchronizes the
+        device: the map may have been built on another stream); the probe and
+        the ratio report use them."""
+        if self.d_owner.is_cuda:
+            self.torch.cuda.synchronize(self.d_owner.device)
         self.h_owner = self.d_owner[:self.P].cpu().numpy()
         self.h_pid_off = self.d_pid_off.cpu().numpy()
         self.h_pids = self.d_pids[:int(self.h_pid_off[-1])].cpu().numpy()

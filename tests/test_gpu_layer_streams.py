@@ -3,7 +3,8 @@ own: a replica's gradients are in its row whatever the other streams do."""
 import pytest
 import torch
 
-from gradient_reduction_amd import dc, deferred
+from gradient_reduction_amd import dc, deferred, executor
+from synth import workloads as wl
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,27 @@ def test_a_replica_without_layers():
     acc = red.acc.cpu()
     assert bool((acc[0] == 2).all()) and bool((acc[1] == 2).all()) and not acc[2].any()
     assert bool(torch.isfinite(out).all()) and torch.equal(out[0], out[2])
+
+
+def test_registration_waits_for_an_owner_map_on_another_stream():
+    """The map is built behind other work on a side stream; the matrices'
+    rows are the owners that it gives."""
+    sizes = [(40, 30), (64, 64), (7, 200), (90, 11)]
+    w = wl.custom_flush("update", 4, wl.DT_F32, [a * b for a, b in sizes], capacity=9000, pre_div=1, value_seed=3)
+    plain = executor.from_workload(w, reduce_to_owner=True)
+    plain.build_owner_map()
+    plain.fetch_metadata()
+    ex = executor.from_workload(w, reduce_to_owner=True)
+    ex.d_owner.fill_(-1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.ones(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = busy @ busy * 2.0 ** -12
+    ex.build_owner_map(stream=side.cuda_stream)
+    ts = {p: torch.zeros(*s, device="cuda") for p, s in enumerate(sizes)}
+    ex.register_matrices(ts, {p: torch.zeros_like(v) for p, v in ts.items()})
+    assert plain.h_owner.max() > 0 and ex.h_owner.tolist() == plain.h_owner.tolist()
+    assert ex.m_rows.tolist() == [max(int(o), 0) for o in plain.h_owner]
