@@ -109,31 +109,25 @@ def forward(x, w, bias=None, residual=None, act="none", save_pre=False, out=None
     return out if pre is None else (out, pre)
 
 
-def _share(a, ld_a, b, ld_b):
-    """Whether two operands (vectors, or matrices with their row strides)
-    share an element.  Between rows of one stride there may be others' columns,
-    or a vector."""
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    ea, eb, pa, pb = a.element_size(), b.element_size(), a.data_ptr(), b.data_ptr()
-    ca, cb = a.shape[-1] * ea, b.shape[-1] * eb
-    ra, rb = a.numel() // a.shape[-1], b.numel() // b.shape[-1]
-    step_a, step_b = ld_a * ea, ld_b * eb
-    if pa >= pb + (rb - 1) * step_b + cb or pb >= pa + (ra - 1) * step_a + ca:
-        return False
-    step = step_a if rb == 1 else step_b
-    if ra > 1 and rb > 1 and step_a != step_b:
-        return True
-    d = (pb - pa) % step
-    return d < ca or d + cb > step
+def _span(name, t, rows, cols, ld, size):
+    """Where an operand of `size`-byte elements lies: (name, first byte, end,
+    bytes of a row, bytes from row to row, rows)."""
+    p, step = t.data_ptr(), ld * size
+    return name, p, p + (rows - 1) * step + cols * size, cols * size, step, rows
 
 
 def _apart(out, ins):
-    """Refuses a written operand that shares an element with one of the others;
-    each is (name, tensor, row stride)."""
-    for other, t, ld in ins:
-        if _share(out[1], out[2], t, ld):
-            raise ValueError(f"{out[0]} and {other} overlap")
+    """Refuses a written operand (a _span) that shares an element with one of
+    the others.  Between rows of one stride there may be others' columns, or a
+    vector."""
+    name, pa, end_a, ca, step_a, ra = out
+    for other, pb, end_b, cb, step_b, rb in ins:
+        if pa >= end_b or pb >= end_a or not ra or not rb:
+            continue
+        step = step_a if rb == 1 else step_b
+        d = (pb - pa) % step
+        if (ra > 1 and rb > 1 and step_a != step_b) or d < ca or d + cb > step:
+            raise ValueError(f"{name} and {other} overlap")
 
 
 def _bias_act(dy, pre, act, dz, db, accumulate, need_dz, need_db, grad_dtype):
@@ -230,12 +224,19 @@ def _backward(dy, x, w, pre, act, dw, db, accumulate, need_dx, need_dw, grad_dty
     if act != "none" or db is not None:
         dz, db, elementwise = _bias_act(dy, pre, act, None, db, accumulate and db is not None, True, False,
                                         grad_dtype)
-    products = ([("x", x, ld_x)] if need_dw else []) + ([("w", w, ld_w)] if need_dx else [])
-    if given:       # dy and pre are read before it is written, unless dy is dz
-        _apart(("dw", dw, ld_dw), products + ([("dy", dy, ld_dy)] if act == "none" else []))
-    if db is not None:
-        _apart(("db", db, N), products + [("dy", dy, ld_dy)] + ([("dw", dw, ld_dw)] if given else [])
-               + ([("pre", pre, pre.stride(0) if T > 1 else N)] if act != "none" else []))
+    if given or db is not None:
+        size = 2 if dtype == dc.DC_BF16 else 4
+        grads = [_span("dw", dw, N, K, ld_dw, 2 if dw_type == dc.DC_BF16 else 4)] if given else []
+        products = [_span("x", x, T, K, ld_x, size)] if need_dw else []
+        if need_dx:
+            products.append(_span("w", w, N, K, ld_w, size))
+        first = [_span("dy", dy, T, N, ld_dy, size)]
+        if given:       # dy and pre are read before it is written, unless dy is dz
+            _apart(grads[0], products + first if act == "none" else products)
+        if db is not None:
+            if act != "none":
+                first.append(_span("pre", pre, T, N, pre.stride(0) if T > 1 else N, size))
+            _apart(_span("db", db, 1, N, N, db.element_size()), products + first + grads)
     dz, ld_dz = _rows("dz", dz, T, N, dt, dev)
     dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
     any_product = (need_dx and T) or need_dw

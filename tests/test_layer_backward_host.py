@@ -217,7 +217,9 @@ def test_overlap_is_found_exactly():
         if a[1] > 1 and b[1] > 1 and ld[0] != ld[1]:
             want = max(ea) >= min(eb) and max(eb) >= min(ea)
         views = [torch.as_strided(flat, v[1:], (d, 1), v[0]) for v, d in ((a, ld[0]), (b, ld[1]))]
-        assert linear._share(views[0], ld[0], views[1], ld[1]) == want, (a, b, ld)
+        spans = [linear._span("ab"[k], t, *v[1:], d, 4) for k, (t, v, d) in enumerate(zip(views, (a, b), ld))]
+        with pytest.raises(ValueError, match="a and b overlap") if want else contextlib.nullcontext():
+            linear._apart(spans[0], spans[1:])
         m = np.zeros(2, dc.MATRIX_DTYPE)
         m["rows"], m["cols"] = (a[1], b[1]), (a[2], b[2])
         m["out"], m["ld_out"] = (base + 4 * a[0], far), (ld[0], b[2])
