@@ -812,7 +812,8 @@ dc_status dc_stream_rows_shaped(const void* src, int64_t src_ld_vec, int32_t row
  * faster.  What an output's row holds between its length and its stride stays
  * as it was.  Outputs must not overlap inputs or other outputs (DC_ERR_ARG)
  * except where said; two matrices that interleave as column ranges of rows
- * with one common stride do not overlap.  Sizes are at most 2^28 and the
+ * with one common stride do not overlap, nor does a single row that lies between
+ * another matrix's rows.  Sizes are at most 2^28 and the
  * elements of one matrix at most 2^36 (2^20 and 2^34 for dc_matrix), else
  * DC_ERR_SHAPE.
  * A workspace is device memory, 16-byte aligned, of at least the bytes that
