@@ -1227,6 +1227,49 @@ dc_status check_disjoint(std::vector<Named>& all, bool in_place) {
   return DC_OK;
 }
 
+// A list of gradients; with `clips` what it writes too, and the scalars.
+dc_status check_gradients(const dc_gradient* grads, int32_t num, bool clips, const double* squares, const float* norm,
+                          const float* coef) {
+  dc_status st;
+  if (num < 0 || num > 1 << 20) return fail(DC_ERR_ARG, "num=%d outside [0, 2^20]", num);
+  if (num > 0 && grads == nullptr) return fail(DC_ERR_NULL, "grads is NULL");
+  const struct {
+    const char* name;
+    const void* p;
+    int32_t bytes;
+  } scalars[3] = {{"squares", squares, 8}, {"norm", norm, 4}, {"coef", coef, 4}};
+  for (const auto& s : scalars)
+    if (reinterpret_cast<uintptr_t>(s.p) % s.bytes != 0) return fail(DC_ERR_ALIGN, "%s is not aligned", s.name);
+  std::vector<Named> all;
+  try {
+    all.reserve((size_t)num * 2 + 3);
+  } catch (const std::bad_alloc&) {
+    return fail(DC_ERR_UNSUPPORTED, "no host memory to check %d gradients", num);
+  }
+  for (int32_t k = 0; k < num; ++k) {
+    const dc_gradient& g = grads[k];
+    if ((st = check_dtype(g.dtype))) return st;
+    if (g.rows < 0 || g.cols < 0) return fail(DC_ERR_ARG, "gradient %d: %lld x %lld", k, (long long)g.rows, (long long)g.cols);
+    if (g.counted < 0 || g.counted > g.rows)
+      return fail(DC_ERR_ARG, "gradient %d: %lld of %lld rows counted", k, (long long)g.counted, (long long)g.rows);
+    if (g.rows == 0 || g.cols == 0) continue;
+    if (g.rows > kMaxElements || g.cols > kMaxElements || g.rows > kMaxElements / g.cols)
+      return fail(DC_ERR_SHAPE, "gradient %d: %lld x %lld exceeds 2^36 elements", k, (long long)g.rows, (long long)g.cols);
+    const Rows in{"grad", g.grad, g.rows, g.cols, g.ld_grad, elem_bytes(g.dtype)};
+    const Rows out{"out", g.out, g.rows, g.cols, g.ld_out, elem_bytes(g.dtype)};
+    if ((st = check_rows(in)) || (clips && (st = check_rows(out)))) {
+      g_last_error = "gradient " + std::to_string(k) + ": " + g_last_error;
+      return st;
+    }
+    all.push_back({in, k, false});
+    if (clips) all.push_back({out, k, true});
+  }
+  for (int32_t k = 0; k < 3; ++k)
+    if (scalars[k].p)
+      all.push_back({Rows{scalars[k].name, scalars[k].p, 1, 1, 1, scalars[k].bytes}, num + k, !(clips && k == 0)});
+  return check_disjoint(all, true);
+}
+
 // The checks that both list operators share.
 dc_status check_list(int32_t dtype, int32_t out_dtype, const dc_matrix* mats, int32_t num, bool update) {
   dc_status st;
@@ -1463,6 +1506,40 @@ dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, int32_t hold,
   a.lr_scale = lr_scale;
   a.workspace = workspace;
   return hip_status(dc::launch_ns(a, static_cast<hipStream_t>(stream)), "update launch");
+}
+
+dc_status dc_grad_clip_workspace(int64_t* bytes) {
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::clip_workspace();
+  return ok();
+}
+
+dc_status dc_grad_norm(const dc_gradient* grads, int32_t num, int32_t accumulate, double* squares,
+                       float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  dc_status st;
+  if (accumulate != 0 && accumulate != 1) return fail(DC_ERR_ARG, "accumulate=%d", accumulate);
+  if (squares == nullptr && (accumulate || norm == nullptr))
+    return fail(DC_ERR_NULL, accumulate ? "squares is NULL" : "squares and norm are both NULL");
+  if ((st = check_gradients(grads, num, false, squares, norm, nullptr)) ||
+      (st = check_workspace(workspace, workspace_bytes, dc::clip_workspace())))
+    return st;
+  return hip_status(dc::launch_grad_norm(grads, num, accumulate, squares, norm, workspace,
+                                         static_cast<hipStream_t>(stream)),
+                    "gradient norm launch");
+}
+
+dc_status dc_grad_clip(const dc_gradient* grads, int32_t num, const double* squares, float max_norm,
+                       float eps, float* norm, float* coef, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+  dc_status st;
+  if (!(max_norm >= 0)) return fail(DC_ERR_ARG, "max_norm=%g", (double)max_norm);
+  if (!(eps >= 0) || !std::isfinite(eps)) return fail(DC_ERR_ARG, "eps=%g", (double)eps);
+  if ((st = check_gradients(grads, num, true, squares, norm, coef)) ||
+      (st = check_workspace(workspace, workspace_bytes, dc::clip_workspace())))
+    return st;
+  return hip_status(dc::launch_grad_clip(grads, num, squares, max_norm, eps, norm, coef, workspace,
+                                         static_cast<hipStream_t>(stream)),
+                    "clip launch");
 }
 
 }  // extern "C"

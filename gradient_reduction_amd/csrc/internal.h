@@ -243,4 +243,11 @@ void ns_forms(int32_t dtype, int32_t out_dtype, int32_t hold, const dc_matrix* m
               int32_t index, LaunchForm forms[4]);
 hipError_t launch_ns(const NsLaunch& a, hipStream_t stream);
 
+// The global norm of a list of gradients, and clipping by it.
+int64_t clip_workspace();
+hipError_t launch_grad_norm(const dc_gradient* grads, int32_t num, int32_t accumulate, double* squares, float* norm,
+                            void* workspace, hipStream_t stream);
+hipError_t launch_grad_clip(const dc_gradient* grads, int32_t num, const double* squares, float max_norm, float eps,
+                            float* norm, float* coef, void* workspace, hipStream_t stream);
+
 }  // namespace dc

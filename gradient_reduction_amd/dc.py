@@ -38,6 +38,9 @@ TILE_DTYPE = np.dtype([("first", "<i4"), ("last", "<i4"), ("root", "<i4"), ("fla
 MATRIX_DTYPE = np.dtype([("grad", "<u8"), ("out", "<u8"), ("momentum", "<u8"), ("ld_grad", "<i8"),
                          ("ld_out", "<i8"), ("rows", "<i4"), ("cols", "<i4")])
 
+GRADIENT_DTYPE = np.dtype([("grad", "<u8"), ("out", "<u8"), ("ld_grad", "<i8"), ("ld_out", "<i8"), ("rows", "<i8"),
+                           ("cols", "<i8"), ("counted", "<i8"), ("dtype", "<i4"), ("reserved", "<i4")])
+
 
 class dc_probe(ctypes.Structure):
     _fields_ = [("tasks", ctypes.c_int32), ("owner_tasks", ctypes.c_int32),
@@ -114,6 +117,9 @@ _SIGS = {
     "dc_orthogonalize": ([_i32, _i32, _vp, _i32, _i32, _vp, _f32, _vp, _i64, _vp], _i32),
     "dc_muon_update": ([_i32, _i32, _i32, _vp, _i32, _f32, _vp, _f32, _i32, _f32, _i32, _i32, _vp, _f32, _vp,
                         _i64, _vp], _i32),
+    "dc_grad_clip_workspace": ([_vp], _i32),
+    "dc_grad_norm": ([_vp, _i32, _i32, _vp, _vp, _vp, _i64, _vp], _i32),
+    "dc_grad_clip": ([_vp, _i32, _vp, _f32, _f32, _vp, _vp, _vp, _i64, _vp], _i32),
     "dc_round_bf16": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_copy": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_rows": ([_vp, _i64, _i32, _vp, _i64, _i32, _i64, _vp], _i32),
@@ -558,6 +564,28 @@ def dc_muon_update(dtype, weight_dtype, hold, mats, num, lr, lr_scale, mu, neste
     _check("dc_muon_update", lib().dc_muon_update(
         dtype, weight_dtype, hold, mp, num, lr, _dev(lr_scale), mu, nesterov, weight_decay, scale_mode, steps,
         cp, eps, _dev(workspace), workspace_bytes, _stream(stream)))
+
+
+def dc_grad_clip_workspace():
+    """Host only; bytes of workspace."""
+    n = ctypes.c_int64(0)
+    _check("dc_grad_clip_workspace", lib().dc_grad_clip_workspace(ctypes.byref(n)))
+    return n.value
+
+
+def dc_grad_norm(grads, num, accumulate, squares, norm, workspace, workspace_bytes, stream=None):
+    """grads: GRADIENT_DTYPE records (host)."""
+    gp, _a = _host(grads, GRADIENT_DTYPE)
+    _check("dc_grad_norm", lib().dc_grad_norm(gp, num, accumulate, _dev(squares), _dev(norm), _dev(workspace),
+                                              workspace_bytes, _stream(stream)))
+
+
+def dc_grad_clip(grads, num, squares, max_norm, eps, norm, coef, workspace, workspace_bytes, stream=None):
+    """grads: GRADIENT_DTYPE records (host); squares: device double or None."""
+    gp, _a = _host(grads, GRADIENT_DTYPE)
+    _check("dc_grad_clip", lib().dc_grad_clip(
+        gp, num, _dev(squares), max_norm, eps, _dev(norm), _dev(coef), _dev(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def dc_round_bf16(in_, out, n, stream=None):

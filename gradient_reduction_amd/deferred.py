@@ -115,6 +115,28 @@ class DeferredReducer:
                                     ld_out, out_rows, self.M, stream)
         self.micro_batches = 0
 
+    def clip(self, out, ld_out: int, max_norm: float, out_rows: int = 1, eps: float = 1e-6, stream=None):
+        """After reduce(), on its stream: scales the reduced gradients in
+        out[0..out_rows) by min(1, max_norm / (norm + eps)) and returns their global
+        norm before, a float32 scalar tensor; every row holds the same sums, the
+        norm counts the first."""
+        from . import clip
+        import numpy as np
+        if out_rows not in (1, self.W):
+            raise ValueError(f"out_rows={out_rows}: 1 or W={self.W}")
+        if ld_out < self.M:
+            raise ValueError(f"ld_out={ld_out} < M={self.M}")
+        if not isinstance(out, int):
+            have = out.untyped_storage().nbytes() // 4 - out.storage_offset()
+            if out.dtype != self.torch.float32 or out.device != self.acc.device or \
+                    (out_rows - 1) * ld_out + self.M > have:
+                raise ValueError(f"out {tuple(out.shape)} of {out.dtype} on {out.device} with ld_out={ld_out} "
+                                 f"does not hold {out_rows} rows of {self.M}")
+        at = out if isinstance(out, int) else out.data_ptr()
+        rec = np.zeros(1, dc.GRADIENT_DTYPE)
+        rec[0] = (at, at, ld_out, ld_out, out_rows, self.M, 1, dc.DC_F32, 0)
+        return clip.clip_records(rec, max_norm, eps, None, self.acc.device, stream)
+
     def state_dict(self) -> dict:
         """The accumulator's state mid-step: a copy of the slab's M columns
         and the micro-batch count."""

@@ -20,7 +20,8 @@ no per-tile search.
 
 register_matrices + muon_update take the step after the flush: every matrix
 parameter's orthogonalised momentum update (dc_muon_update), read from the
-row that holds its whole reduced gradient.
+row that holds its whole reduced gradient.  clip_gradients comes in between:
+the global norm of what the flush wrote, and clipping by it (dc_grad_clip).
 
 torch supplies device memory and the stream; every step runs in libdc.so.
 """
@@ -83,6 +84,7 @@ class Zero1FlushExecutor:
         self.h_owner: Optional[np.ndarray] = None
         self.map_built = False
         self.m_recs: Optional[np.ndarray] = None    # register_matrices()
+        self.clip_recs = {}                         # clip_gradients(), by row stride
         self.d_tiles = None        # flush plans (plan()), one table for all buckets
         self.tile_begin = None
         self.root_tiles = None
@@ -470,6 +472,84 @@ class Zero1FlushExecutor:
             dc.dc_muon_update(self.dtype, self.m_wtype, held, recs, len(recs), lr, lr_scale, mu,
                               1 if nesterov else 0, weight_decay, mode, steps, table, eps,
                               linear.workspace(nbytes, self.d_owner.device), nbytes)
+
+    # -- clipping by the global norm ----------------------------------------------
+
+    def _clip_records(self, ld_out: int) -> np.ndarray:
+        """Where the flush left every reduced element, as one-row gradients: (row,
+        column, columns, counted), addresses from 0.  A sum that several rows
+        hold is counted on the first."""
+        W, pieces = self.W, []
+        flat = self.d_flat[:self.P].cpu().numpy() if self.zero2 else None
+
+        def whole(rows, col, numel):
+            for k, r in enumerate(rows):
+                pieces.append((r, col, numel, 1 if k == 0 else 0))
+
+        for bk in self.buckets:
+            for off, numel, param, comm in bk.tasks:
+                col = bk.col + off
+                c, step = int(self.comms[comm]["size"]), int(self.comms[comm]["stride"])
+                if comm != 0:
+                    for b in range(W // c):
+                        first = b * c if step == 1 else b
+                        whole(range(first, first + c * step, step), col, numel)
+                elif self.zero2 and self.h_psize[param] > 0:
+                    a, size, e = int(flat[param]), int(self.h_psize[param]), 0
+                    while e < numel:
+                        q = (a + e) // size
+                        n = min(numel, (q + 1) * size - a) - e
+                        whole([q] if q < W else range(W), col + e, n)
+                        e += n
+                elif self.reduce_to_owner and not self.zero2 and self.h_owner[param] >= 0:
+                    whole([int(self.h_owner[param])], col, numel)
+                else:
+                    whole(range(W), col, numel)
+        merged = []
+        for r, col, n, counted in sorted(p for p in pieces if p[2] > 0):
+            if merged and merged[-1][0] == r and merged[-1][3] == counted and merged[-1][1] + merged[-1][2] == col:
+                merged[-1][2] += n
+            else:
+                merged.append([r, col, n, counted])
+        eb = 2 if self.dtype == dc.DC_BF16 else 4
+        recs = np.zeros(len(merged), dc.GRADIENT_DTYPE)
+        for k, (r, col, n, counted) in enumerate(merged):
+            at = (r * ld_out + col) * eb
+            recs[k] = (at, at, n, n, 1, n, counted, self.dtype, 0)
+        return recs
+
+    def clip_gradients(self, slab_out, ld_out: int, max_norm: float, eps: float = 1e-6, stream=None):
+        """Scales the reduced gradients in the flushed slab by min(1, max_norm /
+        (norm + eps)) and returns the global norm before, a float32 scalar tensor
+        (after flush() of every bucket into slab_out, on the same stream).  The
+        norm counts every reduced element once: on its owner's row (or its
+        partition's), an AllReduced one on the first row that holds it, one of a
+        sub-communicator once in each of its blocks, whose sums differ; every row
+        that holds one is scaled.  Comes after build_owner_map; the first call
+        for a row stride reads the map back and synchronizes."""
+        from . import clip
+        if (self.reduce_to_owner or self.zero2) and not self.map_built:
+            raise RuntimeError("clip_gradients() before build_owner_map()")
+        if ld_out not in self.clip_recs:
+            if (self.reduce_to_owner or self.zero2) and self.h_owner is None:
+                self.fetch_metadata()
+            ends = [bk.col + bk.numel for bk in self.buckets]
+            if ends and ld_out < max(ends):
+                raise ValueError(f"ld_out={ld_out} is less than a row with every bucket ({max(ends)})")
+            self.clip_recs[ld_out] = self._clip_records(ld_out)
+        recs = self.clip_recs[ld_out].copy()
+        base = slab_out
+        if not isinstance(slab_out, int):
+            base = slab_out.data_ptr()
+            eb = 2 if self.dtype == dc.DC_BF16 else 4
+            have = slab_out.untyped_storage().nbytes() - slab_out.storage_offset() * slab_out.element_size()
+            end = int((recs["grad"] + recs["cols"].astype(np.uint64) * np.uint64(eb)).max()) if len(recs) else 0
+            if slab_out.element_size() != eb or slab_out.device != self.d_owner.device or end > have:
+                raise ValueError(f"slab_out {tuple(slab_out.shape)} of {slab_out.dtype} on {slab_out.device} "
+                                 f"with ld_out={ld_out} does not hold every bucket")
+        recs["grad"] += np.uint64(base)
+        recs["out"] = recs["grad"]
+        return clip.clip_records(recs, max_norm, eps, None, self.d_owner.device, stream)
 
     # -- one step as a HIP graph --------------------------------------------------
 

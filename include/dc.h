@@ -206,6 +206,28 @@ typedef struct {
   int32_t cols;
 } dc_matrix;
 
+/* One gradient of dc_grad_norm or dc_grad_clip: rows x cols, row-major, in any
+ * order of rows.  64 bytes.
+ *   grad, ld_grad  device: row r starts at grad + r * ld_grad (in elements; any
+ *                  alignment to an element), ld_grad >= cols
+ *   out, ld_out    device, dc_grad_clip's result; may be grad (same ld)
+ *   rows, cols     at least 0
+ *   counted        the first rows, 0 to rows, that the norm counts: 1 for a
+ *                  reduced gradient that every rank's row holds
+ *   dtype          DC_BF16 or DC_F32, of grad and out
+ *   reserved       not read */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t ld_grad;
+  int64_t ld_out;
+  int64_t rows;
+  int64_t cols;
+  int64_t counted;
+  int32_t dtype;
+  int32_t reserved;
+} dc_gradient;
+
 /* Library version string (static storage). */
 const char* dc_version(void);
 
@@ -948,6 +970,42 @@ dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, int32_t hold,
                          float mu, int32_t nesterov, float weight_decay, int32_t scale_mode,
                          int32_t steps, const float* coeffs, float eps, void* workspace, int64_t workspace_bytes,
                          void* stream);
+
+/* ---- Clipping by the global norm -----------------------------------------
+ *
+ * Between the reduction and the update: over a list of gradients of both
+ * dtypes, as the flush or the deferred reduce left them, the global norm
+ *   n = sqrt(sum over the counted rows of every gradient of g^2)
+ * and
+ *   c = n + eps <= max_norm ? 1 : max_norm / (n + eps),   out = c g
+ * over all rows.  Squares and sums are fp64, in an order fixed by the sizes; c is rounded
+ * once to fp32 and c g once to the dtype.  An infinity among the counted
+ * gradients gives c = 0 (and NaN where it stands), a NaN gives NaN throughout:
+ * read *norm to pass such a step over.  Rules of the section above hold, with
+ * 2^36 elements per gradient and 2^44 per row stride. */
+
+/* Bytes of workspace of dc_grad_norm and dc_grad_clip.  Host only. */
+dc_status dc_grad_clip_workspace(int64_t* bytes);
+
+/* The norm alone.
+ *   grads, num   host dc_gradient[num], num <= 2^20; out is not read
+ *   accumulate   1: *squares is added to, so that lists, or ranks that add
+ *                their *squares up, share one norm (squares is then required)
+ *   squares      device double[1] out, the sum of squares; or NULL
+ *   norm         device float[1] out, sqrt(*squares); or NULL */
+dc_status dc_grad_norm(const dc_gradient* grads, int32_t num, int32_t accumulate, double* squares,
+                       float* norm, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Clipping.  No out overlaps another gradient's grad or out; with `squares`,
+ * norm and coef, none overlaps anything else.
+ *   squares      device double[1], the sum of squares to clip by (not
+ *                changed), or NULL: that of this list
+ *   max_norm     >= 0, may be infinite (c = 1); eps >= 0, finite
+ *   norm, coef   device float[1] out: n and c; or NULL
+ * Gradients clipped in place by a factor of 1 are not touched. */
+dc_status dc_grad_clip(const dc_gradient* grads, int32_t num, const double* squares, float max_norm,
+                       float eps, float* norm, float* coef, void* workspace, int64_t workspace_bytes,
+                       void* stream);
 
 #ifdef __cplusplus
 }
