@@ -1227,6 +1227,22 @@ dc_status check_disjoint(std::vector<Named>& all, bool in_place) {
   return DC_OK;
 }
 
+constexpr int64_t kMostTokens = (int64_t)1 << 26, kMostColumns = (int64_t)1 << 22;  // grids of 2^32 threads
+
+dc_status check_embedding(int32_t dtype, int64_t T, int64_t rows, int64_t D, float scale) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, rows, D))) return st;
+  if (T > kMostTokens || D > kMostColumns)
+    return fail(DC_ERR_SHAPE, "T=%lld exceeds 2^26 or D=%lld exceeds 2^22", (long long)T, (long long)D);
+  if (!std::isfinite(scale)) return fail(DC_ERR_ARG, "scale=%g", (double)scale);
+  return DC_OK;
+}
+
+dc_status check_id_bytes(int32_t id_bytes) {
+  if (id_bytes != 4 && id_bytes != 8) return fail(DC_ERR_DTYPE, "ids of %d bytes", id_bytes);
+  return DC_OK;
+}
+
 // A list of gradients; with `clips` what it writes too, and the scalars.
 dc_status check_gradients(const dc_gradient* grads, int32_t num, bool clips, const double* squares, const float* norm,
                           const float* coef) {
@@ -1540,6 +1556,51 @@ dc_status dc_grad_clip(const dc_gradient* grads, int32_t num, const double* squa
   return hip_status(dc::launch_grad_clip(grads, num, squares, max_norm, eps, norm, coef, workspace,
                                          static_cast<hipStream_t>(stream)),
                     "clip launch");
+}
+
+dc_status dc_embedding(int32_t dtype, int32_t id_bytes, int64_t T, int64_t rows, int64_t D, const void* ids,
+                       const void* table, int64_t ld_table, float scale, void* out, int64_t ld_out,
+                       void* stream) {
+  dc_status st;
+  if ((st = check_embedding(dtype, T, rows, D, scale)) || (st = check_id_bytes(id_bytes))) return st;
+  const int32_t e = elem_bytes(dtype);
+  const Rows mi{"ids", ids, 1, T, T, id_bytes}, mt{"table", T ? table : nullptr, rows, D, ld_table, e},
+      mo{"out", out, T, D, ld_out, e};
+  if (T && ((st = check_rows(mi)) || (st = check_rows(mt)) || (st = check_rows(mo)) ||
+            (st = check_apart(mo, {&mi, &mt}))))
+    return st;
+  return hip_status(dc::launch_embedding(dtype, id_bytes, T, rows, D, ids, table, ld_table, scale, out, ld_out,
+                                         static_cast<hipStream_t>(stream)),
+                    "embedding launch");
+}
+
+dc_status dc_embedding_backward_workspace(int32_t dtype, int64_t T, int64_t rows, int64_t D,
+                                          int64_t* bytes) {
+  dc_status st;
+  if ((st = check_embedding(dtype, T, rows, D, 1.f))) return st;
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::embedding_workspace(T, D);
+  return ok();
+}
+
+dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int64_t rows, int64_t D,
+                                const void* dy, int64_t ld_dy, const void* ids, float scale,
+                                int32_t grad_dtype, void* dtable, int64_t ld, int32_t accumulate,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+  dc_status st;
+  if ((st = check_embedding(dtype, T, rows, D, scale)) || (st = check_id_bytes(id_bytes)) ||
+      (st = check_grad_dtype(dtype, grad_dtype)))
+    return st;
+  if (accumulate != 0 && accumulate != 1) return fail(DC_ERR_ARG, "accumulate=%d", accumulate);
+  const Rows mi{"ids", T ? ids : nullptr, 1, T, T, id_bytes}, my{"dy", dy, T, D, ld_dy, elem_bytes(dtype)},
+      mt{"dtable", dtable, rows, D, ld, elem_bytes(grad_dtype)};
+  if (T && ((st = check_rows(mi)) || (st = check_rows(my)))) return st;
+  if ((st = check_rows(mt)) || (st = check_apart(mt, {&mi, &my}))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, dc::embedding_workspace(T, D)))) return st;
+  return hip_status(dc::launch_embedding_backward(dtype, grad_dtype, id_bytes, T, rows, D, dy, ld_dy, ids, scale,
+                                                  dtable, ld, accumulate, workspace,
+                                                  static_cast<hipStream_t>(stream)),
+                    "embedding backward launch");
 }
 
 }  // extern "C"

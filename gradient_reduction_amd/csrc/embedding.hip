@@ -1,0 +1,500 @@
+// An embedding's lookup with scaling, and its table's gradient by sorted tokens:
+//   out[t] = scale E[ids[t]]                       (zeros for an id outside the table)
+//   dE[v] (+)= scale sum over {t: ids[t] = v} of dy[t]
+// The gradient's tokens are sorted by id, stably, so that every row's sum runs
+// over ascending t: no atomics, the same result every time.  The sorted
+// tokens are cut into tiles of kTile; a wave adds up one tile's rows over one
+// run of columns and writes every row of dE that lies whole in its tile.  A
+// row whose tokens reach over tiles leaves one partial sum in each, which a
+// second launch adds up in order; a frequent token is so spread over the chip.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "internal.h"
+
+namespace dc {
+namespace {
+
+// A 16-byte, or 8-byte, access at any address of an element.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+template <int BYTES>
+struct Access {
+  typedef u32x4_any type;
+};
+template <>
+struct Access<8> {
+  typedef u32x2_any type;
+};
+
+// V values of a row from column j on (columns past `left` are zeros), in fp32.
+template <class T, int V>
+__device__ __forceinline__ void load_columns(const T* p, int64_t left, float (&v)[V]) {
+  constexpr int B = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = B / sizeof(T);
+  using A = typename Access<B>::type;
+  T x[V];
+  if (left >= V) {
+#pragma unroll
+    for (int k = 0; k < V / N; ++k) {
+      const A w = *reinterpret_cast<const A*>(p + k * N);
+      __builtin_memcpy(x + k * N, &w, B);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < V; ++t) x[t] = t < left ? p[t] : (T)0.f;
+  }
+#pragma unroll
+  for (int t = 0; t < V; ++t) v[t] = (float)x[t];
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_columns(T* p, int64_t left, const float (&v)[V]) {
+  constexpr int B = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = B / sizeof(T);
+  using A = typename Access<B>::type;
+  T x[V];
+#pragma unroll
+  for (int t = 0; t < V; ++t) x[t] = (T)v[t];
+  if (left >= V) {
+#pragma unroll
+    for (int k = 0; k < V / N; ++k) {
+      A w;
+      __builtin_memcpy(&w, x + k * N, B);
+      *reinterpret_cast<A*>(p + k * N) = w;
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < V; ++t)
+      if (t < left) p[t] = x[t];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Lookup: a wave takes kLookup tokens over 64 vectors of columns, their rows'
+// loads in flight together.
+// ---------------------------------------------------------------------------
+constexpr int kLookup = 4;
+
+template <class T, class Id>
+__global__ void __launch_bounds__(256) k_lookup(int64_t T_, int64_t rows, int64_t D, const Id* ids, const T* table,
+                                                int64_t ld_table, float scale, T* out, int64_t ld_out) {
+  constexpr int V = 16 / sizeof(T);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * kLookup, j = ((int64_t)blockIdx.y * 64 + lane) * V;
+  const int64_t left = D - j;
+  if (left <= 0) return;
+  float v[kLookup][V];
+#pragma unroll
+  for (int k = 0; k < kLookup; ++k) {
+    const int64_t id = t0 + k < T_ ? (int64_t)ids[t0 + k] : -1;
+    if (id >= 0 && id < rows) load_columns<T, V>(table + id * ld_table + j, left, v[k]);
+    else
+#pragma unroll
+      for (int t = 0; t < V; ++t) v[k][t] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kLookup; ++k) {
+    if (t0 + k >= T_) break;
+#pragma unroll
+    for (int t = 0; t < V; ++t) v[k][t] *= scale;
+    store_columns<T, V>(out + (t0 + k) * ld_out + j, left, v[k]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sorting (id, token) by id: stable passes over `bits` bits of the id from the
+// low ones up.  A workgroup of 1024 takes kSortTile tokens, each wave a run of
+// them; a token's place is the number of tokens with smaller digits, plus
+// those of its digit in earlier workgroups, earlier waves, and before it in
+// its wave.  Ids outside the table sort behind it, as `rows`.
+// ---------------------------------------------------------------------------
+constexpr int kSortItems = 4;
+constexpr int kSortTile = 1024 * kSortItems;
+constexpr int kMostBits = 10;                 // of a pass
+constexpr int kDigits = 1 << kMostBits;
+constexpr int kSortSelf = 16;                 // tiles up to which workgroups count by themselves
+
+template <class Id>
+__device__ __forceinline__ uint32_t key_of(Id id, uint32_t rows) {
+  return id >= 0 && (uint64_t)id < rows ? (uint32_t)id : rows;
+}
+
+struct SortPass {
+  int64_t n;
+  const uint32_t* keys;     // NULL: the ids themselves, token t at place t
+  const uint32_t* tokens;
+  uint32_t* out_keys;
+  uint32_t* out_tokens;
+  uint32_t* counts;         // [tiles + 1][kDigits], the last row the totals; NULL: count here
+  int32_t tiles;
+  uint32_t rows;
+  int32_t shift, bits;
+};
+
+template <class Id>
+__device__ __forceinline__ uint32_t sort_key(const SortPass& p, const Id* ids, int64_t i) {
+  return p.keys ? p.keys[i] : key_of(ids[i], p.rows);
+}
+
+// counts[tile][digit] of every tile.
+template <class Id>
+__global__ void __launch_bounds__(1024) k_sort_count(SortPass p, const Id* ids) {
+  __shared__ uint32_t count[kDigits];
+  const uint32_t mask = (1u << p.bits) - 1;
+  count[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * kSortTile, i1 = i0 + kSortTile < p.n ? i0 + kSortTile : p.n;
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += 1024) atomicAdd(&count[(sort_key(p, ids, i) >> p.shift) & mask], 1u);
+  __syncthreads();
+  p.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
+}
+
+// Every digit's counts become the numbers of its tokens in earlier tiles; the
+// totals go behind them.  A wave for 64 neighbouring digits, 16 tiles' loads
+// in flight.
+__global__ void __launch_bounds__(64) k_sort_scan(uint32_t* counts, int32_t tiles) {
+  const int d = blockIdx.x * 64 + threadIdx.x;
+  uint32_t sum = 0;
+  for (int32_t b = 0; b < tiles; b += 16) {
+    uint32_t c[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) c[k] = b + k < tiles ? counts[(int64_t)(b + k) * kDigits + d] : 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (b + k < tiles) counts[(int64_t)(b + k) * kDigits + d] = sum;
+      sum += c[k];
+    }
+  }
+  counts[(int64_t)tiles * kDigits + d] = sum;
+}
+
+template <class Id>
+__global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
+  __shared__ uint32_t place[16][kDigits];  // counts, then first places, by wave
+  __shared__ uint32_t earlier[kDigits], total[kDigits];
+  __shared__ uint32_t wave_total[16];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, d = threadIdx.x;
+  const uint32_t mask = (1u << p.bits) - 1;
+  const int64_t i0 = (int64_t)blockIdx.x * kSortTile;
+  for (int w = 0; w < 16; ++w) place[w][d] = 0;
+  if (p.counts) {
+    earlier[d] = p.counts[(int64_t)blockIdx.x * kDigits + d];
+    total[d] = p.counts[(int64_t)p.tiles * kDigits + d];
+  } else {
+    earlier[d] = 0;
+    total[d] = 0;
+  }
+  __syncthreads();
+  if (!p.counts) {
+    for (int64_t i = threadIdx.x; i < p.n; i += 1024) {
+      const uint32_t g = (sort_key(p, ids, i) >> p.shift) & mask;
+      atomicAdd(&total[g], 1u);
+      if (i < i0) atomicAdd(&earlier[g], 1u);
+    }
+  }
+  uint32_t key[kSortItems], token[kSortItems], rank[kSortItems];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int64_t i = i0 + (wave * kSortItems + k) * 64 + lane;
+    const bool in = i < p.n;
+    key[k] = in ? sort_key(p, ids, i) : 0;
+    token[k] = in ? (p.keys ? p.tokens[i] : (uint32_t)i) : 0;
+    const uint32_t g = (key[k] >> p.shift) & mask;
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < p.bits; ++b) {
+      const bool one = (g >> b) & 1;
+      const uint64_t ones = __ballot(one);
+      same &= one ? ones : ~ones;
+    }
+    const int before = __popcll(same & ((1ull << lane) - 1));
+    uint32_t old = 0;
+    if (in && before == 0) old = atomicAdd(&place[wave][g], (uint32_t)__popcll(same));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the next item's lanes see it
+    old = __shfl(old, in ? __ffsll((unsigned long long)same) - 1 : lane);
+    rank[k] = old + before;
+  }
+  __syncthreads();
+  // the digit's first place: tokens of smaller digits, then of earlier tiles
+  uint32_t first = total[d];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t up = __shfl_up(first, o);
+    if (lane >= o) first += up;
+  }
+  if (lane == 63) wave_total[wave] = first;
+  __syncthreads();
+  uint32_t at = first - total[d] + earlier[d];
+  for (int w = 0; w < wave; ++w) at += wave_total[w];
+  for (int w = 0; w < 16; ++w) {
+    const uint32_t c = place[w][d];
+    place[w][d] = at;
+    at += c;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    if (i0 + (wave * kSortItems + k) * 64 + lane >= p.n) continue;
+    const uint32_t to = place[wave][(key[k] >> p.shift) & mask] + rank[k];
+    p.out_keys[to] = key[k];
+    p.out_tokens[to] = token[k];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of rows.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 16;   // sorted tokens per wave
+constexpr int kAhead = 4;   // rows in flight
+constexpr int kFill = 16;   // rows of dE that a wave of the fill looks at
+
+struct RowSums {
+  int64_t n, rows, D;
+  const uint32_t* keys;
+  const uint32_t* tokens;
+  const void* dy;
+  int64_t ld_dy;
+  void* dtable;
+  int64_t ld;
+  float* partial;  // [tiles][2][D]: of the row that came in from the tile before, of the one that goes on
+  float scale;
+  int32_t accumulate;
+  uint32_t tile_blocks;  // workgroups of tiles; the others fill
+};
+
+// The first place with a key of at least `key`.
+__device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, uint32_t key) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (keys[mid] < key) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <class T, class G>
+__global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
+  constexpr int V = 16 / sizeof(T) > 4 ? 8 : 4;  // columns per lane
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
+  G* dtable = static_cast<G*>(a.dtable) + j;
+  if (blockIdx.x >= a.tile_blocks) {
+    // rows that no token names: zeros
+    const int64_t r0 = ((int64_t)(blockIdx.x - a.tile_blocks) * 4 + wave) * kFill;
+    if (r0 >= a.rows || left <= 0) return;
+    const int64_t r1 = r0 + kFill < a.rows ? r0 + kFill : a.rows;
+    int64_t at = lower_bound(a.keys, a.n, (uint32_t)r0);
+    const float zero[V] = {};
+    for (int64_t r = r0; r < r1; ++r) {
+      if (at < a.n && a.keys[at] == (uint32_t)r) {
+        at = r + 1 < r1 ? at + lower_bound(a.keys + at, a.n - at, (uint32_t)r + 1) : at;
+        continue;
+      }
+      store_columns<G, V>(dtable + r * a.ld, left, zero);
+    }
+    return;
+  }
+  const int64_t tile = (int64_t)blockIdx.x * 4 + wave, p0 = tile * kTile;
+  // lanes past the last column stay: the tile's keys are held across the wave
+  if (p0 >= a.n) return;
+  const int have = a.n - p0 < kTile ? (int)(a.n - p0) : kTile;
+  // lane i holds place p0 + i - 1: the tile, with the places before and after it
+  const int64_t mine = p0 + lane - 1;
+  const bool exists = lane <= have + 1 && mine >= 0 && mine < a.n;
+  const uint32_t key = exists ? a.keys[mine] : (uint32_t)a.rows;
+  const uint32_t token = exists ? a.tokens[mine] : 0;
+  const uint32_t outside = (uint32_t)a.rows;
+  auto key_at = [&](int i) { return (uint32_t)__builtin_amdgcn_readlane((int)key, i + 1); };
+  const uint32_t first = key_at(0), last = key_at(have - 1);
+  const bool came = p0 > 0 && key_at(-1) == first, goes = p0 + have < a.n && key_at(have) == last;
+  const T* dy = static_cast<const T*>(a.dy) + j;
+  float sum[V] = {};
+  for (int i0 = 0; i0 < have; i0 += kAhead) {
+    float v[kAhead][V], old[kAhead][V];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k;
+      if (i >= have || key_at(i) == outside) break;
+      load_columns<T, V>(dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)token, i + 1) * a.ld_dy, left, v[k]);
+      if (a.accumulate && key_at(i) != key_at(i + 1)) load_columns<G, V>(dtable + (int64_t)key_at(i) * a.ld, left, old[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k;
+      if (i >= have || key_at(i) == outside) break;
+#pragma unroll
+      for (int t = 0; t < V; ++t) sum[t] += v[k][t];
+      const bool ends = i == have - 1 || key_at(i) != key_at(i + 1);
+      if (!ends) continue;
+      const bool in = came && key_at(i) == first, on = goes && i == have - 1;
+      if (in || on) {
+        store_columns<float, V>(a.partial + (tile * 2 + (in ? 0 : 1)) * a.D + j, left, sum);
+      } else {
+        float y[V];
+#pragma unroll
+        for (int t = 0; t < V; ++t) y[t] = a.scale * sum[t] + (a.accumulate ? old[k][t] : 0.f);
+        store_columns<G, V>(dtable + (int64_t)key_at(i) * a.ld, left, y);
+      }
+#pragma unroll
+      for (int t = 0; t < V; ++t) sum[t] = 0.f;
+    }
+  }
+}
+
+// A row whose tokens reach over tiles: the workgroup of the tile in which it
+// ends adds up its partial sums, eight waves a run of them each.
+template <class G>
+__global__ void __launch_bounds__(512) k_row_join(RowSums a) {
+  constexpr int V = 4;
+  __shared__ float part[8][64][V];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
+  const int64_t tile = blockIdx.x, p0 = tile * kTile, p1 = p0 + kTile < a.n ? p0 + kTile : a.n;
+  const uint32_t key = a.keys[p0];
+  if (tile == 0 || key >= a.rows || a.keys[p0 - 1] != key) return;
+  if (p1 < a.n && a.keys[p1] == key) return;
+  const int64_t from = lower_bound(a.keys, p0, key) / kTile, parts = tile - from + 1;
+  const int64_t per = (parts + 7) / 8, k0 = wave * per, k1 = k0 + per < parts ? k0 + per : parts;
+  float sum[V] = {};
+  if (left > 0) {
+#pragma unroll 4
+    for (int64_t k = k0; k < k1; ++k) {
+      float v[V];
+      load_columns<float, V>(a.partial + ((from + k) * 2 + (k == 0 ? 1 : 0)) * a.D + j, left, v);
+#pragma unroll
+      for (int t = 0; t < V; ++t) sum[t] += v[t];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < V; ++t) part[wave][lane][t] = sum[t];
+  __syncthreads();
+  if (wave || left <= 0) return;
+  G* to = static_cast<G*>(a.dtable) + (int64_t)key * a.ld + j;
+  float y[V] = {};
+  if (a.accumulate) load_columns<G, V>(to, left, y);
+#pragma unroll
+  for (int t = 0; t < V; ++t) {
+    float s = part[0][lane][t];
+    for (int w = 1; w < 8; ++w) s += part[w][lane][t];
+    y[t] = a.scale * s + y[t];
+  }
+  store_columns<G, V>(to, left, y);
+}
+
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// Where the workspace holds what: two buffers of keys and tokens, the counts,
+// the partial sums.
+struct EmbeddingSpace {
+  int64_t tokens, sort_tiles, tiles, keys_at[2], tokens_at[2], counts_at, partial_at, bytes;
+  EmbeddingSpace(int64_t T, int64_t D) {
+    sort_tiles = (T + kSortTile - 1) / kSortTile;
+    tiles = (T + kTile - 1) / kTile;
+    int64_t at = 0;
+    for (int k = 0; k < 2; ++k) {
+      keys_at[k] = at;
+      at += up16(4 * T);
+      tokens_at[k] = at;
+      at += up16(4 * T);
+    }
+    counts_at = at;
+    if (sort_tiles > kSortSelf) at += (sort_tiles + 1) * kDigits * 4;
+    partial_at = at;
+    if (tiles > 1) at += up16(tiles * 2 * D * 4);
+    bytes = at;
+  }
+};
+
+template <class Id>
+int sort_tokens(int64_t T, int64_t rows, const void* ids, char* ws, const EmbeddingSpace& e, hipStream_t stream) {
+  int32_t bits = 1;
+  while (rows >> bits) ++bits;  // keys are 0 .. rows
+  const int32_t passes = (bits + kMostBits - 1) / kMostBits, each = (bits + passes - 1) / passes;
+  const Id* id = static_cast<const Id*>(ids);
+  for (int32_t k = 0; k < passes; ++k) {
+    SortPass p{};
+    p.n = T;
+    if (k) {
+      p.keys = reinterpret_cast<uint32_t*>(ws + e.keys_at[(k - 1) & 1]);
+      p.tokens = reinterpret_cast<uint32_t*>(ws + e.tokens_at[(k - 1) & 1]);
+    }
+    p.out_keys = reinterpret_cast<uint32_t*>(ws + e.keys_at[k & 1]);
+    p.out_tokens = reinterpret_cast<uint32_t*>(ws + e.tokens_at[k & 1]);
+    p.tiles = (int32_t)e.sort_tiles;
+    p.rows = (uint32_t)rows;
+    p.shift = k * each;
+    p.bits = std::min(each, bits - p.shift);
+    if (e.sort_tiles > kSortSelf) {
+      p.counts = reinterpret_cast<uint32_t*>(ws + e.counts_at);
+      k_sort_count<Id><<<dim3((uint32_t)e.sort_tiles), 1024, 0, stream>>>(p, id);
+      k_sort_scan<<<kDigits / 64, 64, 0, stream>>>(p.counts, p.tiles);
+    }
+    k_sort_pass<Id><<<dim3((uint32_t)e.sort_tiles), 1024, 0, stream>>>(p, id);
+  }
+  return (passes - 1) & 1;
+}
+
+template <class T, class G>
+void row_sums(const RowSums& s, int64_t tiles, hipStream_t stream) {
+  RowSums a = s;
+  constexpr int64_t per = 64 * (sizeof(T) == 2 ? 8 : 4);
+  const uint32_t across = (uint32_t)((a.D + per - 1) / per);
+  a.tile_blocks = (uint32_t)((tiles + 3) / 4);
+  const int64_t fill = a.accumulate ? 0 : (a.rows + 4 * kFill - 1) / (4 * kFill);
+  if (a.tile_blocks + fill) k_row_sums<T, G><<<dim3((uint32_t)(a.tile_blocks + fill), across), 256, 0, stream>>>(a);
+  if (tiles > 1)
+    k_row_join<G><<<dim3((uint32_t)tiles, (uint32_t)((a.D + 255) / 256)), 512, 0, stream>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_embedding(int32_t dtype, int32_t id_bytes, int64_t T, int64_t rows, int64_t D, const void* ids,
+                            const void* table, int64_t ld_table, float scale, void* out, int64_t ld_out,
+                            hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  auto launch = [&](auto type, auto id) {
+    using E = decltype(type);
+    using Id = decltype(id);
+    constexpr int64_t per = 64 * (16 / sizeof(E));
+    const dim3 grid((uint32_t)((T + 4 * kLookup - 1) / (4 * kLookup)), (uint32_t)((D + per - 1) / per));
+    k_lookup<E, Id><<<grid, 256, 0, stream>>>(T, rows, D, static_cast<const Id*>(ids), static_cast<const E*>(table),
+                                              ld_table, scale, static_cast<E*>(out), ld_out);
+  };
+  if (dtype == DC_BF16) id_bytes == 8 ? launch(__bf16{}, int64_t{}) : launch(__bf16{}, int32_t{});
+  else id_bytes == 8 ? launch(float{}, int64_t{}) : launch(float{}, int32_t{});
+  return hipGetLastError();
+}
+
+int64_t embedding_workspace(int64_t T, int64_t D) { return EmbeddingSpace(T, D).bytes; }
+
+hipError_t launch_embedding_backward(int32_t dtype, int32_t grad_dtype, int32_t id_bytes, int64_t T, int64_t rows,
+                                     int64_t D, const void* dy, int64_t ld_dy, const void* ids, float scale,
+                                     void* dtable, int64_t ld, int32_t accumulate, void* workspace,
+                                     hipStream_t stream) {
+  if (T == 0 && accumulate) return hipSuccess;
+  const EmbeddingSpace e(T, D);
+  char* ws = static_cast<char*>(workspace);
+  int at = 0;
+  if (T) at = id_bytes == 8 ? sort_tokens<int64_t>(T, rows, ids, ws, e, stream)
+                            : sort_tokens<int32_t>(T, rows, ids, ws, e, stream);
+  RowSums a{};
+  a.n = T;
+  a.rows = rows;
+  a.D = D;
+  a.keys = reinterpret_cast<const uint32_t*>(ws + e.keys_at[at]);
+  a.tokens = reinterpret_cast<const uint32_t*>(ws + e.tokens_at[at]);
+  a.dy = dy;
+  a.ld_dy = ld_dy;
+  a.dtable = dtable;
+  a.ld = ld;
+  a.partial = reinterpret_cast<float*>(ws + e.partial_at);
+  a.scale = scale;
+  a.accumulate = accumulate;
+  if (dtype == DC_F32) row_sums<float, float>(a, e.tiles, stream);
+  else if (grad_dtype == DC_F32) row_sums<__bf16, float>(a, e.tiles, stream);
+  else row_sums<__bf16, __bf16>(a, e.tiles, stream);
+  return hipGetLastError();
+}
+
+}  // namespace dc

@@ -120,6 +120,10 @@ _SIGS = {
     "dc_grad_clip_workspace": ([_vp], _i32),
     "dc_grad_norm": ([_vp, _i32, _i32, _vp, _vp, _vp, _i64, _vp], _i32),
     "dc_grad_clip": ([_vp, _i32, _vp, _f32, _f32, _vp, _vp, _vp, _i64, _vp], _i32),
+    "dc_embedding": ([_i32, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _f32, _vp, _i64, _vp], _i32),
+    "dc_embedding_backward_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
+    "dc_embedding_backward": ([_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _f32, _i32, _vp, _i64, _i32, _vp,
+                               _i64, _vp], _i32),
     "dc_round_bf16": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_copy": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_rows": ([_vp, _i64, _i32, _vp, _i64, _i32, _i64, _vp], _i32),
@@ -586,6 +590,26 @@ def dc_grad_clip(grads, num, squares, max_norm, eps, norm, coef, workspace, work
     _check("dc_grad_clip", lib().dc_grad_clip(
         gp, num, _dev(squares), max_norm, eps, _dev(norm), _dev(coef), _dev(workspace), workspace_bytes,
         _stream(stream)))
+
+
+def dc_embedding(dtype, id_bytes, T, rows, D, ids, table, ld_table, scale, out, ld_out, stream=None):
+    _check("dc_embedding", lib().dc_embedding(
+        dtype, id_bytes, T, rows, D, _dev(ids), _dev(table), ld_table, scale, _dev(out), ld_out, _stream(stream)))
+
+
+def dc_embedding_backward_workspace(dtype, T, rows, D):
+    """Host only; bytes of workspace."""
+    n = ctypes.c_int64(0)
+    _check("dc_embedding_backward_workspace", lib().dc_embedding_backward_workspace(dtype, T, rows, D,
+                                                                                    ctypes.byref(n)))
+    return n.value
+
+
+def dc_embedding_backward(dtype, id_bytes, T, rows, D, dy, ld_dy, ids, scale, grad_dtype, dtable, ld, accumulate,
+                          workspace, workspace_bytes, stream=None):
+    _check("dc_embedding_backward", lib().dc_embedding_backward(
+        dtype, id_bytes, T, rows, D, _dev(dy), ld_dy, _dev(ids), scale, grad_dtype, _dev(dtable), ld, accumulate,
+        _dev(workspace), workspace_bytes, _stream(stream)))
 
 
 def dc_round_bf16(in_, out, n, stream=None):

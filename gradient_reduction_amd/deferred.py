@@ -12,9 +12,11 @@ every step runs in libdc.so (dc_accumulate, dc_deferred_reduce,
 dc_accumulate_reduce); torch supplies the memory and the stream.
 
 A micro-batch comes either whole, as a slab of gradients (accumulate), or
-layer by layer as the products that make them (accumulate_linear, then
-end_micro_batch): a weight's gradient is then added to its replica's row by
-the product itself (dc_linear_backward) and never stored on its own.
+layer by layer as the products that make them (accumulate_linear and its
+like, then end_micro_batch): a weight's gradient is then added to its
+replica's row by the product itself (dc_linear_backward,
+dc_embedding_backward) and never stored on its own.  clip() takes the reduced
+gradients' global norm (dc_grad_clip).
 """
 from . import dc
 
@@ -81,18 +83,35 @@ class DeferredReducer:
             raise ValueError("the weight's and the bias's elements overlap")
         with linear.on(self.acc.device, stream):
             dx, _, _, launch = linear._backward(dy, x, w, pre, act, dw, db, True, need_dx, True)
-            stale = self.stale if self.open or self.micro_batches else set(range(self.W))
-            if row in stale:                                  # the layer is accepted
-                self.acc[row].zero_()
-            launch()
+            self._add(row, launch)
+        return dx
+
+    def _add(self, row, launch):
+        """An accepted layer's launches into a row, cleared before its first of a
+        step."""
+        stale = self.stale if self.open or self.micro_batches else set(range(self.W))
+        if row in stale:
+            self.acc[row].zero_()
+        launch()
         self.stale = stale - {row}
         self.open = True
-        return dx
+
+    def accumulate_embedding(self, row: int, offset: int, dy, ids, rows: int, scale: float = 1.0,
+                             stream=None) -> None:
+        """The gradient of replica `row`'s embedding table [rows, D], from the
+        gradient dy [..., D] of its lookup of `ids` (embedding.backward), added at
+        elements offset .. offset + rows D of the row; otherwise as
+        accumulate_linear.  A table that is the output's too is given to both."""
+        from . import embedding, linear
+        dtable = self._place(row, offset, rows * dy.shape[-1]).view(rows, dy.shape[-1])
+        with linear.on(self.acc.device, stream):
+            _, launch = embedding._backward(dy, ids, rows, scale, dtable, True, None)
+            self._add(row, launch)
 
     def end_micro_batch(self) -> None:
         """Every layer of every replica's micro-batch has been added."""
         if not self.open:
-            raise RuntimeError("end_micro_batch() before any accumulate_linear()")
+            raise RuntimeError("end_micro_batch() before any layer")
         self.open = False
         self.micro_batches += 1
 

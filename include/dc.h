@@ -1007,6 +1007,41 @@ dc_status dc_grad_clip(const dc_gradient* grads, int32_t num, const double* squa
                        float eps, float* norm, float* coef, void* workspace, int64_t workspace_bytes,
                        void* stream);
 
+/* ---- The embedding ---------------------------------------------------------
+ *
+ * Rules of the layer's products hold; T at most 2^26, D at most 2^22. */
+
+/* Lookup of T tokens in a table of `rows` rows and D columns, with scaling:
+ *   out[t] = scale E[ids[t]]          in fp32, rounded once
+ * An id outside [0, rows) gives zeros: padding, or a token of another rank's
+ * part of the table.
+ *   id_bytes         4 or 8 (else DC_ERR_DTYPE): signed ids of 32 or 64 bits
+ *   ids              device [T], aligned to their size
+ *   table, ld_table  device [rows, ld_table]
+ *   out, ld_out      device [T, ld_out] out */
+dc_status dc_embedding(int32_t dtype, int32_t id_bytes, int64_t T, int64_t rows, int64_t D, const void* ids,
+                       const void* table, int64_t ld_table, float scale, void* out, int64_t ld_out,
+                       void* stream);
+
+/* Bytes of workspace of dc_embedding_backward.  Host only. */
+dc_status dc_embedding_backward_workspace(int32_t dtype, int64_t T, int64_t rows, int64_t D,
+                                          int64_t* bytes);
+
+/* The table's gradient:
+ *   dE[v] = (accumulate ? dE[v] : 0) + scale sum over {t: ids[t] = v} of dy[t]
+ * in fp32, every row's sum in the order of its tokens (in parts fixed by the
+ * ids, added in order), rounded once.  With accumulate, rows that no id names are neither
+ * read nor written; without it they become zeros.  An id outside [0, rows)
+ * gives nothing.  With accumulate and DC_F32, dE is a parameter's place in a
+ * replica's accumulator row ([MT] What: micro-batch gradients add up locally).
+ *   dy, ld_dy    device [T, ld_dy], ld_dy >= D; a row of a dropped id is not read
+ *   grad_dtype   of dtable: DC_F32, or dtype
+ *   dtable, ld   device [rows, ld], ld >= D */
+dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int64_t rows, int64_t D,
+                                const void* dy, int64_t ld_dy, const void* ids, float scale,
+                                int32_t grad_dtype, void* dtable, int64_t ld, int32_t accumulate,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
