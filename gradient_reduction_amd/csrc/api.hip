@@ -1243,6 +1243,33 @@ dc_status check_id_bytes(int32_t id_bytes) {
   return DC_OK;
 }
 
+dc_status check_norm(int32_t dtype, int64_t T, int64_t D, int64_t gate_rows, const void* h, const void* post,
+                     const void* gate, const void* gain, float scale, float offset, float eps) {
+  dc_status st;
+  if ((st = check_dtype(dtype)) || (st = check_sizes(T, D, 1))) return st;
+  if (D > dc::norm_most_columns())
+    return fail(DC_ERR_UNSUPPORTED, "D=%lld exceeds %lld", (long long)D, (long long)dc::norm_most_columns());
+  if (gate_rows < 1) return fail(DC_ERR_ARG, "gate_rows=%lld < 1", (long long)gate_rows);
+  if (T % gate_rows != 0)
+    return fail(DC_ERR_SHAPE, "%lld gate rows do not divide T=%lld", (long long)gate_rows, (long long)T);
+  if (gate_rows > kMaxSide) return fail(DC_ERR_SHAPE, "gate_rows=%lld exceeds 2^28", (long long)gate_rows);
+  if (!std::isfinite(scale) || !std::isfinite(offset))
+    return fail(DC_ERR_ARG, "scale=%g offset=%g", (double)scale, (double)offset);
+  if (!(eps >= 0) || !std::isfinite(eps)) return fail(DC_ERR_ARG, "eps=%g", (double)eps);
+  if (T && h == nullptr && (post || gate)) return fail(DC_ERR_NULL, "h is NULL");
+  return DC_OK;
+}
+
+// Of the rows that `o` writes: other inputs it must not touch, and those that
+// it may be (same base and stride).
+dc_status check_rows_apart(const Rows& o, std::initializer_list<const Rows*> others,
+                           std::initializer_list<const Rows*> may) {
+  dc_status st;
+  for (const Rows* m : may)
+    if (!same(o, *m) && (st = check_apart(o, {m}))) return st;
+  return check_apart(o, others);
+}
+
 // A list of gradients; with `clips` what it writes too, and the scalars.
 dc_status check_gradients(const dc_gradient* grads, int32_t num, bool clips, const double* squares, const float* norm,
                           const float* coef) {
@@ -1601,6 +1628,93 @@ dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int6
                                                   dtable, ld, accumulate, workspace,
                                                   static_cast<hipStream_t>(stream)),
                     "embedding backward launch");
+}
+
+dc_status dc_norm(int32_t dtype, int64_t T, int64_t D, const void* x, int64_t ld_x, const void* h,
+                  int64_t ld_h, const void* post_gain, const void* gate, int64_t gate_rows,
+                  int64_t ld_gate, const void* gain, float scale, float offset, float eps, void* s,
+                  int64_t ld_s, void* y, int64_t ld_y, void* stream) {
+  dc_status st;
+  if ((st = check_norm(dtype, T, D, gate_rows, h, post_gain, gate, gain, scale, offset, eps))) return st;
+  if (T == 0) return ok();
+  if ((h == nullptr && s) || (gain == nullptr && y))
+    return fail(DC_ERR_NULL, h == nullptr && s ? "s without h" : "y without gain");
+  if (s == nullptr && y == nullptr) return fail(DC_ERR_NULL, "s and y are both NULL");
+  if (gain && y == nullptr) return fail(DC_ERR_NULL, "y is NULL");
+  const int32_t e = elem_bytes(dtype);
+  const Rows mx{"x", x, T, D, ld_x, e}, mh{"h", h, T, D, ld_h, e}, mp{"post_gain", post_gain, 1, D, D, e},
+      mg{"gate", gate, gate_rows, D, ld_gate, e}, mw{"gain", gain, 1, D, D, e}, ms{"s", s, T, D, ld_s, e},
+      my{"y", y, T, D, ld_y, e};
+  if ((st = check_rows(mx))) return st;
+  for (const Rows* m : {&mh, &mp, &mg, &mw, &ms, &my})
+    if (m->p && (st = check_rows(*m))) return st;
+  if ((st = check_rows_apart(ms, {&mp, &mg, &mw}, {&mx, &mh})) ||
+      (st = check_rows_apart(my, {&mp, &mg, &mw, &ms}, {&mx, &mh})))
+    return st;
+  dc::NormLaunch l{};
+  l.dtype = dtype;
+  l.T = T, l.D = D, l.gate_rows = gate_rows;
+  l.x = x, l.h = h, l.post = post_gain, l.gate = gate, l.gain = gain;
+  l.ld_x = ld_x, l.ld_h = ld_h, l.ld_gate = ld_gate;
+  l.scale = scale, l.offset = offset, l.eps = eps;
+  l.out_s = s, l.ld_out_s = ld_s, l.y = y, l.ld_y = ld_y;
+  return hip_status(dc::launch_norm(l, static_cast<hipStream_t>(stream)), "norm launch");
+}
+
+dc_status dc_norm_backward_workspace(int32_t dtype, int64_t T, int64_t D, int64_t gate_rows,
+                                     int64_t* bytes) {
+  dc_status st;
+  if ((st = check_norm(dtype, T, D, gate_rows, nullptr, nullptr, nullptr, nullptr, 1.f, 0.f, 0.f))) return st;
+  if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
+  *bytes = dc::norm_workspace(T, D, gate_rows);
+  return ok();
+}
+
+dc_status dc_norm_backward(int32_t dtype, int64_t T, int64_t D, const void* dy, int64_t ld_dy,
+                           const void* ds, int64_t ld_ds, const void* s, int64_t ld_s, const void* h,
+                           int64_t ld_h, const void* post_gain, const void* gate, int64_t gate_rows,
+                           int64_t ld_gate, const void* gain, float scale, float offset, float eps,
+                           void* dx, int64_t ld_dx, void* dh, int64_t ld_dh, int32_t grad_dtype,
+                           void* dgain, void* dpost_gain, void* dgate, int64_t ld_dgate,
+                           int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
+  dc_status st;
+  if ((st = check_norm(dtype, T, D, gate_rows, h, post_gain, gate, gain, scale, offset, eps)) ||
+      (st = check_grad_dtype(dtype, grad_dtype)))
+    return st;
+  if (accumulate != 0 && accumulate != 1) return fail(DC_ERR_ARG, "accumulate=%d", accumulate);
+  if (T && h == nullptr && gain == nullptr) return fail(DC_ERR_NULL, "h and gain are both NULL");
+  if ((T && dh && !h) || (dgain && !gain) || (dpost_gain && !post_gain) || (dgate && !gate))
+    return fail(DC_ERR_NULL, "the gradient of an operand that is NULL");
+  if (!dx && !dh && !dgain && !dpost_gain && !dgate) return fail(DC_ERR_NULL, "every output is NULL");
+  const int32_t e = elem_bytes(dtype), ge = elem_bytes(grad_dtype);
+  const Rows my{"dy", gain ? dy : nullptr, T, D, ld_dy, e}, md{"ds", ds, T, D, ld_ds, e},
+      ms{"s", gain ? s : nullptr, T, D, ld_s, e}, mh{"h", h, T, D, ld_h, e},
+      mp{"post_gain", post_gain, 1, D, D, e}, mg{"gate", gate, gate_rows, D, ld_gate, e},
+      mw{"gain", gain, 1, D, D, e}, ox{"dx", dx, T, D, ld_dx, e}, oh{"dh", dh, T, D, ld_dh, e},
+      ow{"dgain", dgain, 1, D, D, ge}, op{"dpost_gain", dpost_gain, 1, D, D, ge},
+      og{"dgate", dgate, gate_rows, D, ld_dgate, ge};
+  if (gain && ((st = check_rows(my)) || (st = check_rows(ms)))) return st;
+  for (const Rows* m : {&md, &mh, &mp, &mg, &mw, &ox, &oh, &ow, &op, &og})
+    if (m->p && (st = check_rows(*m))) return st;
+  if ((st = check_rows_apart(ox, {&mp, &mg, &mw}, {&my, &md, &ms, &mh})) ||
+      (st = check_rows_apart(oh, {&mp, &mg, &mw, &ox}, {&my, &md, &ms, &mh})) ||
+      (st = check_apart(ow, {&my, &md, &ms, &mh, &mp, &mg, &mw, &ox, &oh})) ||
+      (st = check_apart(op, {&my, &md, &ms, &mh, &mp, &mg, &mw, &ox, &oh, &ow})) ||
+      (st = check_apart(og, {&my, &md, &ms, &mh, &mp, &mg, &mw, &ox, &oh, &ow, &op})))
+    return st;
+  if ((st = check_workspace(workspace, workspace_bytes, dc::norm_workspace(T, D, gate_rows)))) return st;
+  dc::NormLaunch l{};
+  l.dtype = dtype, l.grad_dtype = grad_dtype;
+  l.T = T, l.D = D, l.gate_rows = gate_rows;
+  l.x = s, l.h = h, l.post = post_gain, l.gate = gate, l.gain = gain;
+  l.ld_x = ld_s, l.ld_h = ld_h, l.ld_gate = ld_gate;
+  l.scale = scale, l.offset = offset, l.eps = eps;
+  l.dy = dy, l.ds = ds, l.ld_dy = ld_dy, l.ld_ds = ld_ds;
+  l.dx = dx, l.dh = dh, l.dgain = dgain, l.dpost = dpost_gain, l.dgate = dgate;
+  l.ld_dx = ld_dx, l.ld_dh = ld_dh, l.ld_dgate = ld_dgate;
+  l.accumulate = accumulate;
+  l.workspace = workspace;
+  return hip_status(dc::launch_norm_backward(l, static_cast<hipStream_t>(stream)), "norm backward launch");
 }
 
 }  // extern "C"

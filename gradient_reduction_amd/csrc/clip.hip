@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "columns.h"
 #include "device_common.h"
 #include "internal.h"
 
@@ -84,9 +85,6 @@ __device__ __forceinline__ double group_total(double v) {
   __syncthreads();
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
-
-// A 16-byte access at any address of an element.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // A unit's elements in 16-byte vectors, four to a thread: f(vector index,
 // elements in it) for those that exist.

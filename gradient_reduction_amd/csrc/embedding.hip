@@ -11,64 +11,12 @@
 
 #include <algorithm>
 
+#include "columns.h"
 #include "device_common.h"
 #include "internal.h"
 
 namespace dc {
 namespace {
-
-// A 16-byte, or 8-byte, access at any address of an element.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-template <int BYTES>
-struct Access {
-  typedef u32x4_any type;
-};
-template <>
-struct Access<8> {
-  typedef u32x2_any type;
-};
-
-// V values of a row from column j on (columns past `left` are zeros), in fp32.
-template <class T, int V>
-__device__ __forceinline__ void load_columns(const T* p, int64_t left, float (&v)[V]) {
-  constexpr int B = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = B / sizeof(T);
-  using A = typename Access<B>::type;
-  T x[V];
-  if (left >= V) {
-#pragma unroll
-    for (int k = 0; k < V / N; ++k) {
-      const A w = *reinterpret_cast<const A*>(p + k * N);
-      __builtin_memcpy(x + k * N, &w, B);
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < V; ++t) x[t] = t < left ? p[t] : (T)0.f;
-  }
-#pragma unroll
-  for (int t = 0; t < V; ++t) v[t] = (float)x[t];
-}
-
-template <class T, int V>
-__device__ __forceinline__ void store_columns(T* p, int64_t left, const float (&v)[V]) {
-  constexpr int B = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = B / sizeof(T);
-  using A = typename Access<B>::type;
-  T x[V];
-#pragma unroll
-  for (int t = 0; t < V; ++t) x[t] = (T)v[t];
-  if (left >= V) {
-#pragma unroll
-    for (int k = 0; k < V / N; ++k) {
-      A w;
-      __builtin_memcpy(&w, x + k * N, B);
-      *reinterpret_cast<A*>(p + k * N) = w;
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < V; ++t)
-      if (t < left) p[t] = x[t];
-  }
-}
 
 // ---------------------------------------------------------------------------
 // Lookup: a wave takes kLookup tokens over 64 vectors of columns, their rows'

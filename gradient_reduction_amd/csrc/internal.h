@@ -260,4 +260,26 @@ hipError_t launch_embedding_backward(int32_t dtype, int32_t grad_dtype, int32_t 
                                      void* dtable, int64_t ld, int32_t accumulate, void* workspace,
                                      hipStream_t stream);
 
+// The norms after a block and before the next one, and their backward.  x is
+// the residual stream before the block forward, after it backward.
+struct NormLaunch {
+  int32_t dtype, grad_dtype;
+  int64_t T, D, gate_rows;
+  const void *x, *h, *post, *gate, *gain;
+  int64_t ld_x, ld_h, ld_gate;
+  float scale, offset, eps;
+  void *out_s, *y;  // forward
+  int64_t ld_out_s, ld_y;
+  const void *dy, *ds;  // backward
+  int64_t ld_dy, ld_ds;
+  void *dx, *dh, *dgain, *dpost, *dgate;
+  int64_t ld_dx, ld_dh, ld_dgate;
+  int32_t accumulate;
+  void* workspace;
+};
+int64_t norm_most_columns();
+int64_t norm_workspace(int64_t T, int64_t D, int64_t gate_rows);
+hipError_t launch_norm(const NormLaunch& l, hipStream_t stream);
+hipError_t launch_norm_backward(const NormLaunch& l, hipStream_t stream);
+
 }  // namespace dc

@@ -124,6 +124,12 @@ _SIGS = {
     "dc_embedding_backward_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
     "dc_embedding_backward": ([_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _f32, _i32, _vp, _i64, _i32, _vp,
                                _i64, _vp], _i32),
+    "dc_norm": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _f32, _f32, _f32, _vp, _i64,
+                 _vp, _i64, _vp], _i32),
+    "dc_norm_backward_workspace": ([_i32, _i64, _i64, _i64, _vp], _i32),
+    "dc_norm_backward": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp,
+                          _f32, _f32, _f32, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _i64,
+                          _vp], _i32),
     "dc_round_bf16": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_copy": ([_vp, _vp, _i64, _vp], _i32),
     "dc_stream_rows": ([_vp, _i64, _i32, _vp, _i64, _i32, _i64, _vp], _i32),
@@ -610,6 +616,30 @@ def dc_embedding_backward(dtype, id_bytes, T, rows, D, dy, ld_dy, ids, scale, gr
     _check("dc_embedding_backward", lib().dc_embedding_backward(
         dtype, id_bytes, T, rows, D, _dev(dy), ld_dy, _dev(ids), scale, grad_dtype, _dev(dtable), ld, accumulate,
         _dev(workspace), workspace_bytes, _stream(stream)))
+
+
+def dc_norm(dtype, T, D, x, ld_x, h, ld_h, post_gain, gate, gate_rows, ld_gate, gain, scale, offset, eps, s, ld_s,
+            y, ld_y, stream=None):
+    _check("dc_norm", lib().dc_norm(
+        dtype, T, D, _dev(x), ld_x, _dev(h), ld_h, _dev(post_gain), _dev(gate), gate_rows, ld_gate, _dev(gain),
+        scale, offset, eps, _dev(s), ld_s, _dev(y), ld_y, _stream(stream)))
+
+
+def dc_norm_backward_workspace(dtype, T, D, gate_rows):
+    """Host only; bytes of workspace."""
+    n = ctypes.c_int64(0)
+    _check("dc_norm_backward_workspace", lib().dc_norm_backward_workspace(dtype, T, D, gate_rows, ctypes.byref(n)))
+    return n.value
+
+
+def dc_norm_backward(dtype, T, D, dy, ld_dy, ds, ld_ds, s, ld_s, h, ld_h, post_gain, gate, gate_rows, ld_gate, gain,
+                     scale, offset, eps, dx, ld_dx, dh, ld_dh, grad_dtype, dgain, dpost_gain, dgate, ld_dgate,
+                     accumulate, workspace, workspace_bytes, stream=None):
+    _check("dc_norm_backward", lib().dc_norm_backward(
+        dtype, T, D, _dev(dy), ld_dy, _dev(ds), ld_ds, _dev(s), ld_s, _dev(h), ld_h, _dev(post_gain), _dev(gate),
+        gate_rows, ld_gate, _dev(gain), scale, offset, eps, _dev(dx), ld_dx, _dev(dh), ld_dh, grad_dtype,
+        _dev(dgain), _dev(dpost_gain), _dev(dgate), ld_dgate, accumulate, _dev(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def dc_round_bf16(in_, out, n, stream=None):

@@ -15,7 +15,7 @@ A micro-batch comes either whole, as a slab of gradients (accumulate), or
 layer by layer as the products that make them (accumulate_linear and its
 like, then end_micro_batch): a weight's gradient is then added to its
 replica's row by the product itself (dc_linear_backward,
-dc_embedding_backward) and never stored on its own.  clip() takes the reduced
+dc_embedding_backward, dc_norm_backward) and never stored on its own.  clip() takes the reduced
 gradients' global norm (dc_grad_clip).
 """
 from . import dc
@@ -107,6 +107,30 @@ class DeferredReducer:
         with linear.on(self.acc.device, stream):
             _, launch = embedding._backward(dy, ids, rows, scale, dtable, True, None)
             self._add(row, launch)
+
+    def accumulate_norm(self, row: int, dy, s, gain=None, ds=None, h=None, post_gain=None, gate=None,
+                        scale: float = 1.0, offset: float = 0.0, eps: float = 1e-6, gain_at=None, post_gain_at=None,
+                        gate_at=None, need_dx: bool = True, need_dh: bool = True, stream=None):
+        """The backward of the norms around a block of replica `row`
+        (norm.backward): the gradients of gain [D], post_gain [D] and gate
+        ([rows, D] or [D]) are added at elements gain_at, post_gain_at and gate_at
+        of the row, where given; returns (dx, dh).  Otherwise as accumulate_linear."""
+        from . import linear, norm
+
+        def place(name, operand, at):
+            if at is None:
+                return None
+            if operand is None:
+                raise ValueError(f"{name}_at without {name}")
+            return self._place(row, at, operand.numel()).view(operand.shape)
+
+        self._place(row, 0, 0)
+        grads = [place("gain", gain, gain_at), place("post_gain", post_gain, post_gain_at), place("gate", gate, gate_at)]
+        with linear.on(self.acc.device, stream):
+            (dx, dh, *_), launch = norm._backward(dy, s, gain, ds, h, post_gain, gate, scale, offset, eps, *grads,
+                                                  any(g is not None for g in grads), need_dx, need_dh, False, None)
+            self._add(row, launch)
+        return dx, dh
 
     def end_micro_batch(self) -> None:
         """Every layer of every replica's micro-batch has been added."""

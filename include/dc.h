@@ -1042,6 +1042,68 @@ dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int6
                                 int32_t grad_dtype, void* dtable, int64_t ld, int32_t accumulate,
                                 void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---- Norms around a block ---------------------------------------------------
+ *
+ * Rules of the layer's products hold; D is at most 16384, the columns that a
+ * workgroup holds in registers (else DC_ERR_UNSUPPORTED). */
+
+/* The norm after a block, its gate and the residual's scale, and the norm
+ * before the next block, on T rows (tokens) of D columns:
+ *   u[t] = (offset + post_gain) h[t] / sqrt(mean(h[t]^2) + eps)
+ *   s[t] = x[t] + scale gate[t / (T / gate_rows)] u[t]
+ *   y[t] = (offset + gain) s[t] / sqrt(mean(s[t]^2) + eps)
+ * in fp32 with the means' sums in fp64, s and y each rounded once (y from the
+ * s before its rounding).  What is NULL falls away: without post_gain u = h, without gate it is 1,
+ * without h s = x, without gain there is no y; h or gain is needed, and h for
+ * post_gain and gate.
+ *   x, ld_x          device [T, ld_x]: the residual stream
+ *   h, ld_h          device [T, ld_h] or NULL: the block's output
+ *   post_gain, gain  device [D] or NULL
+ *   gate, ld_gate    device [gate_rows, ld_gate] or NULL; gate_rows >= 1 divides
+ *                    T, and every row serves T / gate_rows tokens in turn
+ *   s, ld_s          device [T, ld_s] out, or NULL; with h only; may be x (same
+ *                    ld) or h
+ *   y, ld_y          device [T, ld_y] out; with gain only; may be x or h,
+ *                    where s is not
+ * T = 0 writes nothing. */
+dc_status dc_norm(int32_t dtype, int64_t T, int64_t D, const void* x, int64_t ld_x, const void* h,
+                  int64_t ld_h, const void* post_gain, const void* gate, int64_t gate_rows,
+                  int64_t ld_gate, const void* gain, float scale, float offset, float eps, void* s,
+                  int64_t ld_s, void* y, int64_t ld_y, void* stream);
+
+/* Bytes of workspace of dc_norm_backward.  Host only. */
+dc_status dc_norm_backward_workspace(int32_t dtype, int64_t T, int64_t D, int64_t gate_rows,
+                                     int64_t* bytes);
+
+/* Its backward.  With n = s / sqrt(mean(s^2) + eps), m = h / sqrt(mean(h^2) + eps)
+ * (h without post_gain), r2 and r1 those factors:
+ *   q = (offset + gain) dy,  dx = ds + r2 (q - n mean(q n))
+ *   dgain (+)= sum_t dy n
+ *   v = scale gate dx,  dgate (+)= sum over the row's tokens of scale dx u
+ *   g = (offset + post_gain) v,  dh = r1 (g - m mean(g m))
+ *   dpost_gain (+)= sum_t v m
+ * in fp32 with the means' sums in fp64, from s as it is stored; sums over
+ * tokens are fp32 in an order fixed by the sizes; each output is rounded once,
+ * dx and dh from the same unrounded dx.
+ *   dy, ld_dy        device [T, ld_dy]: y's gradient; read with gain
+ *   ds, ld_ds        device [T, ld_ds] or NULL (0): what reaches s from later
+ *   s, ld_s          device [T, ld_s]: read with gain
+ *   dx, ld_dx        device [T, ld_dx] out, or NULL; may be ds, dy, s or h
+ *   dh, ld_dh        device [T, ld_dh] out, or NULL; with h only; may be ds,
+ *                    dy, s or h, where dx is not
+ *   grad_dtype       of dgain, dpost_gain and dgate: DC_F32, or dtype
+ *   dgain, dpost_gain  device [D], or NULL
+ *   dgate, ld_dgate  device [gate_rows, ld_dgate], or NULL
+ *   accumulate       1: added to what dgain, dpost_gain and dgate hold
+ * Other arguments as for dc_norm.  T = 0 gives the gradients' empty sums. */
+dc_status dc_norm_backward(int32_t dtype, int64_t T, int64_t D, const void* dy, int64_t ld_dy,
+                           const void* ds, int64_t ld_ds, const void* s, int64_t ld_s, const void* h,
+                           int64_t ld_h, const void* post_gain, const void* gate, int64_t gate_rows,
+                           int64_t ld_gate, const void* gain, float scale, float offset, float eps,
+                           void* dx, int64_t ld_dx, void* dh, int64_t ld_dh, int32_t grad_dtype,
+                           void* dgain, void* dpost_gain, void* dgate, int64_t ld_dgate,
+                           int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
