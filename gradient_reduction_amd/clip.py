@@ -40,6 +40,20 @@ def _runs(name, t):
 def gradients(grads, outs=None):
     """GRADIENT_DTYPE records of lists of tensors, every row counted."""
     recs = np.zeros(len(grads), dc.GRADIENT_DTYPE)
+    lists = (grads,) if outs is None else (grads, outs)
+    if all(all(map(torch.Tensor.is_contiguous, ts)) for ts in lists):
+        # one run each: a list call a field, a tenth of what a tensor at a time costs
+        shapes, kinds = [list(map(torch.Tensor.size, ts)) for ts in lists], [[t.dtype for t in ts] for ts in lists]
+        codes = {k: dtype_of(t) for k, t in {t.dtype: t for t in grads}.items()}
+        if shapes[0] == shapes[-1] and kinds[0] == kinds[-1]:
+            recs["grad"] = list(map(torch.Tensor.data_ptr, grads))
+            if outs is not None:
+                recs["out"] = list(map(torch.Tensor.data_ptr, outs))
+            n = np.array(list(map(torch.Tensor.numel, grads)), np.int64)
+            recs["cols"] = recs["ld_grad"] = recs["ld_out"] = n
+            recs["rows"] = recs["counted"] = n > 0
+            recs["dtype"] = [codes[k] for k in kinds[0]]
+            return recs
     for k, g in enumerate(grads):
         rows, cols, ld = _runs(f"gradient {k}", g)
         o, ld_out = 0, ld
@@ -66,10 +80,15 @@ def _list(tensors):
     ts = [tensors] if torch.is_tensor(tensors) else list(tensors)
     if not ts:
         raise ValueError("no gradients")
-    for k, t in enumerate(ts):
-        if t.device != ts[0].device:
-            raise ValueError(f"gradient {k} on {t.device}, expected {ts[0].device}")
-    return ts, ts[0].device
+    return ts, _one_device("gradient", ts, ts[0].device)
+
+
+def _one_device(name, ts, device):
+    if set(map(torch.Tensor.get_device, ts)) != {device.index if device.type == "cuda" else -1}:
+        for k, t in enumerate(ts):
+            if t.device != device:
+                raise ValueError(f"{name} {k} on {t.device}, expected {device}")
+    return device
 
 
 def _scalar(name, t, dtype, device):
@@ -119,9 +138,7 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, squares=None, stream=Non
         outs = [out] if torch.is_tensor(out) else list(out)
         if len(outs) != len(gs):
             raise ValueError(f"{len(outs)} outputs for {len(gs)} gradients")
-        for k, t in enumerate(outs):
-            if t.device != dev:
-                raise ValueError(f"out {k} on {t.device}, expected {dev}")
+        _one_device("out", outs, dev)
     recs = gradients(gs, outs)
     if squares is not None:
         _scalar("squares", squares, torch.float64, dev)

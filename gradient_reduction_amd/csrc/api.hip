@@ -1666,7 +1666,7 @@ dc_status dc_norm_backward_workspace(int32_t dtype, int64_t T, int64_t D, int64_
   dc_status st;
   if ((st = check_norm(dtype, T, D, gate_rows, nullptr, nullptr, nullptr, nullptr, 1.f, 0.f, 0.f))) return st;
   if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
-  *bytes = dc::norm_workspace(T, D, gate_rows);
+  *bytes = dc::norm_workspace(dtype, T, D, gate_rows);
   return ok();
 }
 
@@ -1702,7 +1702,7 @@ dc_status dc_norm_backward(int32_t dtype, int64_t T, int64_t D, const void* dy, 
       (st = check_apart(op, {&my, &md, &ms, &mh, &mp, &mg, &mw, &ox, &oh, &ow})) ||
       (st = check_apart(og, {&my, &md, &ms, &mh, &mp, &mg, &mw, &ox, &oh, &ow, &op})))
     return st;
-  if ((st = check_workspace(workspace, workspace_bytes, dc::norm_workspace(T, D, gate_rows)))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, dc::norm_workspace(dtype, T, D, gate_rows)))) return st;
   dc::NormLaunch l{};
   l.dtype = dtype, l.grad_dtype = grad_dtype;
   l.T = T, l.D = D, l.gate_rows = gate_rows;

@@ -115,12 +115,25 @@ __device__ __forceinline__ void load_unit(const Unit& t, u32x4 (&v)[kVectors]) {
   }
 }
 
+// The entry of unit u: every lane looks at one in 64 of the list's beginnings,
+// so that a long list costs one read of the arguments, not one per entry.
+template <class List>
+__device__ __forceinline__ int find_entry(const List& l, int32_t u) {
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < List::kMost; k += 64) {
+    const int e = k + (threadIdx.x & 63);
+    n += __popcll(__ballot(e < l.count && l.begin[e] <= u));
+  }
+  return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
 // partial[workgroup] (+)= the squares of its units.
 template <class List>
 __global__ void __launch_bounds__(256) k_squares(List l, double* partial, int32_t add) {
   double s = 0;
   const int32_t units = l.begin[l.count];
-  int e = 0;
+  int e = (int32_t)blockIdx.x < units ? find_entry(l, blockIdx.x) : 0;
   for (int32_t u = blockIdx.x; u < units; u += gridDim.x) {
     while (l.begin[e + 1] <= u) ++e;
     const Unit t = unit_at(l, e, u);
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int
   }
   if (in_place && c == 1.f) return;
   const int32_t units = l.begin[l.count];
-  int e = l.count - 1;
+  int e = (int32_t)blockIdx.x < units ? find_entry(l, units - 1 - (int32_t)blockIdx.x) : 0;
   for (int32_t u = units - 1 - (int32_t)blockIdx.x; u >= 0; u -= gridDim.x) {
     while (l.begin[e] > u) --e;
     const Unit t = unit_at(l, e, u);

@@ -41,8 +41,9 @@ __device__ __forceinline__ void load_columns(const T* p, int64_t left, float (&v
   for (int t = 0; t < V; ++t) v[t] = (float)x[t];
 }
 
-// V values rounded to T; columns past `left` are not written.
-template <class T, int V>
+// V values rounded to T; columns past `left` are not written.  WHOLE: `left` is
+// never between 0 and V.
+template <class T, int V, bool WHOLE = false>
 __device__ __forceinline__ void store_columns(T* p, int64_t left, const float (&v)[V]) {
   constexpr int B = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = B / sizeof(T);
   using A = typename Access<B>::type;
@@ -56,7 +57,7 @@ __device__ __forceinline__ void store_columns(T* p, int64_t left, const float (&
       __builtin_memcpy(&w, x + k * N, B);
       *reinterpret_cast<A*>(p + k * N) = w;
     }
-  } else {
+  } else if constexpr (!WHOLE) {
 #pragma unroll
     for (int t = 0; t < V; ++t)
       if (t < left) p[t] = x[t];
@@ -72,12 +73,17 @@ struct Pack {
     if constexpr (sizeof(T) == 2) return t & 1 ? bf16_hi(w[t / 2]) : bf16_lo(w[t / 2]);
     else return __uint_as_float(w[t]);
   }
+  // Keeps the compiler from carrying the widened values of a bf16 pack from
+  // what came before to what follows: twice the registers.
+  __device__ __forceinline__ void forget() {
+    if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(w));
+  }
+  // WHOLE: `left` is never between 0 and V.
+  template <bool WHOLE = false>
   __device__ __forceinline__ void load(const T* p, int64_t left) {
-    if (left >= V) {
-      w = *reinterpret_cast<const u32x4_any*>(p);
-      return;
-    }
     w = u32x4{0, 0, 0, 0};
+    if (left >= V) w = *reinterpret_cast<const u32x4_any*>(p);
+    if (WHOLE || left >= V) return;
 #pragma unroll
     for (int t = 0; t < V; ++t)
       if (t < left) {

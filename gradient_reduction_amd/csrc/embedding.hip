@@ -135,10 +135,17 @@ __global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
   }
   __syncthreads();
   if (!p.counts) {
-    for (int64_t i = threadIdx.x; i < p.n; i += 1024) {
-      const uint32_t g = (sort_key(p, ids, i) >> p.shift) & mask;
-      atomicAdd(&total[g], 1u);
-      if (i < i0) atomicAdd(&earlier[g], 1u);
+    // 16 keys' loads in flight; the first tiles are counted on their own
+    for (int64_t b = threadIdx.x; b < p.n; b += 16 * 1024) {
+      uint32_t g[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) g[k] = b + k * 1024 < p.n ? sort_key(p, ids, b + k * 1024) : 0;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if (b + k * 1024 >= p.n) break;
+        const uint32_t d = (g[k] >> p.shift) & mask;
+        atomicAdd(b + k * 1024 < i0 ? &earlier[d] : &total[d], 1u);
+      }
     }
   }
   uint32_t key[kSortItems], token[kSortItems], rank[kSortItems];
@@ -164,6 +171,7 @@ __global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
   }
   __syncthreads();
   // the digit's first place: tokens of smaller digits, then of earlier tiles
+  if (!p.counts) total[d] += earlier[d];
   uint32_t first = total[d];
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -194,6 +202,7 @@ __global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;   // sorted tokens per wave
 constexpr int kAhead = 4;   // rows in flight
+constexpr int kJoinTiles = 16;  // tiles that a workgroup of the join looks at
 constexpr int kFill = 16;   // rows of dE that a wave of the fill looks at
 
 struct RowSums {
@@ -290,44 +299,74 @@ __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
   }
 }
 
-// A row whose tokens reach over tiles: the workgroup of the tile in which it
-// ends adds up its partial sums, eight waves a run of them each.
+// A row whose tokens reach over tiles: the wave of the tile in which it ends
+// adds up its partial sums, kJoin loads in flight; with more than a few of
+// them the workgroup's four waves take a run each.
+constexpr int kJoin = 8;
+
 template <class G>
-__global__ void __launch_bounds__(512) k_row_join(RowSums a) {
+__global__ void __launch_bounds__(256) k_row_join(RowSums a) {
   constexpr int V = 4;
-  __shared__ float part[8][64][V];
+  __shared__ float part[4][64][V];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t tiles = (a.n + kTile - 1) / kTile, base = (int64_t)blockIdx.x * kJoinTiles;
+  // lane i looks at the tile base + i: whether a row that came in ends there
+  const int64_t mine = base + lane, p0 = mine * kTile, p1 = p0 + kTile < a.n ? p0 + kTile : a.n;
+  uint32_t first = 0;
+  bool ends = false;
+  if (lane < kJoinTiles && mine > 0 && mine < tiles) {
+    first = a.keys[p0];
+    ends = first < a.rows && a.keys[p0 - 1] == first && (p1 == a.n || a.keys[p1] != first);
+  }
+  uint64_t todo = __ballot(ends);
   const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
-  const int64_t tile = blockIdx.x, p0 = tile * kTile, p1 = p0 + kTile < a.n ? p0 + kTile : a.n;
-  const uint32_t key = a.keys[p0];
-  if (tile == 0 || key >= a.rows || a.keys[p0 - 1] != key) return;
-  if (p1 < a.n && a.keys[p1] == key) return;
-  const int64_t from = lower_bound(a.keys, p0, key) / kTile, parts = tile - from + 1;
-  const int64_t per = (parts + 7) / 8, k0 = wave * per, k1 = k0 + per < parts ? k0 + per : parts;
-  float sum[V] = {};
-  if (left > 0) {
-#pragma unroll 4
-    for (int64_t k = k0; k < k1; ++k) {
-      float v[V];
-      load_columns<float, V>(a.partial + ((from + k) * 2 + (k == 0 ? 1 : 0)) * a.D + j, left, v);
-#pragma unroll
-      for (int t = 0; t < V; ++t) sum[t] += v[t];
+  while (todo) {
+    const int at = __ffsll((unsigned long long)todo) - 1;
+    todo &= todo - 1;
+    const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)first, at);
+    const int64_t tile = base + at;
+    // the tiles before it that the row came into, 64 at a time
+    int64_t from = tile;
+    for (;;) {
+      const int64_t k = from - 1 - lane;
+      const uint64_t came = __ballot(k > 0 && a.keys[k > 0 ? k * kTile - 1 : 0] == key && a.keys[k > 0 ? k * kTile : 0] == key);
+      const int n = came == ~0ull ? 64 : __ffsll((unsigned long long)~came) - 1;
+      from -= n;
+      if (n < 64) break;
     }
-  }
+    --from;  // the one that it begins in
+    const int64_t parts = tile - from + 1;
+    const bool alone = parts <= 2 * kJoin;
+    if (alone && wave != (at & 3)) continue;
+    const int64_t per = alone ? parts : (parts + 3) / 4, k0 = alone ? 0 : wave * per;
+    const int64_t k1 = k0 + per < parts ? k0 + per : parts;
+    float sum[V] = {};
+    for (int64_t k = k0; k < k1; k += kJoin) {
+      float v[kJoin][V];
 #pragma unroll
-  for (int t = 0; t < V; ++t) part[wave][lane][t] = sum[t];
-  __syncthreads();
-  if (wave || left <= 0) return;
-  G* to = static_cast<G*>(a.dtable) + (int64_t)key * a.ld + j;
-  float y[V] = {};
-  if (a.accumulate) load_columns<G, V>(to, left, y);
+      for (int u = 0; u < kJoin; ++u)
+        load_columns<float, V>(a.partial + ((from + k + u) * 2 + (k + u == 0 ? 1 : 0)) * a.D + j, k + u < k1 ? left : 0, v[u]);
 #pragma unroll
-  for (int t = 0; t < V; ++t) {
-    float s = part[0][lane][t];
-    for (int w = 1; w < 8; ++w) s += part[w][lane][t];
-    y[t] = a.scale * s + y[t];
+      for (int u = 0; u < kJoin; ++u)
+#pragma unroll
+        for (int t = 0; t < V; ++t) sum[t] += v[u][t];
+    }
+    if (!alone) {
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < V; ++t) part[wave][lane][t] = sum[t];
+      __syncthreads();
+      if (wave) continue;
+#pragma unroll
+      for (int t = 0; t < V; ++t) sum[t] = (part[0][lane][t] + part[1][lane][t]) + (part[2][lane][t] + part[3][lane][t]);
+    }
+    G* to = static_cast<G*>(a.dtable) + (int64_t)key * a.ld + j;
+    float y[V] = {};
+    if (a.accumulate) load_columns<G, V>(to, left, y);
+#pragma unroll
+    for (int t = 0; t < V; ++t) y[t] = a.scale * sum[t] + y[t];
+    store_columns<G, V>(to, left, y);
   }
-  store_columns<G, V>(to, left, y);
 }
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -392,7 +431,8 @@ void row_sums(const RowSums& s, int64_t tiles, hipStream_t stream) {
   const int64_t fill = a.accumulate ? 0 : (a.rows + 4 * kFill - 1) / (4 * kFill);
   if (a.tile_blocks + fill) k_row_sums<T, G><<<dim3((uint32_t)(a.tile_blocks + fill), across), 256, 0, stream>>>(a);
   if (tiles > 1)
-    k_row_join<G><<<dim3((uint32_t)tiles, (uint32_t)((a.D + 255) / 256)), 512, 0, stream>>>(a);
+    k_row_join<G><<<dim3((uint32_t)((tiles + kJoinTiles - 1) / kJoinTiles), (uint32_t)((a.D + 255) / 256)), 256, 0,
+                    stream>>>(a);
 }
 
 }  // namespace

@@ -278,7 +278,7 @@ struct NormLaunch {
   void* workspace;
 };
 int64_t norm_most_columns();
-int64_t norm_workspace(int64_t T, int64_t D, int64_t gate_rows);
+int64_t norm_workspace(int32_t dtype, int64_t T, int64_t D, int64_t gate_rows);
 hipError_t launch_norm(const NormLaunch& l, hipStream_t stream);
 hipError_t launch_norm_backward(const NormLaunch& l, hipStream_t stream);
 

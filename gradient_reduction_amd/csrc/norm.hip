@@ -14,6 +14,9 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <type_traits>
+#include <utility>
 
 #include "columns.h"
 #include "device_common.h"
@@ -24,15 +27,47 @@ namespace {
 
 constexpr int kEach = 16;  // values of a row per thread
 
+// v and its partner's value added, for partners inside 16 lanes (CTRL: which),
+// 16 or 32 lanes apart: register moves, where a shuffle goes through LDS.
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+  const int2 x = __builtin_bit_cast(int2, v);
+  const int2 y = {__builtin_amdgcn_update_dpp(0, x.x, CTRL, 0xf, 0xf, true),
+                  __builtin_amdgcn_update_dpp(0, x.y, CTRL, 0xf, 0xf, true)};
+  return v + __builtin_bit_cast(double, y);
+}
+template <int APART>
+__device__ __forceinline__ double add_apart(double v) {
+  const uint2 x = __builtin_bit_cast(uint2, v);
+  uint2 a, b;
+  if constexpr (APART == 16) {
+    const auto lo = __builtin_amdgcn_permlane16_swap(x.x, x.x, false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(x.y, x.y, false, false);
+    a = {lo[0], hi[0]}, b = {lo[1], hi[1]};
+  } else {
+    const auto lo = __builtin_amdgcn_permlane32_swap(x.x, x.x, false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap(x.y, x.y, false, false);
+    a = {lo[0], hi[0]}, b = {lo[1], hi[1]};
+  }
+  return __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b);
+}
+template <int G>
+__device__ __forceinline__ double lanes_total(double v) {
+  v = add_dpp<0xB1>(v);   // lane ^ 1
+  v = add_dpp<0x4E>(v);   // lane ^ 2
+  v = add_dpp<0x141>(v);  // mirrored in 8
+  v = add_dpp<0x140>(v);  // mirrored in 16
+  if constexpr (G >= 64) v = add_apart<32>(add_apart<16>(v));
+  return v;
+}
+
 // Sums over the G threads of a row, N at once, to all of them.  With rows of
 // more than a wave every thread of the workgroup must come, and `buf` is
 // written anew: the caller keeps two calls on one buffer a barrier apart.
 template <int G, int N, int THREADS>
 __device__ __forceinline__ void row_total(double (&v)[N], double (*buf)[THREADS / 64]) {
 #pragma unroll
-  for (int o = (G < 64 ? G : 64) / 2; o; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], o);
+  for (int k = 0; k < N; ++k) v[k] = lanes_total<G>(v[k]);
   if constexpr (G > 64) {
     constexpr int W = G / 64;
     const int wave = threadIdx.x >> 6, first = wave / W * W;
@@ -50,6 +85,65 @@ __device__ __forceinline__ void row_total(double (&v)[N], double (*buf)[THREADS 
   }
 }
 
+// A row as a buffer: what lies past its columns, or of a row or an operand that
+// is not there, loads as zeros and is not stored, without a branch.  (Behind a
+// branch around a load every later wait is for all loads in flight, the next
+// row's among them.)  For rows of whole 16 bytes; `row` is the wave's.
+// The stores are streamed (nt): 8192 rows of 4096 bf16 backward take 84 us with
+// it, 95 without, 89 with the loads streamed too.
+constexpr int kStoreStream = 2;
+template <class T>
+struct RowBuffer {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ RowBuffer(const T* p, int64_t row, int64_t ld, int D, bool there) {
+    r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p + (there ? row : 0) * ld), (short)0,
+                                          p && there ? D * (int)sizeof(T) : 0, kBufferFlags);
+  }
+  __device__ __forceinline__ u32x4 load(int j) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, j * (int)sizeof(T), 0, 0);
+  }
+  template <int V>
+  __device__ __forceinline__ void store(int j, const float (&v)[V]) const {
+    T x[V];
+#pragma unroll
+    for (int t = 0; t < V; ++t) x[t] = (T)v[t];
+    u32x4 w;
+    __builtin_memcpy(&w, x, 16);
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, j * (int)sizeof(T), 0, kStoreStream);
+  }
+};
+
+// One row of an operand, either way.
+template <class T, int N, bool DIRECT>
+__device__ __forceinline__ void load_row(Pack<T> (&v)[N], const T* p, int64_t row, int64_t ld, int D, bool there,
+                                         int lane, int G) {
+  if constexpr (DIRECT) {
+    const RowBuffer<T> b(p, row, ld, D, there);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k].w = b.load((lane + G * k) * Pack<T>::V);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int j = (lane + G * k) * Pack<T>::V;
+      v[k].w = u32x4{0, 0, 0, 0};
+      if (p && there) v[k].load(p + row * ld + j, D - j);
+    }
+  }
+}
+template <class T, int N, int V, bool DIRECT>
+__device__ __forceinline__ void store_row(const float (&v)[N][V], T* p, int64_t row, int64_t ld, int D, bool there,
+                                          int lane, int G) {
+  if constexpr (DIRECT) {
+    const RowBuffer<T> b(p, row, ld, D, there);
+#pragma unroll
+    for (int k = 0; k < N; ++k) b.store((lane + G * k) * V, v[k]);
+  } else {
+    if (!p || !there) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k) store_columns<T, V>(p + row * ld + (lane + G * k) * V, D - (lane + G * k) * V, v[k]);
+  }
+}
+
 // 1 / sqrt(m): the hardware's where fp32 holds m well inside its range.
 __device__ __forceinline__ float inverse_root(double m) {
   if (m > 1e-30 && m < 1e30) return __builtin_amdgcn_rsqf((float)m);
@@ -60,39 +154,34 @@ template <class T>
 struct NormIn {
   int64_t T_, D;
   const T *x, *h, *post, *gate, *gain;
-  int64_t ld_x, ld_h, ld_gate, per_gate;  // tokens per row of the gate
+  int64_t ld_x, ld_h, ld_gate, per_gate, gate_rows;  // per_gate: tokens per row of the gate
   float scale, offset;
   double eps, over;                       // over = 1 / D
   T *s, *y;
   int64_t ld_s, ld_y;
 };
 
-template <class T, int G, int THREADS>
+template <class T, int G, int THREADS, bool DIRECT>
 __global__ void __launch_bounds__(THREADS) k_norm(NormIn<T> a) {
   constexpr int V = 16 / sizeof(T), N = kEach / V, ROWS = THREADS / G;
   __shared__ double buf[2][1][THREADS / 64];
-  const int lane = threadIdx.x % G;
+  const int lane = threadIdx.x % G, D = (int)a.D;
+  const int group = G < 64 ? threadIdx.x / G : __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.T_; row0 += (int64_t)gridDim.x * ROWS) {
-    const int64_t row = row0 + threadIdx.x / G;
+    const int64_t row = row0 + group;
     const bool in = row < a.T_;
+    Pack<T> x[N], h[N], post[N], gate[N], gain[N];
+    load_row<T, N, DIRECT>(x, a.x, row, a.ld_x, D, in, lane, G);
+    load_row<T, N, DIRECT>(h, a.h, row, a.ld_h, D, in, lane, G);
+    load_row<T, N, DIRECT>(post, a.post, 0, 0, D, true, lane, G);
+    load_row<T, N, DIRECT>(gate, a.gate, in && a.gate_rows > 1 ? row / a.per_gate : 0, a.ld_gate, D, true, lane, G);
+    load_row<T, N, DIRECT>(gain, a.gain, 0, 0, D, true, lane, G);
     float s[N][V];
-    {
-      Pack<T> x[N];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V;
-        x[k].load(a.x + row * a.ld_x + j, in ? a.D - j : 0);
+    for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int t = 0; t < V; ++t) s[k][t] = x[k][t];
-      }
-    }
+      for (int t = 0; t < V; ++t) s[k][t] = x[k][t];
     if (a.h) {
-      Pack<T> h[N];
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V;
-        h[k].load(a.h + row * a.ld_h + j, in ? a.D - j : 0);
-      }
       float r = 1.f;
       if (a.post) {
         double sum[1] = {0};
@@ -106,23 +195,17 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormIn<T> a) {
         row_total<G, 1, THREADS>(sum, buf[0]);
         r = inverse_root(__builtin_fma(sum[0], a.over, a.eps));
       }
-      const T* gate = a.gate ? a.gate + (in ? row / a.per_gate : 0) * a.ld_gate : nullptr;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V, left = in ? a.D - j : 0;
-        Pack<T> p, g;
-        if (a.post) p.load(a.post + j, left);
-        if (gate) g.load(gate + j, left);
+      for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
           float u = h[k][t] * r;
-          if (a.post) u *= a.offset + p[t];
+          if (a.post) u *= a.offset + post[k][t];
           u *= a.scale;
-          if (gate) u *= g[t];
+          if (a.gate) u *= gate[k][t];
           s[k][t] += u;
         }
-        if (a.s) store_columns<T, V>(a.s + row * a.ld_s + j, left, s[k]);
-      }
+      store_row<T, N, V, DIRECT>(s, a.s, row, a.ld_s, D, in, lane, G);
     }
     if (a.gain) {
       double sum[1] = {0};
@@ -133,14 +216,10 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormIn<T> a) {
       row_total<G, 1, THREADS>(sum, buf[1]);
       const float r = inverse_root(__builtin_fma(sum[0], a.over, a.eps));
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V, left = in ? a.D - j : 0;
-        Pack<T> p;
-        p.load(a.gain + j, left);
+      for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int t = 0; t < V; ++t) s[k][t] = s[k][t] * r * (a.offset + p[t]);
-        store_columns<T, V>(a.y + row * a.ld_y + j, left, s[k]);
-      }
+        for (int t = 0; t < V; ++t) s[k][t] = s[k][t] * r * (a.offset + gain[k][t]);
+      store_row<T, N, V, DIRECT>(s, a.y, row, a.ld_y, D, in, lane, G);
     }
     if constexpr (G > 64) __syncthreads();  // buf is free for the next row
   }
@@ -164,20 +243,20 @@ struct NormBack {
 };
 
 // Adds every row group's column sums up in `cols` (LDS) and writes them.
-template <class T, int G, int THREADS>
-__device__ __forceinline__ void columns_out(float (&sum)[kEach], float* cols, float* to, int64_t D) {
+template <class T, int G, int EACH, int THREADS>
+__device__ __forceinline__ void columns_out(float (&sum)[EACH], float* cols, float* to, int64_t D) {
   constexpr int V = 16 / sizeof(T), ROWS = THREADS / G;
   const int lane = threadIdx.x % G, mine = threadIdx.x / G;
   auto at = [&](int e) { return (lane + G * (e / V)) * V + e % V; };
   if constexpr (ROWS == 1) {
 #pragma unroll
-    for (int e = 0; e < kEach; ++e)
+    for (int e = 0; e < EACH; ++e)
       if (at(e) < D) to[at(e)] = sum[e];
   } else {
     for (int r = 0; r < ROWS; ++r) {
       if (mine == r)
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) cols[at(e)] = r ? cols[at(e)] + sum[e] : sum[e];
+        for (int e = 0; e < EACH; ++e) cols[at(e)] = r ? cols[at(e)] + sum[e] : sum[e];
       __syncthreads();
     }
     for (int64_t j = threadIdx.x; j < D; j += THREADS) to[j] = cols[j];
@@ -185,108 +264,108 @@ __device__ __forceinline__ void columns_out(float (&sum)[kEach], float* cols, fl
   }
 }
 
+// What the backward reads of a token's row.
+template <class T, int N>
+struct BackRow {
+  Pack<T> s[N], dy[N], ds[N], h[N];
+};
+
 // Every row group takes a run of neighbouring rows and keeps the column sums of
-// the parameters' gradients in registers.  GATES: the gate has several rows;
-// its sums are handed out where a gate row ends.  Without, sum_t d m is kept,
-// which gives dpost and dgate both (k_norm_join).
-template <class T, class G_, int G, int THREADS, bool GATES>
+// the parameters' gradients in registers; the next row's loads are under way
+// while a row is worked on (bf16; fp32 rows fill the registers).  GATES: the
+// gate has several rows; its sums are handed out where a gate row ends.
+// Without, sum_t d m is kept, which gives dpost and dgate both (k_norm_join).
+template <class T, class G_, int G, int EACH, int THREADS, bool GATES, bool DIRECT>
 __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
-  constexpr int V = 16 / sizeof(T), N = kEach / V, ROWS = THREADS / G;
+  constexpr int V = 16 / sizeof(T), N = EACH / V, ROWS = THREADS / G;
+  constexpr bool AHEAD = THREADS <= 512;
   __shared__ double buf[2][3][THREADS / 64];
-  __shared__ float cols[ROWS == 1 ? 1 : G * kEach];
-  const int lane = threadIdx.x % G;
-  const int64_t run = (int64_t)blockIdx.x * ROWS + threadIdx.x / G, first = run * a.run;
+  __shared__ float cols[ROWS == 1 ? 1 : G * EACH];
+  const int lane = threadIdx.x % G, D = (int)a.D;
+  // (a wave is of one row: what follows from it is scalar)
+  const int group = G < 64 ? threadIdx.x / G : __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+  const int64_t run = (int64_t)blockIdx.x * ROWS + group, first = run * a.run;
   const int64_t end = first + a.run < a.T_ ? first + a.run : a.T_;
-  float sum_gain[kEach] = {}, sum_post[kEach] = {}, sum_gate[GATES ? kEach : 1] = {};
+  float sum_gain[EACH] = {}, sum_post[EACH] = {}, sum_gate[GATES ? EACH : 1] = {};
+  auto load = [&](BackRow<T, N>& r, int64_t row) {
+    const bool in = row < end;
+    load_row<T, N, DIRECT>(r.s, a.s, row, a.ld_s, D, in, lane, G);
+    load_row<T, N, DIRECT>(r.dy, a.dy, row, a.ld_dy, D, in, lane, G);
+    load_row<T, N, DIRECT>(r.h, a.h, row, a.ld_h, D, in, lane, G);
+    load_row<T, N, DIRECT>(r.ds, a.ds, row, a.ld_ds, D, in, lane, G);
+  };
+  Pack<T> gain[N], post[N], gate[N];
+  load_row<T, N, DIRECT>(gain, a.gain, 0, 0, D, true, lane, G);
+  load_row<T, N, DIRECT>(post, a.post, 0, 0, D, true, lane, G);
+  if constexpr (!GATES) load_row<T, N, DIRECT>(gate, a.gate, 0, 0, D, true, lane, G);
+  BackRow<T, N> cur;
+  load(cur, first);
   for (int64_t i = 0; i < a.run; ++i) {
     const int64_t row = first + i;
-    const bool in = row < a.T_;
-    Pack<T> s[N], dy[N], h[N];
+    const bool in = row < end;
+    BackRow<T, N> next;
+    if constexpr (AHEAD) load(next, row + 1);
     float d[N][V];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int64_t j = (int64_t)(lane + G * k) * V, left = in ? a.D - j : 0;
-      if (a.gain) {
-        s[k].load(a.s + row * a.ld_s + j, left);
-        dy[k].load(a.dy + row * a.ld_dy + j, left);
-      }
-      if (a.h) h[k].load(a.h + row * a.ld_h + j, left);
-      Pack<T> v;
-      v.w = u32x4{0, 0, 0, 0};
-      if (a.ds) v.load(a.ds + row * a.ld_ds + j, left);
-#pragma unroll
-      for (int t = 0; t < V; ++t) d[k][t] = v[t];
-    }
     double sum[3] = {0, 0, 0};
     if (a.gain) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V;
-        Pack<T> p;
-        p.load(a.gain + j, a.D - j);
+      for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const double v = s[k][t], q = dy[k][t] * (a.offset + p[t]);
+          const double v = cur.s[k][t], q = cur.dy[k][t] * (a.offset + gain[k][t]);
           sum[0] = __builtin_fma(v, v, sum[0]);
           sum[1] = __builtin_fma(q, v, sum[1]);
         }
-      }
     }
     if (a.post) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const double v = h[k][t];
+          const double v = cur.h[k][t];
           sum[2] = __builtin_fma(v, v, sum[2]);
         }
     }
     row_total<G, 3, THREADS>(sum, buf[0]);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      cur.s[k].forget(), cur.dy[k].forget(), cur.h[k].forget(), gain[k].forget();
+#pragma unroll
+      for (int t = 0; t < V; ++t) d[k][t] = cur.ds[k][t];
+    }
     if (a.gain) {
       // (a row past the last one adds zeros, whatever eps is)
       const float r = in ? inverse_root(__builtin_fma(sum[0], a.over, a.eps)) : 0.f;
       const float mean = (float)(sum[1] * a.over * r);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V;
-        Pack<T> p;
-        p.load(a.gain + j, a.D - j);
+      for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const float n = s[k][t] * r, q = dy[k][t] * (a.offset + p[t]);
-          sum_gain[k * V + t] += dy[k][t] * n;
-          d[k][t] += r * (q - n * mean);
+          const float n = cur.s[k][t] * r, y = cur.dy[k][t], q = y * (a.offset + gain[k][t]);
+          sum_gain[k * V + t] = __builtin_fmaf(y, n, sum_gain[k * V + t]);
+          d[k][t] = __builtin_fmaf(r, q - n * mean, d[k][t]);
         }
-      }
     }
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int64_t j = (int64_t)(lane + G * k) * V, left = in ? a.D - j : 0;
-      if (a.dx) store_columns<T, V>(a.dx + row * a.ld_dx + j, left, d[k]);
-    }
+    store_row<T, N, V, DIRECT>(d, a.dx, row, a.ld_dx, D, in, lane, G);
     if (a.h) {
       const float r = !in ? 0.f : a.post ? inverse_root(__builtin_fma(sum[2], a.over, a.eps)) : 1.f;
       const int64_t gate_row = GATES && in ? row / a.per_gate : 0;
-      const T* gate = a.gate ? a.gate + gate_row * a.ld_gate : nullptr;
+      if constexpr (GATES) load_row<T, N, DIRECT>(gate, a.gate, gate_row, a.ld_gate, D, true, lane, G);
       float g[N][V];
       double dot[1] = {0};
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const int64_t j = (int64_t)(lane + G * k) * V;
-        Pack<T> p, w;
-        if (a.post) p.load(a.post + j, a.D - j);
-        if (gate) w.load(gate + j, a.D - j);
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const float m = h[k][t] * r, gain = a.post ? a.offset + p[t] : 1.f;
-          const float du = a.scale * d[k][t] * (gate ? w[t] : 1.f);
+          const float m = cur.h[k][t] * r, w = a.post ? a.offset + post[k][t] : 1.f, v = a.scale * d[k][t];
+          const float du = a.gate ? v * gate[k][t] : v;
           if constexpr (GATES) {
-            sum_post[k * V + t] += du * m;
-            sum_gate[k * V + t] += a.scale * d[k][t] * (m * gain);
+            sum_post[k * V + t] = __builtin_fmaf(du, m, sum_post[k * V + t]);
+            sum_gate[k * V + t] = __builtin_fmaf(v, m * w, sum_gate[k * V + t]);
           } else {
-            sum_post[k * V + t] += d[k][t] * m;
+            sum_post[k * V + t] = __builtin_fmaf(d[k][t], m, sum_post[k * V + t]);
           }
-          g[k][t] = du * gain;
+          g[k][t] = du * w;
           dot[0] = __builtin_fma((double)g[k][t], (double)m, dot[0]);
         }
       }
@@ -295,22 +374,20 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
         row_total<G, 1, THREADS>(dot, buf[1]);
         mean = (float)(dot[0] * a.over);
       }
-      if (a.dh) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int64_t j = (int64_t)(lane + G * k) * V, left = in ? a.D - j : 0;
+      for (int k = 0; k < N; ++k) cur.h[k].forget(), post[k].forget(), gate[k].forget();
 #pragma unroll
-          for (int t = 0; t < V; ++t) g[k][t] = r * (g[k][t] - h[k][t] * r * mean);
-          store_columns<T, V>(a.dh + row * a.ld_dh + j, left, g[k]);
-        }
-      }
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int t = 0; t < V; ++t) g[k][t] = r * (g[k][t] - cur.h[k][t] * r * mean);
+      store_row<T, N, V, DIRECT>(g, a.dh, row, a.ld_dh, D, in, lane, G);
       if constexpr (GATES) {
         const int64_t g0 = gate_row * a.per_gate, g1 = g0 + a.per_gate;
         if (a.sums_gate && in && (row + 1 == g1 || row + 1 == end)) {
           const bool here = g0 >= first && g1 <= end;
 #pragma unroll
           for (int k = 0; k < N; ++k) {
-            const int64_t j = (int64_t)(lane + G * k) * V, left = a.D - j;
+            const int j = (lane + G * k) * V, left = D - j;
             float v[V];
 #pragma unroll
             for (int t = 0; t < V; ++t) v[t] = sum_gate[k * V + t];
@@ -328,15 +405,19 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
             }
           }
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) sum_gate[e] = 0.f;
+          for (int e = 0; e < EACH; ++e) sum_gate[e] = 0.f;
         }
       }
     }
+#pragma unroll
+    for (int k = 0; k < N; ++k) gain[k].forget();
     if constexpr (G > 64) __syncthreads();
+    if constexpr (AHEAD) cur = next;
+    else load(cur, row + 1);
   }
-  if (a.gain) columns_out<T, G, THREADS>(sum_gain, cols, a.partial + (int64_t)blockIdx.x * a.D, a.D);
+  if (a.gain) columns_out<T, G, EACH, THREADS>(sum_gain, cols, a.partial + (int64_t)blockIdx.x * a.D, a.D);
   if (a.sums_post)
-    columns_out<T, G, THREADS>(sum_post, cols, a.partial + ((int64_t)gridDim.x + blockIdx.x) * a.D, a.D);
+    columns_out<T, G, EACH, THREADS>(sum_post, cols, a.partial + ((int64_t)gridDim.x + blockIdx.x) * a.D, a.D);
 }
 
 template <class T, class G_>
@@ -360,8 +441,10 @@ __global__ void __launch_bounds__(256) k_norm_join(NormJoin<T, G_> a) {
   const int which = a.from + (int)blockIdx.y;
   const float* p = a.partial + (int64_t)which * a.blocks * a.D;
   float v = 0.f;
-  if (j < a.D)
+  if (j < a.D) {
+#pragma unroll 16
     for (int32_t b = l; b < a.blocks; b += 8) v += p[b * a.D + j];
+  }
   sum[l][c] = v;
   __syncthreads();
   if (l || j >= a.D) return;
@@ -398,21 +481,38 @@ __global__ void __launch_bounds__(256) k_gate_join(int64_t D, int64_t T_, int64_
   }
 }
 
-// Threads per row, and of the workgroup in the backward.
+// Threads per row.  Backward a thread takes 32 bytes of a row of each operand
+// (64 for fp32 rows of more than 8192), and a workgroup 512 threads: two waves
+// a SIMD, whose 256 registers hold two rows' operands and the sums.
 int row_threads(int64_t D) { return D <= 256 ? 16 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
+int back_row_threads(int32_t dtype, int64_t D) {
+  const int64_t n = dtype == DC_BF16 ? 16 : 8;
+  return D <= 16 * n ? 16 : D <= 64 * n ? 64 : D <= 256 * n ? 256 : D <= 512 * n ? 512 : 1024;
+}
+constexpr int back_threads(int g) { return g > 512 ? g : 512; }
 
 // Runs of the backward: about one workgroup a compute unit, each row group
 // with as few rows as that leaves.
 constexpr int64_t kBlocks = 256;
 struct Runs {
   int64_t rows, count, blocks;
-  Runs(int64_t T, int64_t D) {
-    const int64_t groups = 1024 / row_threads(D);
+  Runs(int32_t dtype, int64_t T, int64_t D) {
+    const int g = back_row_threads(dtype, D);
+    const int64_t groups = back_threads(g) / g;
     rows = std::max<int64_t>(1, (T + kBlocks * groups - 1) / (kBlocks * groups));
     count = (T + rows - 1) / rows;
     blocks = std::max<int64_t>(1, (count + groups - 1) / groups);
   }
 };
+
+// Whether rows are whole 16 bytes apart and long, from a 16-byte boundary.
+template <class T>
+bool direct_rows(int64_t D, std::initializer_list<std::pair<const void*, int64_t>> rows) {
+  bool yes = D % Pack<T>::V == 0;
+  for (const auto& r : rows)
+    yes &= r.first == nullptr || (reinterpret_cast<uintptr_t>(r.first) % 16 == 0 && r.second % Pack<T>::V == 0);
+  return yes;
+}
 
 template <class T>
 hipError_t norm(const NormLaunch& l, hipStream_t stream) {
@@ -436,29 +536,37 @@ hipError_t norm(const NormLaunch& l, hipStream_t stream) {
   a.y = static_cast<T*>(l.y);
   a.ld_s = l.ld_out_s;
   a.ld_y = l.ld_y;
-  auto launch = [&](auto kernel, int threads, int rows) {
-    const int64_t blocks = std::min<int64_t>((l.T + rows - 1) / rows, (int64_t)1 << 20);
-    kernel<<<dim3((uint32_t)blocks), threads, 0, stream>>>(a);
+  a.gate_rows = l.gate_rows;
+  const bool direct = direct_rows<T>(l.D, {{l.x, l.ld_x}, {l.h, l.ld_h}, {l.post, 0}, {l.gain, 0},
+                                           {l.gate, l.gate_rows > 1 ? l.ld_gate : 0}, {l.out_s, l.ld_out_s}, {l.y, l.ld_y}});
+  auto launch = [&](auto g) {
+    constexpr int kG = decltype(g)::value, kThreads = kG > 256 ? kG : 256, kRows = kThreads / kG;
+    auto kernel = k_norm<T, kG, kThreads, false>;
+    if constexpr (kG >= 64) {  // (a row to a wave)
+      if (direct) kernel = k_norm<T, kG, kThreads, true>;
+    }
+    const int64_t blocks = std::min<int64_t>((l.T + kRows - 1) / kRows, (int64_t)1 << 20);
+    kernel<<<dim3((uint32_t)blocks), kThreads, 0, stream>>>(a);
   };
   switch (row_threads(l.D)) {
-    case 16: launch(k_norm<T, 16, 256>, 256, 16); break;
-    case 64: launch(k_norm<T, 64, 256>, 256, 4); break;
-    case 256: launch(k_norm<T, 256, 256>, 256, 1); break;
-    default: launch(k_norm<T, 1024, 1024>, 1024, 1); break;
+    case 16: launch(std::integral_constant<int, 16>{}); break;
+    case 64: launch(std::integral_constant<int, 64>{}); break;
+    case 256: launch(std::integral_constant<int, 256>{}); break;
+    default: launch(std::integral_constant<int, 1024>{}); break;
   }
   return hipGetLastError();
 }
 
 template <class T, class G_>
 hipError_t norm_back(const NormLaunch& l, hipStream_t stream) {
-  const Runs runs(l.T, l.D);
+  const Runs runs(l.dtype, l.T, l.D);
   const bool gates = l.gate && l.gate_rows > 1;
   NormBack<T, G_> a{};
   a.T_ = l.T;
   a.D = l.D;
-  a.dy = static_cast<const T*>(l.dy);
+  a.dy = static_cast<const T*>(l.gain ? l.dy : nullptr);
   a.ds = static_cast<const T*>(l.ds);
-  a.s = static_cast<const T*>(l.x);
+  a.s = static_cast<const T*>(l.gain ? l.x : nullptr);
   a.h = static_cast<const T*>(l.h);
   a.post = static_cast<const T*>(l.post);
   a.gate = static_cast<const T*>(l.gate);
@@ -485,15 +593,28 @@ hipError_t norm_back(const NormLaunch& l, hipStream_t stream) {
   a.run = runs.rows;
   a.partial = static_cast<float*>(l.workspace);
   a.gate_partial = a.partial + 2 * runs.blocks * l.D;
-  auto launch = [&](auto one, auto several, int threads) {
-    if (gates) several<<<dim3((uint32_t)runs.blocks), threads, 0, stream>>>(a);
-    else one<<<dim3((uint32_t)runs.blocks), threads, 0, stream>>>(a);
+  const bool direct = direct_rows<T>(
+      l.D, {{a.dy, l.ld_dy}, {l.ds, l.ld_ds}, {a.s, l.ld_x}, {l.h, l.ld_h}, {l.post, 0}, {l.gain, 0},
+            {l.gate, gates ? l.ld_gate : 0}, {l.dx, l.ld_dx}, {l.dh, l.ld_dh}});
+  auto launch = [&](auto g, auto each) {
+    constexpr int kG = decltype(g)::value, kE = decltype(each)::value, kThreads = back_threads(kG);
+    auto kernel = k_norm_back<T, G_, kG, kE, kThreads, false, false>;
+    if (gates) kernel = k_norm_back<T, G_, kG, kE, kThreads, true, false>;
+    if constexpr (kG >= 64) {  // (a row to a wave)
+      if (direct && gates) kernel = k_norm_back<T, G_, kG, kE, kThreads, true, true>;
+      else if (direct) kernel = k_norm_back<T, G_, kG, kE, kThreads, false, true>;
+    }
+    kernel<<<dim3((uint32_t)runs.blocks), kThreads, 0, stream>>>(a);
   };
-  switch (row_threads(l.D)) {
-    case 16: launch(k_norm_back<T, G_, 16, 1024, false>, k_norm_back<T, G_, 16, 1024, true>, 1024); break;
-    case 64: launch(k_norm_back<T, G_, 64, 1024, false>, k_norm_back<T, G_, 64, 1024, true>, 1024); break;
-    case 256: launch(k_norm_back<T, G_, 256, 1024, false>, k_norm_back<T, G_, 256, 1024, true>, 1024); break;
-    default: launch(k_norm_back<T, G_, 1024, 1024, false>, k_norm_back<T, G_, 1024, 1024, true>, 1024); break;
+  constexpr std::integral_constant<int, 32 / sizeof(T)> each;
+  switch (back_row_threads(l.dtype, l.D)) {
+    case 16: launch(std::integral_constant<int, 16>{}, each); break;
+    case 64: launch(std::integral_constant<int, 64>{}, each); break;
+    case 256: launch(std::integral_constant<int, 256>{}, each); break;
+    case 512: launch(std::integral_constant<int, 512>{}, each); break;
+    default:
+      if (l.D <= 1024 * each) launch(std::integral_constant<int, 1024>{}, each);
+      else launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, kEach>{});
   }
   NormJoin<T, G_> j{};
   j.D = l.D;
@@ -523,8 +644,8 @@ hipError_t norm_back(const NormLaunch& l, hipStream_t stream) {
 
 int64_t norm_most_columns() { return 1024 * kEach; }
 
-int64_t norm_workspace(int64_t T, int64_t D, int64_t gate_rows) {
-  const Runs runs(T, D);
+int64_t norm_workspace(int32_t dtype, int64_t T, int64_t D, int64_t gate_rows) {
+  const Runs runs(dtype, T, D);
   return 4 * D * (2 * runs.blocks + (gate_rows > 1 ? 2 * runs.count : 0));
 }
 
