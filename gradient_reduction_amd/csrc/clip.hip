@@ -18,7 +18,22 @@
 namespace dc {
 namespace {
 
-constexpr int64_t kUnit = 16384;      // bytes
+#ifndef DC_UNIT
+#define DC_UNIT 16384
+#endif
+#ifndef DC_PARTS
+#define DC_PARTS 2048
+#endif
+#ifndef DC_NTL
+#define DC_NTL 0
+#endif
+#ifndef DC_NTC
+#define DC_NTC 0
+#endif
+#ifndef DC_NTS
+#define DC_NTS 0
+#endif
+constexpr int64_t kUnit = DC_UNIT;      // bytes
 constexpr int64_t kLaunchUnits = (int64_t)1 << 30;
 
 // Flat gradients of one launch: numel2 = 2 numel + (fp32).
@@ -105,12 +120,13 @@ __device__ __forceinline__ u32x4 load_part(const char* p, int have, bool wide) {
 }
 
 // Vectors of a unit: elements past its end read as zeros.
+template <bool NT>
 __device__ __forceinline__ void load_unit(const Unit& t, u32x4 (&v)[kVectors]) {
   const int V = t.wide ? 4 : 8;
 #pragma unroll
   for (int j = 0; j < kVectors; ++j) {
     const int i = j * 256 + (int)threadIdx.x, have = t.n - i * V;
-    if (have >= V) v[j] = *reinterpret_cast<const u32x4_any*>(t.grad + 16 * i);
+    if (have >= V) v[j] = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(t.grad + 16 * i)) : *reinterpret_cast<const u32x4_any*>(t.grad + 16 * i);
     else v[j] = have > 0 ? load_part(t.grad + 16 * i, have, t.wide) : u32x4{0, 0, 0, 0};
   }
 }
@@ -138,7 +154,7 @@ __global__ void __launch_bounds__(256) k_squares(List l, double* partial, int32_
     while (l.begin[e + 1] <= u) ++e;
     const Unit t = unit_at(l, e, u);
     u32x4 v[kVectors];
-    load_unit(t, v);
+    load_unit<DC_NTL>(t, v);
 #pragma unroll
     for (int j = 0; j < kVectors; ++j)
 #pragma unroll
@@ -200,7 +216,7 @@ __global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int
     while (l.begin[e] > u) --e;
     const Unit t = unit_at(l, e, u);
     u32x4 v[kVectors];
-    load_unit(t, v);
+    load_unit<DC_NTC>(t, v);
     const int V = t.wide ? 4 : 8;
 #pragma unroll
     for (int j = 0; j < kVectors; ++j) {
@@ -214,7 +230,8 @@ __global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int
       }
       char* to = t.out + 16 * i;
       if (have >= V) {
-        *reinterpret_cast<u32x4_any*>(to) = y;
+        if (DC_NTS) __builtin_nontemporal_store((u32x4_any)y, reinterpret_cast<u32x4_any*>(to));
+        else *reinterpret_cast<u32x4_any*>(to) = y;
       } else if (t.wide) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -275,7 +292,7 @@ void for_lists(const dc_gradient* grads, int32_t num, Rows rows, bool writes, F&
 
 // Workgroups of a launch: eight of 256 threads a compute unit, 2048 in all,
 // hold every wave that fits, and their sums are 16 KB.
-constexpr int32_t kParts = 2048;
+constexpr int32_t kParts = DC_PARTS;
 
 int32_t counted(const dc_gradient* grads, int32_t num) {
   int32_t most = 1;

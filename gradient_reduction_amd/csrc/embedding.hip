@@ -61,7 +61,7 @@ constexpr int kSortItems = 4;
 constexpr int kSortTile = 1024 * kSortItems;
 constexpr int kMostBits = 10;                 // of a pass
 constexpr int kDigits = 1 << kMostBits;
-constexpr int kSortSelf = 16;                 // tiles up to which workgroups count by themselves
+constexpr int kSortSelf = 16;                 // tiles up to which every workgroup adds the counts up by itself
 
 template <class Id>
 __device__ __forceinline__ uint32_t key_of(Id id, uint32_t rows) {
@@ -74,8 +74,8 @@ struct SortPass {
   const uint32_t* tokens;
   uint32_t* out_keys;
   uint32_t* out_tokens;
-  uint32_t* counts;         // [tiles + 1][kDigits], the last row the totals; NULL: count here
-  int32_t tiles;
+  uint32_t* counts;         // [tiles + 1][kDigits]; the last row the totals, when scanned
+  int32_t tiles, scanned;
   uint32_t rows;
   int32_t shift, bits;
 };
@@ -92,8 +92,13 @@ __global__ void __launch_bounds__(1024) k_sort_count(SortPass p, const Id* ids) 
   const uint32_t mask = (1u << p.bits) - 1;
   count[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kSortTile, i1 = i0 + kSortTile < p.n ? i0 + kSortTile : p.n;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += 1024) atomicAdd(&count[(sort_key(p, ids, i) >> p.shift) & mask], 1u);
+  const int64_t i0 = (int64_t)blockIdx.x * kSortTile + threadIdx.x;
+  uint32_t key[kSortItems];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) key[k] = i0 + k * 1024 < p.n ? sort_key(p, ids, i0 + k * 1024) : 0;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k)
+    if (i0 + k * 1024 < p.n) atomicAdd(&count[(key[k] >> p.shift) & mask], 1u);
   __syncthreads();
   p.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
 }
@@ -117,44 +122,45 @@ __global__ void __launch_bounds__(64) k_sort_scan(uint32_t* counts, int32_t tile
   counts[(int64_t)tiles * kDigits + d] = sum;
 }
 
+// One pass over one tile.
 template <class Id>
-__global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
+__device__ __forceinline__ void sort_pass(const SortPass& p, const Id* ids) {
   __shared__ uint32_t place[16][kDigits];  // counts, then first places, by wave
-  __shared__ uint32_t earlier[kDigits], total[kDigits];
   __shared__ uint32_t wave_total[16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, d = threadIdx.x;
   const uint32_t mask = (1u << p.bits) - 1;
   const int64_t i0 = (int64_t)blockIdx.x * kSortTile;
-  for (int w = 0; w < 16; ++w) place[w][d] = 0;
-  if (p.counts) {
-    earlier[d] = p.counts[(int64_t)blockIdx.x * kDigits + d];
-    total[d] = p.counts[(int64_t)p.tiles * kDigits + d];
-  } else {
-    earlier[d] = 0;
-    total[d] = 0;
-  }
-  __syncthreads();
-  if (!p.counts) {
-    // 16 keys' loads in flight; the first tiles are counted on their own
-    for (int64_t b = threadIdx.x; b < p.n; b += 16 * 1024) {
-      uint32_t g[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) g[k] = b + k * 1024 < p.n ? sort_key(p, ids, b + k * 1024) : 0;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (b + k * 1024 >= p.n) break;
-        const uint32_t d = (g[k] >> p.shift) & mask;
-        atomicAdd(b + k * 1024 < i0 ? &earlier[d] : &total[d], 1u);
-      }
-    }
-  }
   uint32_t key[kSortItems], token[kSortItems], rank[kSortItems];
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const int64_t i = i0 + (wave * kSortItems + k) * 64 + lane;
-    const bool in = i < p.n;
-    key[k] = in ? sort_key(p, ids, i) : 0;
-    token[k] = in ? (p.keys ? p.tokens[i] : (uint32_t)i) : 0;
+    key[k] = i < p.n ? sort_key(p, ids, i) : 0;
+    token[k] = i < p.n ? (p.keys ? p.tokens[i] : (uint32_t)i) : 0;
+  }
+  // of this digit: tokens in earlier tiles, and in all (one tile: in its waves)
+  uint32_t earlier = 0, total = 0;
+  if (p.tiles > 1 && p.scanned) {
+    earlier = p.counts[(int64_t)blockIdx.x * kDigits + d];
+    total = p.counts[(int64_t)p.tiles * kDigits + d];
+  } else if (p.tiles > 1) {
+    for (int32_t b = 0; b < p.tiles; b += kSortSelf) {
+      uint32_t c[kSortSelf];
+#pragma unroll
+      for (int k = 0; k < kSortSelf; ++k) c[k] = b + k < p.tiles ? p.counts[(int64_t)(b + k) * kDigits + d] : 0;
+#pragma unroll
+      for (int k = 0; k < kSortSelf; ++k) {
+        earlier += b + k < (int32_t)blockIdx.x ? c[k] : 0;
+        total += c[k];
+      }
+    }
+  }
+  if (d <= (int)mask)
+#pragma unroll
+    for (int w = 0; w < 16; ++w) place[w][d] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const bool in = i0 + (wave * kSortItems + k) * 64 + lane < p.n;
     const uint32_t g = (key[k] >> p.shift) & mask;
     uint64_t same = __ballot(in);
     for (int b = 0; b < p.bits; ++b) {
@@ -170,9 +176,14 @@ __global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
     rank[k] = old + before;
   }
   __syncthreads();
+  uint32_t mine[16];
+#pragma unroll
+  for (int w = 0; w < 16; ++w) mine[w] = d <= (int)mask ? place[w][d] : 0;
+  if (p.tiles == 1)
+#pragma unroll
+    for (int w = 0; w < 16; ++w) total += mine[w];
   // the digit's first place: tokens of smaller digits, then of earlier tiles
-  if (!p.counts) total[d] += earlier[d];
-  uint32_t first = total[d];
+  uint32_t first = total;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const uint32_t up = __shfl_up(first, o);
@@ -180,13 +191,15 @@ __global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
   }
   if (lane == 63) wave_total[wave] = first;
   __syncthreads();
-  uint32_t at = first - total[d] + earlier[d];
-  for (int w = 0; w < wave; ++w) at += wave_total[w];
-  for (int w = 0; w < 16; ++w) {
-    const uint32_t c = place[w][d];
-    place[w][d] = at;
-    at += c;
-  }
+  uint32_t at = first - total + earlier;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) at += w < wave ? wave_total[w] : 0;
+  if (d <= (int)mask)
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      place[w][d] = at;
+      at += mine[w];
+    }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
@@ -197,13 +210,31 @@ __global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
   }
 }
 
+template <class Id>
+__global__ void __launch_bounds__(1024) k_sort_pass(SortPass p, const Id* ids) {
+  sort_pass(p, ids);
+}
+
+// Every pass over a single tile, in one launch.
+struct SortPasses {
+  SortPass pass[3];
+  int32_t count;
+};
+template <class Id>
+__global__ void __launch_bounds__(1024) k_sort_tile(SortPasses s, const Id* ids) {
+  for (int k = 0; k < s.count; ++k) {
+    if (k) __syncthreads();  // the last pass is written, and its places are free
+    sort_pass(s.pass[k], ids);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Sums of rows.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;   // sorted tokens per wave
 constexpr int kAhead = 4;   // rows in flight
-constexpr int kJoinTiles = 16;  // tiles that a workgroup of the join looks at
-constexpr int kFill = 16;   // rows of dE that a wave of the fill looks at
+constexpr int kJoinTiles = 4;  // tiles that a workgroup of the join looks at
+constexpr int kFill = 8;   // rows of dE that a workgroup of the fill looks at
 
 struct RowSums {
   int64_t n, rows, D;
@@ -216,7 +247,6 @@ struct RowSums {
   float* partial;  // [tiles][2][D]: of the row that came in from the tile before, of the one that goes on
   float scale;
   int32_t accumulate;
-  uint32_t tile_blocks;  // workgroups of tiles; the others fill
 };
 
 // The first place with a key of at least `key`.
@@ -230,28 +260,41 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, 
   return lo;
 }
 
+// Rows that no token names become zeros: a workgroup looks at kFill of them,
+// each lane at one, and writes whole rows.
+template <class G>
+__global__ void __launch_bounds__(256) k_row_fill(RowSums a) {
+  constexpr int V = 16 / sizeof(G);
+  const int lane = threadIdx.x & 63;
+  for (int64_t r0 = (int64_t)blockIdx.x * kFill; r0 < a.rows; r0 += (int64_t)gridDim.x * kFill) {
+    const int64_t r = r0 + lane;
+    bool named = lane >= kFill || r >= a.rows;
+    if (!named) {
+      const int64_t at = lower_bound(a.keys, a.n, (uint32_t)r);
+      named = at < a.n && a.keys[at] == (uint32_t)r;
+    }
+    uint64_t todo = ~__ballot(named);
+    while (todo) {
+      const int i = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      G* to = static_cast<G*>(a.dtable) + (r0 + i) * a.ld;
+      for (int64_t j = (int64_t)threadIdx.x * V; j < a.D; j += 256 * V) {
+        if (a.D - j >= V) {
+          __builtin_nontemporal_store(u32x4_any{0, 0, 0, 0}, reinterpret_cast<u32x4_any*>(to + j));
+        } else {
+          for (int64_t k = j; k < a.D; ++k) to[k] = (G)0.f;
+        }
+      }
+    }
+  }
+}
+
 template <class T, class G>
 __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
   constexpr int V = 16 / sizeof(T) > 4 ? 8 : 4;  // columns per lane
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
   G* dtable = static_cast<G*>(a.dtable) + j;
-  if (blockIdx.x >= a.tile_blocks) {
-    // rows that no token names: zeros
-    const int64_t r0 = ((int64_t)(blockIdx.x - a.tile_blocks) * 4 + wave) * kFill;
-    if (r0 >= a.rows || left <= 0) return;
-    const int64_t r1 = r0 + kFill < a.rows ? r0 + kFill : a.rows;
-    int64_t at = lower_bound(a.keys, a.n, (uint32_t)r0);
-    const float zero[V] = {};
-    for (int64_t r = r0; r < r1; ++r) {
-      if (at < a.n && a.keys[at] == (uint32_t)r) {
-        at = r + 1 < r1 ? at + lower_bound(a.keys + at, a.n - at, (uint32_t)r + 1) : at;
-        continue;
-      }
-      store_columns<G, V>(dtable + r * a.ld, left, zero);
-    }
-    return;
-  }
   const int64_t tile = (int64_t)blockIdx.x * 4 + wave, p0 = tile * kTile;
   // lanes past the last column stay: the tile's keys are held across the wave
   if (p0 >= a.n) return;
@@ -340,7 +383,9 @@ __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
     if (alone && wave != (at & 3)) continue;
     const int64_t per = alone ? parts : (parts + 3) / 4, k0 = alone ? 0 : wave * per;
     const int64_t k1 = k0 + per < parts ? k0 + per : parts;
-    float sum[V] = {};
+    G* to = static_cast<G*>(a.dtable) + (int64_t)key * a.ld + j;
+    float sum[V] = {}, y[V] = {};
+    if (a.accumulate && (alone || wave == 0)) load_columns<G, V>(to, left, y);
     for (int64_t k = k0; k < k1; k += kJoin) {
       float v[kJoin][V];
 #pragma unroll
@@ -360,9 +405,6 @@ __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
 #pragma unroll
       for (int t = 0; t < V; ++t) sum[t] = (part[0][lane][t] + part[1][lane][t]) + (part[2][lane][t] + part[3][lane][t]);
     }
-    G* to = static_cast<G*>(a.dtable) + (int64_t)key * a.ld + j;
-    float y[V] = {};
-    if (a.accumulate) load_columns<G, V>(to, left, y);
 #pragma unroll
     for (int t = 0; t < V; ++t) y[t] = a.scale * sum[t] + y[t];
     store_columns<G, V>(to, left, y);
@@ -386,7 +428,7 @@ struct EmbeddingSpace {
       at += up16(4 * T);
     }
     counts_at = at;
-    if (sort_tiles > kSortSelf) at += (sort_tiles + 1) * kDigits * 4;
+    if (sort_tiles > 1) at += (sort_tiles + 1) * kDigits * 4;
     partial_at = at;
     if (tiles > 1) at += up16(tiles * 2 * D * 4);
     bytes = at;
@@ -399,8 +441,10 @@ int sort_tokens(int64_t T, int64_t rows, const void* ids, char* ws, const Embedd
   while (rows >> bits) ++bits;  // keys are 0 .. rows
   const int32_t passes = (bits + kMostBits - 1) / kMostBits, each = (bits + passes - 1) / passes;
   const Id* id = static_cast<const Id*>(ids);
+  SortPasses s{};
+  s.count = passes;
   for (int32_t k = 0; k < passes; ++k) {
-    SortPass p{};
+    SortPass& p = s.pass[k];
     p.n = T;
     if (k) {
       p.keys = reinterpret_cast<uint32_t*>(ws + e.keys_at[(k - 1) & 1]);
@@ -409,16 +453,17 @@ int sort_tokens(int64_t T, int64_t rows, const void* ids, char* ws, const Embedd
     p.out_keys = reinterpret_cast<uint32_t*>(ws + e.keys_at[k & 1]);
     p.out_tokens = reinterpret_cast<uint32_t*>(ws + e.tokens_at[k & 1]);
     p.tiles = (int32_t)e.sort_tiles;
+    p.scanned = p.tiles > kSortSelf;
     p.rows = (uint32_t)rows;
     p.shift = k * each;
     p.bits = std::min(each, bits - p.shift);
-    if (e.sort_tiles > kSortSelf) {
-      p.counts = reinterpret_cast<uint32_t*>(ws + e.counts_at);
-      k_sort_count<Id><<<dim3((uint32_t)e.sort_tiles), 1024, 0, stream>>>(p, id);
-      k_sort_scan<<<kDigits / 64, 64, 0, stream>>>(p.counts, p.tiles);
-    }
-    k_sort_pass<Id><<<dim3((uint32_t)e.sort_tiles), 1024, 0, stream>>>(p, id);
+    p.counts = reinterpret_cast<uint32_t*>(ws + e.counts_at);
+    if (p.tiles == 1) continue;
+    k_sort_count<Id><<<dim3((uint32_t)p.tiles), 1024, 0, stream>>>(p, id);
+    if (p.scanned) k_sort_scan<<<kDigits / 64, 64, 0, stream>>>(p.counts, p.tiles);
+    k_sort_pass<Id><<<dim3((uint32_t)p.tiles), 1024, 0, stream>>>(p, id);
   }
+  if (e.sort_tiles == 1) k_sort_tile<Id><<<1, 1024, 0, stream>>>(s, id);
   return (passes - 1) & 1;
 }
 
@@ -427,9 +472,11 @@ void row_sums(const RowSums& s, int64_t tiles, hipStream_t stream) {
   RowSums a = s;
   constexpr int64_t per = 64 * (sizeof(T) == 2 ? 8 : 4);
   const uint32_t across = (uint32_t)((a.D + per - 1) / per);
-  a.tile_blocks = (uint32_t)((tiles + 3) / 4);
-  const int64_t fill = a.accumulate ? 0 : (a.rows + 4 * kFill - 1) / (4 * kFill);
-  if (a.tile_blocks + fill) k_row_sums<T, G><<<dim3((uint32_t)(a.tile_blocks + fill), across), 256, 0, stream>>>(a);
+  if (!a.accumulate) {
+    const int64_t blocks = std::min<int64_t>((a.rows + kFill - 1) / kFill, (int64_t)1 << 20);
+    k_row_fill<G><<<dim3((uint32_t)blocks), 256, 0, stream>>>(a);
+  }
+  if (tiles) k_row_sums<T, G><<<dim3((uint32_t)((tiles + 3) / 4), across), 256, 0, stream>>>(a);
   if (tiles > 1)
     k_row_join<G><<<dim3((uint32_t)((tiles + kJoinTiles - 1) / kJoinTiles), (uint32_t)((a.D + 255) / 256)), 256, 0,
                     stream>>>(a);
