@@ -18,22 +18,7 @@
 namespace dc {
 namespace {
 
-#ifndef DC_UNIT
-#define DC_UNIT 16384
-#endif
-#ifndef DC_PARTS
-#define DC_PARTS 2048
-#endif
-#ifndef DC_NTL
-#define DC_NTL 0
-#endif
-#ifndef DC_NTC
-#define DC_NTC 0
-#endif
-#ifndef DC_NTS
-#define DC_NTS 0
-#endif
-constexpr int64_t kUnit = DC_UNIT;      // bytes
+constexpr int64_t kUnit = 16384;      // bytes
 constexpr int64_t kLaunchUnits = (int64_t)1 << 30;
 
 // Flat gradients of one launch: numel2 = 2 numel + (fp32).
@@ -120,13 +105,21 @@ __device__ __forceinline__ u32x4 load_part(const char* p, int have, bool wide) {
 }
 
 // Vectors of a unit: elements past its end read as zeros.
-template <bool NT>
-__device__ __forceinline__ void load_unit(const Unit& t, u32x4 (&v)[kVectors]) {
+__device__ __forceinline__ void load_unit(const Unit& t, bool streamed, u32x4 (&v)[kVectors]) {
   const int V = t.wide ? 4 : 8;
+  if (t.n == kVectors * 256 * V) {
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j) {
+      const u32x4_any* p = reinterpret_cast<const u32x4_any*>(t.grad + 16 * (j * 256 + (int)threadIdx.x));
+      if (streamed) v[j] = __builtin_nontemporal_load(p);
+      else v[j] = *p;
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < kVectors; ++j) {
     const int i = j * 256 + (int)threadIdx.x, have = t.n - i * V;
-    if (have >= V) v[j] = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(t.grad + 16 * i)) : *reinterpret_cast<const u32x4_any*>(t.grad + 16 * i);
+    if (have >= V) v[j] = *reinterpret_cast<const u32x4_any*>(t.grad + 16 * i);
     else v[j] = have > 0 ? load_part(t.grad + 16 * i, have, t.wide) : u32x4{0, 0, 0, 0};
   }
 }
@@ -144,9 +137,16 @@ __device__ __forceinline__ int find_entry(const List& l, int32_t u) {
   return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
-// partial[workgroup] (+)= the squares of its units.
+// The squares are summed from the list's beginning to its end and the
+// gradients scaled from its end to its beginning: what was read last is then
+// still in the 256 MB cache.  Units further than kCached from the end are
+// streamed both times, past what is kept.
+constexpr int64_t kCached = ((int64_t)192 << 20) / kUnit;
+
+// partial[workgroup] (+)= the squares of its units.  `after`: units that later
+// launches read.
 template <class List>
-__global__ void __launch_bounds__(256) k_squares(List l, double* partial, int32_t add) {
+__global__ void __launch_bounds__(256) k_squares(List l, int64_t after, double* partial, int32_t add) {
   double s = 0;
   const int32_t units = l.begin[l.count];
   int e = (int32_t)blockIdx.x < units ? find_entry(l, blockIdx.x) : 0;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(256) k_squares(List l, double* partial, int32_
     while (l.begin[e + 1] <= u) ++e;
     const Unit t = unit_at(l, e, u);
     u32x4 v[kVectors];
-    load_unit<DC_NTL>(t, v);
+    load_unit(t, after + units - u > kCached, v);
 #pragma unroll
     for (int j = 0; j < kVectors; ++j)
 #pragma unroll
@@ -197,12 +197,13 @@ __device__ __forceinline__ float factor(double squares, float max_norm, float ep
 }
 
 // Every workgroup folds the partial sums by itself (16 KB from the caches) or
-// takes the given sum, then scales its units, the last ones first: what
-// k_squares read last is still in the cache.  A factor of 1 in place leaves
-// nothing to do.
+// takes the given sum, then scales its units.  The list has the gradients in
+// reverse order, and each is gone through from its end.  `before`: units of
+// earlier launches.  A factor of 1 in place leaves nothing to do.
 template <class List>
-__global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int32_t parts, const double* squares,
-                                              float max_norm, float eps, float* norm, float* coef, int32_t in_place) {
+__global__ void __launch_bounds__(256) k_clip(List l, int64_t before, const double* partial, int32_t parts,
+                                              const double* squares, float max_norm, float eps, float* norm,
+                                              float* coef, int32_t in_place) {
   const double s = squares ? *squares : fold_partials(partial, parts);
   const float c = factor(s, max_norm, eps);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -211,12 +212,12 @@ __global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int
   }
   if (in_place && c == 1.f) return;
   const int32_t units = l.begin[l.count];
-  int e = (int32_t)blockIdx.x < units ? find_entry(l, units - 1 - (int32_t)blockIdx.x) : 0;
-  for (int32_t u = units - 1 - (int32_t)blockIdx.x; u >= 0; u -= gridDim.x) {
-    while (l.begin[e] > u) --e;
-    const Unit t = unit_at(l, e, u);
+  int e = (int32_t)blockIdx.x < units ? find_entry(l, blockIdx.x) : 0;
+  for (int32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    while (l.begin[e + 1] <= u) ++e;
+    const Unit t = unit_at(l, e, l.begin[e] + l.begin[e + 1] - 1 - u);
     u32x4 v[kVectors];
-    load_unit<DC_NTC>(t, v);
+    load_unit(t, before + u > kCached, v);
     const int V = t.wide ? 4 : 8;
 #pragma unroll
     for (int j = 0; j < kVectors; ++j) {
@@ -230,8 +231,7 @@ __global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int
       }
       char* to = t.out + 16 * i;
       if (have >= V) {
-        if (DC_NTS) __builtin_nontemporal_store((u32x4_any)y, reinterpret_cast<u32x4_any*>(to));
-        else *reinterpret_cast<u32x4_any*>(to) = y;
+        __builtin_nontemporal_store((u32x4_any)y, reinterpret_cast<u32x4_any*>(to));
       } else if (t.wide) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -245,16 +245,21 @@ __global__ void __launch_bounds__(256) k_clip(List l, const double* partial, int
   }
 }
 
-// Calls f(list, units) for every launch's part of the gradients.  `rows`: of a
+// Calls f(list, units, units of the launches before) for every launch's part of
+// the gradients, in reverse order where they are written.  `rows`: of a
 // gradient, how many take part.
 template <class Rows, class F>
 void for_lists(const dc_gradient* grads, int32_t num, Rows rows, bool writes, F&& f) {
+  int64_t before = 0;
   FlatList flat;
   RowsList strided;
   flat.count = strided.count = 0;
   flat.begin[0] = strided.begin[0] = 0;
   auto close = [&](auto& l) {
-    if (l.count) f(l, l.begin[l.count]);
+    if (l.count) {
+      f(l, l.begin[l.count], before);
+      before += l.begin[l.count];
+    }
     l.count = 0;
   };
   auto units = [&](auto& l, int64_t n) {  // of a new entry; true: it fits
@@ -263,7 +268,7 @@ void for_lists(const dc_gradient* grads, int32_t num, Rows rows, bool writes, F&
     return l.count++;
   };
   for (int32_t k = 0; k < num; ++k) {
-    const dc_gradient& g = grads[k];
+    const dc_gradient& g = grads[writes ? num - 1 - k : k];
     const int64_t r = rows(g), es = g.dtype == DC_F32 ? 4 : 2, per = kUnit / es;
     if (r == 0 || g.cols == 0) continue;
     if (r == 1 || (g.ld_grad == g.cols && (!writes || g.ld_out == g.cols))) {
@@ -292,26 +297,33 @@ void for_lists(const dc_gradient* grads, int32_t num, Rows rows, bool writes, F&
 
 // Workgroups of a launch: eight of 256 threads a compute unit, 2048 in all,
 // hold every wave that fits, and their sums are 16 KB.
-constexpr int32_t kParts = DC_PARTS;
+constexpr int32_t kParts = 2048;
 
-int32_t counted(const dc_gradient* grads, int32_t num) {
-  int32_t most = 1;
+struct Counted {
+  int32_t parts;
+  int64_t units;
+};
+Counted counted(const dc_gradient* grads, int32_t num) {
+  Counted c{1, 0};
   for_lists(grads, num, [](const dc_gradient& g) { return g.counted; }, false,
-            [&](const auto&, int32_t units) { most = std::max(most, std::min(units, kParts)); });
-  return most;
+            [&](const auto&, int32_t units, int64_t) {
+              c.parts = std::max(c.parts, std::min(units, kParts));
+              c.units += units;
+            });
+  return c;
 }
 
-void sum_squares(const dc_gradient* grads, int32_t num, int32_t parts, double* partial, hipStream_t stream) {
-  int32_t add = 0;
-  for_lists(grads, num, [](const dc_gradient& g) { return g.counted; }, false, [&](const auto& l, int32_t) {
-    k_squares<<<dim3((uint32_t)parts), 256, 0, stream>>>(l, partial, add);
-    add = 1;
-  });
-  if (!add) {  // nothing is counted
+void sum_squares(const dc_gradient* grads, int32_t num, const Counted& c, double* partial, hipStream_t stream) {
+  const dim3 grid((uint32_t)c.parts);
+  for_lists(grads, num, [](const dc_gradient& g) { return g.counted; }, false,
+            [&](const auto& l, int32_t units, int64_t before) {
+              k_squares<<<grid, 256, 0, stream>>>(l, c.units - before - units, partial, before > 0);
+            });
+  if (c.units == 0) {  // nothing is counted
     FlatList none;
     none.count = 0;
     none.begin[0] = 0;
-    k_squares<<<dim3((uint32_t)parts), 256, 0, stream>>>(none, partial, 0);
+    k_squares<<<grid, 256, 0, stream>>>(none, (int64_t)0, partial, 0);
   }
 }
 
@@ -322,9 +334,9 @@ int64_t clip_workspace() { return kParts * 8; }
 hipError_t launch_grad_norm(const dc_gradient* grads, int32_t num, int32_t accumulate, double* squares, float* norm,
                             void* workspace, hipStream_t stream) {
   double* partial = static_cast<double*>(workspace);
-  const int32_t parts = counted(grads, num);
-  sum_squares(grads, num, parts, partial, stream);
-  k_norm<<<1, 256, 0, stream>>>(partial, parts, accumulate, squares, norm);
+  const Counted c = counted(grads, num);
+  sum_squares(grads, num, c, partial, stream);
+  k_norm<<<1, 256, 0, stream>>>(partial, c.parts, accumulate, squares, norm);
   return hipGetLastError();
 }
 
@@ -333,13 +345,14 @@ hipError_t launch_grad_clip(const dc_gradient* grads, int32_t num, const double*
   double* partial = static_cast<double*>(workspace);
   int32_t parts = 0, in_place = 1, launches = 0;
   if (!squares) {
-    parts = counted(grads, num);
-    sum_squares(grads, num, parts, partial, stream);
+    const Counted c = counted(grads, num);
+    sum_squares(grads, num, c, partial, stream);
+    parts = c.parts;
   }
   for (int32_t k = 0; k < num; ++k) in_place &= grads[k].out == grads[k].grad;
-  auto clip = [&](const auto& l, int32_t units) {
+  auto clip = [&](const auto& l, int32_t units, int64_t before) {
     k_clip<<<dim3((uint32_t)std::max(1, std::min(units, kParts))), 256, 0, stream>>>(
-        l, partial, parts, squares, max_norm, eps, norm, coef, in_place);
+        l, before, partial, parts, squares, max_norm, eps, norm, coef, in_place);
     ++launches;
   };
   for_lists(grads, num, [](const dc_gradient& g) { return g.rows; }, true, clip);
@@ -347,7 +360,7 @@ hipError_t launch_grad_clip(const dc_gradient* grads, int32_t num, const double*
     FlatList none;
     none.count = 0;
     none.begin[0] = 0;
-    clip(none, 0);
+    clip(none, 0, 0);
   }
   return hipGetLastError();
 }

@@ -232,7 +232,6 @@ __global__ void __launch_bounds__(1024) k_sort_tile(SortPasses s, const Id* ids)
 // Sums of rows.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 16;   // sorted tokens per wave
-constexpr int kAhead = 4;   // rows in flight
 constexpr int kJoinTiles = 4;  // tiles that a workgroup of the join looks at
 constexpr int kFill = 8;   // rows of dE that a workgroup of the fill looks at
 
@@ -291,7 +290,8 @@ __global__ void __launch_bounds__(256) k_row_fill(RowSums a) {
 
 template <class T, class G>
 __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
-  constexpr int V = 16 / sizeof(T) > 4 ? 8 : 4;  // columns per lane
+  constexpr int V = 16 / sizeof(T);  // columns per lane
+  constexpr int kAhead = 32 / V;     // rows in flight
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
   G* dtable = static_cast<G*>(a.dtable) + j;
