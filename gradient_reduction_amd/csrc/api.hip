@@ -1606,7 +1606,7 @@ dc_status dc_embedding_backward_workspace(int32_t dtype, int64_t T, int64_t rows
   dc_status st;
   if ((st = check_embedding(dtype, T, rows, D, 1.f))) return st;
   if (bytes == nullptr) return fail(DC_ERR_NULL, "bytes is NULL");
-  *bytes = dc::embedding_workspace(T, D);
+  *bytes = dc::embedding_workspace(dtype, T, D);
   return ok();
 }
 
@@ -1623,7 +1623,7 @@ dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int6
       mt{"dtable", dtable, rows, D, ld, elem_bytes(grad_dtype)};
   if (T && ((st = check_rows(mi)) || (st = check_rows(my)))) return st;
   if ((st = check_rows(mt)) || (st = check_apart(mt, {&mi, &my}))) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, dc::embedding_workspace(T, D)))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, dc::embedding_workspace(dtype, T, D)))) return st;
   return hip_status(dc::launch_embedding_backward(dtype, grad_dtype, id_bytes, T, rows, D, dy, ld_dy, ids, scale,
                                                   dtable, ld, accumulate, workspace,
                                                   static_cast<hipStream_t>(stream)),

@@ -3,7 +3,7 @@
 //   dE[v] (+)= scale sum over {t: ids[t] = v} of dy[t]
 // The gradient's tokens are sorted by id, stably, so that every row's sum runs
 // over ascending t: no atomics, the same result every time.  The sorted
-// tokens are cut into tiles of kTile; a wave adds up one tile's rows over one
+// tokens are cut into tiles of 8 to 32; a wave adds up one tile's rows over one
 // run of columns and writes every row of dE that lies whole in its tile.  A
 // row whose tokens reach over tiles leaves one partial sum in each, which a
 // second launch adds up in order; a frequent token is so spread over the chip.
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256) k_lookup(int64_t T_, int64_t rows, int64_
 // those of its digit in earlier workgroups, earlier waves, and before it in
 // its wave.  Ids outside the table sort behind it, as `rows`.
 // ---------------------------------------------------------------------------
-constexpr int kSortItems = 4;
+constexpr int kSortItems = 2;
 constexpr int kSortTile = 1024 * kSortItems;
 constexpr int kMostBits = 10;                 // of a pass
 constexpr int kDigits = 1 << kMostBits;
@@ -231,7 +231,6 @@ __global__ void __launch_bounds__(1024) k_sort_tile(SortPasses s, const Id* ids)
 // ---------------------------------------------------------------------------
 // Sums of rows.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 16;   // sorted tokens per wave
 constexpr int kJoinTiles = 4;  // tiles that a workgroup of the join looks at
 constexpr int kFill = 8;   // rows of dE that a workgroup of the fill looks at
 
@@ -243,6 +242,7 @@ struct RowSums {
   int64_t ld_dy;
   void* dtable;
   int64_t ld;
+  int32_t tile;    // sorted tokens per wave
   float* partial;  // [tiles][2][D]: of the row that came in from the tile before, of the one that goes on
   float scale;
   int32_t accumulate;
@@ -295,10 +295,10 @@ __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
   G* dtable = static_cast<G*>(a.dtable) + j;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + wave, p0 = tile * kTile;
+  const int64_t tile = (int64_t)blockIdx.x * 4 + wave, p0 = tile * a.tile;
   // lanes past the last column stay: the tile's keys are held across the wave
   if (p0 >= a.n) return;
-  const int have = a.n - p0 < kTile ? (int)(a.n - p0) : kTile;
+  const int have = a.n - p0 < a.tile ? (int)(a.n - p0) : a.tile;
   // lane i holds place p0 + i - 1: the tile, with the places before and after it
   const int64_t mine = p0 + lane - 1;
   const bool exists = lane <= have + 1 && mine >= 0 && mine < a.n;
@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
   constexpr int V = 4;
   __shared__ float part[4][64][V];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t tiles = (a.n + kTile - 1) / kTile, base = (int64_t)blockIdx.x * kJoinTiles;
+  const int64_t tiles = (a.n + a.tile - 1) / a.tile, base = (int64_t)blockIdx.x * kJoinTiles;
   // lane i looks at the tile base + i: whether a row that came in ends there
-  const int64_t mine = base + lane, p0 = mine * kTile, p1 = p0 + kTile < a.n ? p0 + kTile : a.n;
+  const int64_t mine = base + lane, p0 = mine * a.tile, p1 = p0 + a.tile < a.n ? p0 + a.tile : a.n;
   uint32_t first = 0;
   bool ends = false;
   if (lane < kJoinTiles && mine > 0 && mine < tiles) {
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
     int64_t from = tile;
     for (;;) {
       const int64_t k = from - 1 - lane;
-      const uint64_t came = __ballot(k > 0 && a.keys[k > 0 ? k * kTile - 1 : 0] == key && a.keys[k > 0 ? k * kTile : 0] == key);
+      const uint64_t came = __ballot(k > 0 && a.keys[k > 0 ? k * a.tile - 1 : 0] == key && a.keys[k > 0 ? k * a.tile : 0] == key);
       const int n = came == ~0ull ? 64 : __ffsll((unsigned long long)~came) - 1;
       from -= n;
       if (n < 64) break;
@@ -416,10 +416,16 @@ int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 // Where the workspace holds what: two buffers of keys and tokens, the counts,
 // the partial sums.
 struct EmbeddingSpace {
-  int64_t tokens, sort_tiles, tiles, keys_at[2], tokens_at[2], counts_at, partial_at, bytes;
-  EmbeddingSpace(int64_t T, int64_t D) {
+  int64_t sort_tiles, tile, tiles, keys_at[2], tokens_at[2], counts_at, partial_at, bytes;
+  EmbeddingSpace(int32_t dtype, int64_t T, int64_t D) {
     sort_tiles = (T + kSortTile - 1) / kSortTile;
-    tiles = (T + kTile - 1) / kTile;
+    // The longest tile that leaves eight waves a compute unit: long ones leave
+    // fewer partial sums (32768 tokens x 1024: 32 64 us, 16 68), short ones finish
+    // sooner (1511 x 515 fp32: 8 23 us, 16 27, 32 36).
+    const int64_t per = 64 * (16 / (dtype == DC_F32 ? 4 : 2)), across = (D + per - 1) / per;
+    for (tile = 32; tile > 8 && (T + tile - 1) / tile * across < 2048; tile /= 2) {
+    }
+    tiles = (T + tile - 1) / tile;
     int64_t at = 0;
     for (int k = 0; k < 2; ++k) {
       keys_at[k] = at;
@@ -501,14 +507,14 @@ hipError_t launch_embedding(int32_t dtype, int32_t id_bytes, int64_t T, int64_t 
   return hipGetLastError();
 }
 
-int64_t embedding_workspace(int64_t T, int64_t D) { return EmbeddingSpace(T, D).bytes; }
+int64_t embedding_workspace(int32_t dtype, int64_t T, int64_t D) { return EmbeddingSpace(dtype, T, D).bytes; }
 
 hipError_t launch_embedding_backward(int32_t dtype, int32_t grad_dtype, int32_t id_bytes, int64_t T, int64_t rows,
                                      int64_t D, const void* dy, int64_t ld_dy, const void* ids, float scale,
                                      void* dtable, int64_t ld, int32_t accumulate, void* workspace,
                                      hipStream_t stream) {
   if (T == 0 && accumulate) return hipSuccess;
-  const EmbeddingSpace e(T, D);
+  const EmbeddingSpace e(dtype, T, D);
   char* ws = static_cast<char*>(workspace);
   int at = 0;
   if (T) at = id_bytes == 8 ? sort_tokens<int64_t>(T, rows, ids, ws, e, stream)
@@ -524,6 +530,7 @@ hipError_t launch_embedding_backward(int32_t dtype, int32_t grad_dtype, int32_t 
   a.dtable = dtable;
   a.ld = ld;
   a.partial = reinterpret_cast<float*>(ws + e.partial_at);
+  a.tile = (int32_t)e.tile;
   a.scale = scale;
   a.accumulate = accumulate;
   if (dtype == DC_F32) row_sums<float, float>(a, e.tiles, stream);

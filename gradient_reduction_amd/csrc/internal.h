@@ -254,7 +254,7 @@ hipError_t launch_grad_clip(const dc_gradient* grads, int32_t num, const double*
 hipError_t launch_embedding(int32_t dtype, int32_t id_bytes, int64_t T, int64_t rows, int64_t D, const void* ids,
                             const void* table, int64_t ld_table, float scale, void* out, int64_t ld_out,
                             hipStream_t stream);
-int64_t embedding_workspace(int64_t T, int64_t D);
+int64_t embedding_workspace(int32_t dtype, int64_t T, int64_t D);
 hipError_t launch_embedding_backward(int32_t dtype, int32_t grad_dtype, int32_t id_bytes, int64_t T, int64_t rows,
                                      int64_t D, const void* dy, int64_t ld_dy, const void* ids, float scale,
                                      void* dtable, int64_t ld, int32_t accumulate, void* workspace,
