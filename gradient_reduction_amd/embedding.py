@@ -12,7 +12,7 @@ is called by hand.
 import torch
 
 from . import dc
-from .linear import _apart, _rows, _span, dtype_of, on, workspace
+from .linear import MOST, _apart, _rows, _span, dtype_of, on, workspace
 
 _IDS = {torch.int32: 4, torch.int64: 8}
 
@@ -26,7 +26,7 @@ def _id_bytes(ids, device) -> int:
 
 
 def _check_scale(scale):
-    if not abs(scale) <= torch.finfo(torch.float32).max:
+    if not abs(scale) <= MOST:
         raise ValueError(f"scale {scale} is not finite in float32")
 
 
@@ -34,6 +34,8 @@ def _tokens(name, t, ids, D):
     """t [*ids.shape, D] as rows of one stride."""
     if tuple(t.shape) != tuple(ids.shape) + (D,):
         raise ValueError(f"{name} of shape {tuple(t.shape)}, expected {tuple(ids.shape) + (D,)}")
+    if t.dim() == 2:
+        return t
     try:
         return t.view(ids.numel(), D)
     except RuntimeError:

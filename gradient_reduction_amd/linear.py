@@ -17,6 +17,7 @@ import torch
 from . import dc
 
 ACTS = {"none": dc.DC_ACT_NONE, "relu": dc.DC_ACT_RELU, "gelu": dc.DC_ACT_GELU, "silu": dc.DC_ACT_SILU}
+MOST = torch.finfo(torch.float32).max    # a scalar that the library takes as float
 _DTYPES = {torch.bfloat16: dc.DC_BF16, torch.float32: dc.DC_F32}
 
 

@@ -14,18 +14,18 @@ import math
 import torch
 
 from . import dc
-from .linear import _apart, _rows, _span, _vector, dtype_of, on, workspace
+from .linear import MOST, _apart, _rows, _span, _vector, dtype_of, on, workspace
 
 
-def _tokens(name, t, like, dtype, device):
-    """(t [..., D] as rows, their stride), of `like`'s shape."""
+def _tokens(name, t, like, T, D, dtype, device):
+    """(t [..., D] as T rows, their stride), of `like`'s shape."""
     if t.shape != like:
         raise ValueError(f"{name} of shape {tuple(t.shape)}, expected {tuple(like)}")
-    T, D = like[:-1].numel(), like[-1]
-    try:
-        t = t.view(T, D)
-    except RuntimeError:
-        raise ValueError(f"{name} of strides {t.stride()} is not rows of one stride") from None
+    if t.dim() != 2:
+        try:
+            t = t.view(T, D)
+        except RuntimeError:
+            raise ValueError(f"{name} of strides {t.stride()} is not rows of one stride") from None
     return _rows(name, t, T, D, dtype, device)
 
 
@@ -41,9 +41,8 @@ def _gate(name, gate, T, D, dtypes, device):
 
 
 def _float32(name, v):
-    if not abs(v) <= torch.finfo(torch.float32).max:
+    if not abs(v) <= MOST:
         raise ValueError(f"{name} {v} is not finite in float32")
-    return v
 
 
 class _Operands:
@@ -71,7 +70,7 @@ class _Operands:
             self.gate, self.gate_rows, self.ld_gate = _gate("gate", gate, self.T, self.D, (self.dt,), self.dev)
 
     def rows(self, name, t):
-        return _tokens(name, t, self.like, self.dt, self.dev)
+        return _tokens(name, t, self.like, self.T, self.D, self.dt, self.dev)
 
     def empty(self):
         return torch.empty(self.like, dtype=self.dt, device=self.dev)
