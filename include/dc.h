@@ -28,7 +28,11 @@
  *                     last micro-batch) ([MT] What)
  *   a layer's         dc_linear forward, dc_bias_act_backward and
  *   gradients         dc_linear_backward, whose weight gradient may go
- *                     straight into an accumulator row
+ *                     straight into an accumulator row; dc_norm around a
+ *                     block and dc_embedding before it, likewise with
+ *                     dc_norm_backward and dc_embedding_backward
+ *   clipping          dc_grad_clip on the reduced gradients (dc_grad_norm:
+ *                     their global norm alone)
  *   the owner's step  dc_muon_update on the parameters whose reduced
  *                     gradient the owner holds whole (dc_orthogonalize: its
  *                     orthogonalisation alone)
@@ -978,8 +982,8 @@ dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, int32_t hold,
  *   n = sqrt(sum over the counted rows of every gradient of g^2)
  * and
  *   c = n + eps <= max_norm ? 1 : max_norm / (n + eps),   out = c g
- * over all rows.  Squares and sums are fp64, in an order fixed by the sizes; c is rounded
- * once to fp32 and c g once to the dtype.  An infinity among the counted
+ * over all rows.  Squares and sums are fp64, in an order fixed by the list's sizes and
+ * strides; c is rounded once to fp32, c g to fp32 and then to the dtype.  An infinity among the counted
  * gradients gives c = 0 (and NaN where it stands), a NaN gives NaN throughout:
  * read *norm to pass such a step over.  Rules of the section above hold, with
  * 2^36 elements per gradient and 2^44 per row stride. */
@@ -1065,7 +1069,7 @@ dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int6
  *                    ld) or h
  *   y, ld_y          device [T, ld_y] out; with gain only; may be x or h,
  *                    where s is not
- * T = 0 writes nothing. */
+ * T = 0 writes nothing (and asks for no pointer). */
 dc_status dc_norm(int32_t dtype, int64_t T, int64_t D, const void* x, int64_t ld_x, const void* h,
                   int64_t ld_h, const void* post_gain, const void* gate, int64_t gate_rows,
                   int64_t ld_gate, const void* gain, float scale, float offset, float eps, void* s,
