@@ -6,6 +6,11 @@
 // Gradients are cut into units of 16 KB.  A launch's list travels as kernel
 // arguments, flat gradients (one run of elements) and strided ones apart; its
 // workgroups take units in turn and keep their place in the list.
+//
+// Bound by the bytes: 2 GiB of fp32 or bf16 are read at 5.9 TB/s; 100M bf16
+// take 34 us and, scaled from the cache, 66 more; 395M fp32 847 in all, 5.6
+// TB/s.  Units of 8 and 32 KB took 4% and 6% more on those.  113 vectors: 5.7
+// and 5.0 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -7,6 +7,10 @@
 // run of columns and writes every row of dE that lies whole in its tile.  A
 // row whose tokens reach over tiles leaves one partial sum in each, which a
 // second launch adds up in order; a frequent token is so spread over the chip.
+//
+// 32768 tokens of a natural text's frequencies in a table of 151936 x 1024,
+// bf16 added to fp32: sort 22 us (two passes, each of a count and a pass),
+// rows 30 (167 MB, 5.6 TB/s), join 7.  Lookup of the same: 20, 4.6 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -61,6 +65,8 @@ constexpr int kSortItems = 2;
 constexpr int kSortTile = 1024 * kSortItems;
 constexpr int kMostBits = 10;                 // of a pass
 constexpr int kDigits = 1 << kMostBits;
+// (Workgroups of 1024, 2048 and 4096 tokens: 32768 take 69, 68 and 73 us with
+// all that follows.)
 constexpr int kSortSelf = 16;                 // tiles up to which every workgroup adds the counts up by itself
 
 template <class Id>
@@ -260,7 +266,8 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, 
 }
 
 // Rows that no token names become zeros: a workgroup looks at kFill of them,
-// each lane at one, and writes whole rows.
+// each lane at one, and writes whole rows (92 us for 30000 x 4096 fp32, 5.4
+// TB/s; columns of 16 rows by waves of the next kernel took 139 with its sums).
 template <class G>
 __global__ void __launch_bounds__(256) k_row_fill(RowSums a) {
   constexpr int V = 16 / sizeof(G);
