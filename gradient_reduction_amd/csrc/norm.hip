@@ -12,10 +12,13 @@
 // is read once.  Sums over a row are fp64, so that squares of any fp32 value
 // neither overflow nor vanish.
 //
-// 8192 rows of 4096 bf16: forward 47 us with the call (268 MB, 5.6 TB/s, bound
-// by HBM); backward 75 to 80 and 5 for the join (403 MB, 5.0 TB/s), bound by a row's two
-// reductions, one behind the other, with two rows in flight a compute unit.
-// Eight values a thread instead of 16, twice the waves to a row: 111 to 119.
+// 8192 rows of 4096 bf16: forward 39 us (268 MB, 6.9 TB/s, bound by HBM);
+// backward 75 to 79 and 5 for the join (403 MB, 5.1 to 5.4 TB/s), where the
+// arithmetic of some 750 instructions a wave and row (sums in fp64 among them)
+// takes as long as the bytes and two waves a SIMD do not hide all of it.
+// Tried: 8 values a thread instead of 16, twice the waves to a row, 111 to 119;
+// one sum over the lanes in place of two (three more fp64 products a value in
+// place of a second exchange), 95.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -299,10 +302,20 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
     load_row<T, N, DIRECT>(r.h, a.h, row, a.ld_h, D, in, lane, G);
     load_row<T, N, DIRECT>(r.ds, a.ds, row, a.ld_ds, D, in, lane, G);
   };
-  Pack<T> gain[N], post[N], gate[N];
-  load_row<T, N, DIRECT>(gain, a.gain, 0, 0, D, true, lane, G);
-  load_row<T, N, DIRECT>(post, a.post, 0, 0, D, true, lane, G);
-  if constexpr (!GATES) load_row<T, N, DIRECT>(gate, a.gate, 0, 0, D, true, lane, G);
+  // The vectors as they multiply, in fp32 for the whole run: offset + gain, and
+  // 1 where there is none.
+  float gain[N][V], post[N][V], gate[N][V];
+  auto vector = [&](float (&to)[N][V], const T* p, int64_t row, int64_t ld, float offset) {
+    Pack<T> v[N];
+    load_row<T, N, DIRECT>(v, p, row, ld, D, true, lane, G);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int t = 0; t < V; ++t) to[k][t] = p ? offset + v[k][t] : 1.f;
+  };
+  vector(gain, a.gain, 0, 0, a.offset);
+  vector(post, a.post, 0, 0, a.offset);
+  if constexpr (!GATES) vector(gate, a.gate, 0, 0, 0.f);
   BackRow<T, N> cur;
   load(cur, first);
   for (int64_t i = 0; i < a.run; ++i) {
@@ -317,7 +330,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const double v = cur.s[k][t], q = cur.dy[k][t] * (a.offset + gain[k][t]);
+          const double v = cur.s[k][t], q = cur.dy[k][t] * gain[k][t];
           sum[0] = __builtin_fma(v, v, sum[0]);
           sum[1] = __builtin_fma(q, v, sum[1]);
         }
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
     row_total<G, 3, THREADS>(sum, buf[0]);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      cur.s[k].forget(), cur.dy[k].forget(), cur.h[k].forget(), gain[k].forget();
+      cur.s[k].forget(), cur.dy[k].forget(), cur.h[k].forget();
 #pragma unroll
       for (int t = 0; t < V; ++t) d[k][t] = cur.ds[k][t];
     }
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const float n = cur.s[k][t] * r, y = cur.dy[k][t], q = y * (a.offset + gain[k][t]);
+          const float n = cur.s[k][t] * r, y = cur.dy[k][t], q = y * gain[k][t];
           sum_gain[k * V + t] = __builtin_fmaf(y, n, sum_gain[k * V + t]);
           d[k][t] = __builtin_fmaf(r, q - n * mean, d[k][t]);
         }
@@ -355,15 +368,14 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
     if (a.h) {
       const float r = !in ? 0.f : a.post ? inverse_root(__builtin_fma(sum[2], a.over, a.eps)) : 1.f;
       const int64_t gate_row = GATES && in ? row / a.per_gate : 0;
-      if constexpr (GATES) load_row<T, N, DIRECT>(gate, a.gate, gate_row, a.ld_gate, D, true, lane, G);
+      if constexpr (GATES) vector(gate, a.gate, gate_row, a.ld_gate, 0.f);
       float g[N][V];
       double dot[1] = {0};
 #pragma unroll
       for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const float m = cur.h[k][t] * r, w = a.post ? a.offset + post[k][t] : 1.f, v = a.scale * d[k][t];
-          const float du = a.gate ? v * gate[k][t] : v;
+          const float m = cur.h[k][t] * r, w = post[k][t], v = a.scale * d[k][t], du = v * gate[k][t];
           if constexpr (GATES) {
             sum_post[k * V + t] = __builtin_fmaf(du, m, sum_post[k * V + t]);
             sum_gate[k * V + t] = __builtin_fmaf(v, m * w, sum_gate[k * V + t]);
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
         mean = (float)(dot[0] * a.over);
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) cur.h[k].forget(), post[k].forget(), gate[k].forget();
+      for (int k = 0; k < N; ++k) cur.h[k].forget();
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -414,8 +426,6 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < N; ++k) gain[k].forget();
     if constexpr (G > 64) __syncthreads();
     if constexpr (AHEAD) cur = next;
     else load(cur, row + 1);
