@@ -91,8 +91,8 @@ __device__ __forceinline__ double group_total(double v) {
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// A unit's elements in 16-byte vectors, four to a thread: f(vector index,
-// elements in it) for those that exist.
+// A unit's elements in 16-byte vectors, four to a thread; the last of them may
+// be short.
 constexpr int kVectors = kUnit / 16 / 256;
 
 __device__ __forceinline__ u32x4 load_part(const char* p, int have, bool wide) {

@@ -366,6 +366,31 @@ def test_in_place_and_shapes():
         assert torch.equal(w[over_x], flat[0]) and torch.equal(w[over_h], flat[1])
 
 
+@pytest.mark.parametrize("D", [40, 600, 4096, 9001])
+def test_outputs_over_both_inputs(D):
+    """s over x with y over h, and the other way round."""
+    gen = torch.Generator().manual_seed(12)
+    c = Case(gen, 19, D, "bf16", True, 1, True, True)
+    want = norm.forward(c.x, c.gain, **c.kw())
+    for s_over, y_over in (("x", "h"), ("h", "x")):
+        w = dict(x=c.x.clone(), h=c.h.clone())
+        got = norm.forward(w["x"], c.gain, out=w[s_over], out_norm=w[y_over], **{**c.kw(), "h": w["h"]})
+        assert got[0] is w[s_over] and got[1] is w[y_over]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_rows_too_long_are_refused():
+    x, w = torch.zeros(2, 16385, device="cuda"), torch.zeros(16385, device="cuda")
+    with pytest.raises(dc.DCError) as e:
+        norm.forward(x, w)
+    assert e.value.code == dc.DC_ERR_UNSUPPORTED
+    red = deferred.DeferredReducer(1, 20000)
+    red.acc.fill_(7.0)
+    with pytest.raises(dc.DCError):
+        red.accumulate_norm(0, x, x, w, gain_at=0)
+    assert bool((red.acc == 7).all()) and not red.open
+
+
 def test_offsets_past_32_bits():
     gen = torch.Generator().manual_seed(8)
     big = torch.zeros(33 * (1 << 26), dtype=torch.bfloat16, device="cuda").view(33, 1 << 26)
