@@ -252,6 +252,7 @@ struct RowSums {
   float* partial;  // [tiles][2][D]: of the row that came in from the tile before, of the one that goes on
   float scale;
   int32_t accumulate;
+  uint32_t sum_blocks, across;  // workgroups that add up, across the columns
 };
 
 // The first place with a key of at least `key`.
@@ -266,13 +267,12 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, 
 }
 
 // Rows that no token names become zeros: a workgroup looks at kFill of them,
-// each lane at one, and writes whole rows (92 us for 30000 x 4096 fp32, 5.4
-// TB/s; columns of 16 rows by waves of the next kernel took 139 with its sums).
+// each lane at one, and writes whole rows.
 template <class G>
-__global__ void __launch_bounds__(256) k_row_fill(RowSums a) {
+__device__ __forceinline__ void fill_rows(const RowSums& a, int64_t block, int64_t blocks) {
   constexpr int V = 16 / sizeof(G);
   const int lane = threadIdx.x & 63;
-  for (int64_t r0 = (int64_t)blockIdx.x * kFill; r0 < a.rows; r0 += (int64_t)gridDim.x * kFill) {
+  for (int64_t r0 = block * kFill; r0 < a.rows; r0 += blocks * kFill) {
     const int64_t r = r0 + lane;
     bool named = lane >= kFill || r >= a.rows;
     if (!named) {
@@ -295,14 +295,21 @@ __global__ void __launch_bounds__(256) k_row_fill(RowSums a) {
   }
 }
 
+// The first workgroups add up the tiles' rows, the others write the zero rows
+// beside them (32000 x 4096 fp32 from 8192 tokens: 101 us, 591 MB at 5.8 TB/s;
+// in two launches 92 of zeros and 23 of rows).
 template <class T, class G>
 __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
+  if (blockIdx.x >= a.sum_blocks) {
+    fill_rows<G>(a, blockIdx.x - a.sum_blocks, gridDim.x - a.sum_blocks);
+    return;
+  }
   constexpr int V = 16 / sizeof(T);  // columns per lane
   constexpr int kAhead = 32 / V;     // rows in flight
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t j = ((int64_t)blockIdx.y * 64 + lane) * V, left = a.D - j;
+  const int64_t j = ((int64_t)(blockIdx.x % a.across) * 64 + lane) * V, left = a.D - j;
   G* dtable = static_cast<G*>(a.dtable) + j;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + wave, p0 = tile * a.tile;
+  const int64_t tile = (int64_t)(blockIdx.x / a.across) * 4 + wave, p0 = tile * a.tile;
   // lanes past the last column stay: the tile's keys are held across the wave
   if (p0 >= a.n) return;
   const int have = a.n - p0 < a.tile ? (int)(a.n - p0) : a.tile;
@@ -485,11 +492,10 @@ void row_sums(const RowSums& s, int64_t tiles, hipStream_t stream) {
   RowSums a = s;
   constexpr int64_t per = 64 * (sizeof(T) == 2 ? 8 : 4);
   const uint32_t across = (uint32_t)((a.D + per - 1) / per);
-  if (!a.accumulate) {
-    const int64_t blocks = std::min<int64_t>((a.rows + kFill - 1) / kFill, (int64_t)1 << 20);
-    k_row_fill<G><<<dim3((uint32_t)blocks), 256, 0, stream>>>(a);
-  }
-  if (tiles) k_row_sums<T, G><<<dim3((uint32_t)((tiles + 3) / 4), across), 256, 0, stream>>>(a);
+  a.across = across;
+  a.sum_blocks = (uint32_t)((tiles + 3) / 4) * across;
+  const int64_t fill = a.accumulate ? 0 : std::min<int64_t>((a.rows + kFill - 1) / kFill, (int64_t)1 << 20);
+  if (a.sum_blocks + fill) k_row_sums<T, G><<<dim3((uint32_t)(a.sum_blocks + fill)), 256, 0, stream>>>(a);
   if (tiles > 1)
     k_row_join<G><<<dim3((uint32_t)((tiles + kJoinTiles - 1) / kJoinTiles), (uint32_t)((a.D + 255) / 256)), 256, 0,
                     stream>>>(a);
