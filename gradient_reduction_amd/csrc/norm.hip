@@ -386,17 +386,16 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
           dot[0] = __builtin_fma((double)g[k][t], (double)m, dot[0]);
         }
       }
-      float mean = 0.f;
-      if (a.post) {
+      if (a.post) {  // (without it g is dh, whatever stands in h)
         row_total<G, 1, THREADS>(dot, buf[1]);
-        mean = (float)(dot[0] * a.over);
+        const float mean = (float)(dot[0] * a.over);
+#pragma unroll
+        for (int k = 0; k < N; ++k) cur.h[k].forget();
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int t = 0; t < V; ++t) g[k][t] = r * (g[k][t] - cur.h[k][t] * r * mean);
       }
-#pragma unroll
-      for (int k = 0; k < N; ++k) cur.h[k].forget();
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-#pragma unroll
-        for (int t = 0; t < V; ++t) g[k][t] = r * (g[k][t] - cur.h[k][t] * r * mean);
       store_row<T, N, V, DIRECT>(g, a.dh, row, a.ld_dh, D, in, lane, G);
       if constexpr (GATES) {
         const int64_t g0 = gate_row * a.per_gate, g1 = g0 + a.per_gate;

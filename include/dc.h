@@ -1084,7 +1084,7 @@ dc_status dc_norm_backward_workspace(int32_t dtype, int64_t T, int64_t D, int64_
  *   q = (offset + gain) dy,  dx = ds + r2 (q - n mean(q n))
  *   dgain (+)= sum_t dy n
  *   v = scale gate dx,  dgate (+)= sum over the row's tokens of scale dx u
- *   g = (offset + post_gain) v,  dh = r1 (g - m mean(g m))
+ *   g = (offset + post_gain) v,  dh = r1 (g - m mean(g m))  (v without post_gain)
  *   dpost_gain (+)= sum_t v m
  * in fp32 with the means' sums in fp64, from s as it is stored; sums over
  * tokens are fp32 in an order fixed by the sizes; each output is rounded once,

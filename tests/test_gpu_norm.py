@@ -487,3 +487,19 @@ def test_into_the_deferred_reduction():
         with pytest.raises(ValueError):
             red.accumulate_norm(**{**dict(row=0), **over, **bad})
         assert torch.equal(red.acc, before) and not red.open
+
+
+@pytest.mark.parametrize("D", [40, 300, 4096, 4097, 9000])
+def test_without_a_norm_after_the_block_its_output_does_not_matter(D):
+    """dh = scale gate dx where h is not normed: infinities and NaN in h (of
+    tokens that a gate of zeros shuts out) leave it alone."""
+    gen = torch.Generator().manual_seed(D)
+    for kind in DT:
+        ds, h, gate = randn(gen, (6, D), kind), randn(gen, (6, D), kind), randn(gen, (3, D), kind)
+        h[1, 3], h[2, D - 1], h[3] = float("nan"), float("inf"), float("-inf")
+        gate[1] = 0
+        for g in (None, gate[0], gate):
+            dx, dh, *_ = norm.backward(None, ds, ds=ds, h=h, gate=g, scale=0.5, need_params=False)
+            assert torch.equal(dx, ds)
+            want = host(ds) * 0.5 * (1.0 if g is None else gate_rows(host(g), 6))
+            inside("dh", dh, want, (half_step(kind) + 2 * H) * want.abs())
