@@ -152,10 +152,17 @@ __device__ __forceinline__ void store_row(const float (&v)[N][V], T* p, int64_t 
   }
 }
 
-// 1 / sqrt(m): the hardware's where fp32 holds m well inside its range.
-__device__ __forceinline__ float inverse_root(double m) {
-  if (m > 1e-30 && m < 1e30) return __builtin_amdgcn_rsqf((float)m);
-  return (float)(1.0 / sqrt(m));
+// 1 / sqrt(m) as r lift: the hardware's root where fp32 holds m well inside its
+// range.  Of rows of subnormal values (with eps = 0) it passes fp32's range,
+// though a value times it does not: r is then kLift times smaller.
+constexpr float kLift = 4294967296.f;  // 2^32: the least rms, 2^-149 / sqrt(16384), gives r = 2^124
+struct Root {
+  float r, lift;
+};
+__device__ __forceinline__ Root inverse_root(double m) {
+  if (m > 1e-30 && m < 1e30) return {__builtin_amdgcn_rsqf((float)m), 1.f};
+  if (m < 1e-75) return {(float)(1.0 / (sqrt(m) * (double)kLift)), kLift};
+  return {(float)(1.0 / sqrt(m)), 1.f};
 }
 
 template <class T>
@@ -190,7 +197,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormIn<T> a) {
 #pragma unroll
       for (int t = 0; t < V; ++t) s[k][t] = x[k][t];
     if (a.h) {
-      float r = 1.f;
+      Root root = {1.f, 1.f};
       if (a.post) {
         double sum[1] = {0};
 #pragma unroll
@@ -201,15 +208,16 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormIn<T> a) {
             sum[0] = __builtin_fma(v, v, sum[0]);
           }
         row_total<G, 1, THREADS>(sum, buf[0]);
-        r = inverse_root(__builtin_fma(sum[0], a.over, a.eps));
+        root = inverse_root(__builtin_fma(sum[0], a.over, a.eps));
       }
+      const float scale = a.scale * root.lift;
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          float u = h[k][t] * r;
+          float u = h[k][t] * root.r;
           if (a.post) u *= a.offset + post[k][t];
-          u *= a.scale;
+          u *= scale;
           if (a.gate) u *= gate[k][t];
           s[k][t] += u;
         }
@@ -222,11 +230,11 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormIn<T> a) {
 #pragma unroll
         for (int t = 0; t < V; ++t) sum[0] = __builtin_fma((double)s[k][t], (double)s[k][t], sum[0]);
       row_total<G, 1, THREADS>(sum, buf[1]);
-      const float r = inverse_root(__builtin_fma(sum[0], a.over, a.eps));
+      const Root root = inverse_root(__builtin_fma(sum[0], a.over, a.eps));
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int t = 0; t < V; ++t) s[k][t] = s[k][t] * r * (a.offset + gain[k][t]);
+        for (int t = 0; t < V; ++t) s[k][t] = s[k][t] * root.r * root.lift * (a.offset + gain[k][t]);
       store_row<T, N, V, DIRECT>(s, a.y, row, a.ld_y, D, in, lane, G);
     }
     if constexpr (G > 64) __syncthreads();  // buf is free for the next row
@@ -353,20 +361,23 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
     }
     if (a.gain) {
       // (a row past the last one adds zeros, whatever eps is)
-      const float r = in ? inverse_root(__builtin_fma(sum[0], a.over, a.eps)) : 0.f;
-      const float mean = (float)(sum[1] * a.over * r);
+      // lifted: n is `lift` times too small, y and q that many times too large
+      const Root root = in ? inverse_root(__builtin_fma(sum[0], a.over, a.eps)) : Root{0.f, 1.f};
+      const float r = root.r, mean = (float)(sum[1] * a.over * r * (double)(root.lift * root.lift * root.lift));
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const float n = cur.s[k][t] * r, y = cur.dy[k][t], q = y * gain[k][t];
+          const float n = cur.s[k][t] * r, y = cur.dy[k][t] * root.lift, q = y * gain[k][t];
           sum_gain[k * V + t] = __builtin_fmaf(y, n, sum_gain[k * V + t]);
           d[k][t] = __builtin_fmaf(r, q - n * mean, d[k][t]);
         }
     }
     store_row<T, N, V, DIRECT>(d, a.dx, row, a.ld_dx, D, in, lane, G);
     if (a.h) {
-      const float r = !in ? 0.f : a.post ? inverse_root(__builtin_fma(sum[2], a.over, a.eps)) : 1.f;
+      // lifted: m is `lift` times too small, e, v, du and g that many times too large
+      const Root root = !in ? Root{0.f, 1.f} : a.post ? inverse_root(__builtin_fma(sum[2], a.over, a.eps)) : Root{1.f, 1.f};
+      const float r = root.r;
       const int64_t gate_row = GATES && in ? row / a.per_gate : 0;
       if constexpr (GATES) vector(gate, a.gate, gate_row, a.ld_gate, 0.f);
       float g[N][V];
@@ -375,12 +386,12 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
       for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int t = 0; t < V; ++t) {
-          const float m = cur.h[k][t] * r, w = post[k][t], v = a.scale * d[k][t], du = v * gate[k][t];
+          const float m = cur.h[k][t] * r, w = post[k][t], e = root.lift * d[k][t], v = a.scale * e, du = v * gate[k][t];
           if constexpr (GATES) {
             sum_post[k * V + t] = __builtin_fmaf(du, m, sum_post[k * V + t]);
             sum_gate[k * V + t] = __builtin_fmaf(v, m * w, sum_gate[k * V + t]);
           } else {
-            sum_post[k * V + t] = __builtin_fmaf(d[k][t], m, sum_post[k * V + t]);
+            sum_post[k * V + t] = __builtin_fmaf(e, m, sum_post[k * V + t]);
           }
           g[k][t] = du * w;
           dot[0] = __builtin_fma((double)g[k][t], (double)m, dot[0]);
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormBack<T, G_> a) {
       }
       if (a.post) {  // (without it g is dh, whatever stands in h)
         row_total<G, 1, THREADS>(dot, buf[1]);
-        const float mean = (float)(dot[0] * a.over);
+        const float mean = (float)(dot[0] * a.over * (double)(root.lift * root.lift));
 #pragma unroll
         for (int k = 0; k < N; ++k) cur.h[k].forget();
 #pragma unroll

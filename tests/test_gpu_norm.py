@@ -503,3 +503,50 @@ def test_without_a_norm_after_the_block_its_output_does_not_matter(D):
             assert torch.equal(dx, ds)
             want = host(ds) * 0.5 * (1.0 if g is None else gate_rows(host(g), 6))
             inside("dh", dh, want, (half_step(kind) + 2 * H) * want.abs())
+
+
+@pytest.mark.parametrize("D", [40, 300, 2500, 6000, 9001])
+@pytest.mark.parametrize("kind", DT)
+def test_subnormal_rows(kind, D):
+    """With eps = 0 a row of subnormal values has a factor 1 / rms past fp32's
+    range, and values of order 1 all the same.  Bounds as above; a gradient
+    through such a row is rounded to fp32 or bf16 once more."""
+    gen = torch.Generator().manual_seed(D)
+    T, step = 5, half_step(kind)
+    unit = randn(gen, (T, D), "f32", 1.0)
+    sizes = torch.tensor([1.0, 3e-40, 2e-39, 1e-39 if kind == "bf16" else 4e-42, 1e-38], dtype=torch.float64)
+    tiny = (unit.double() * sizes.cuda()[:, None]).to(DT[kind])
+    tiny[:, D // 2] = 0
+    w, wp = randn(gen, (D,), kind, 0.1, 1.0), randn(gen, (D,), kind, 0.1, 1.0)
+    v = host(tiny)
+    rms = mean(v * v).sqrt()
+    n = v / rms
+    _, y = norm.forward(tiny, w, eps=0.0)
+    want = n * host(w)
+    inside("y", y, want, 12 * H * want.abs() + step * want.abs() * 1.01)
+    s, y = norm.forward(torch.zeros_like(tiny), w, h=tiny, post_gain=wp, eps=0.0)
+    want = n * host(wp)
+    inside("s", s, want, 12 * H * want.abs() + step * want.abs() * 1.01)
+    # every gradient so small that 1 / rms times it stays in range
+    dy, gates = randn(gen, (T, D), kind, 2.0 ** -30), randn(gen, (T, D), kind)
+    dx, _, dgain, _, _ = norm.backward(dy, tiny, w, eps=0.0)
+
+    def through(g):
+        return (g - n * mean(g * n)) / rms, 24 * H * (g.abs() + n.abs() * mean((g * n).abs())) / rms
+
+    want, err = through(host(dy) * host(w))
+    inside("dx", dx, want, err + step * (want.abs() + err))
+    terms = host(dy) * n
+    inside("dgain", dgain, terms.sum(0), 60 * H * terms.abs().sum(0))
+    ds = randn(gen, (T, D), kind, 2.0 ** -30)
+    for gate in (None, gates):
+        dx, dh, _, dpost, dgate = norm.backward(None, ds, ds=ds, h=tiny, post_gain=wp, gate=gate, eps=0.0)
+        assert torch.equal(dx, ds)
+        v = host(ds) * (1.0 if gate is None else host(gate))
+        want, err = through(v * host(wp))
+        inside("dh", dh, want, err + step * (want.abs() + err))
+        terms = v * n
+        inside("dpost", dpost, terms.sum(0), 60 * H * terms.abs().sum(0))
+        if gate is not None:
+            want = host(ds) * n * host(wp)
+            inside("dgate", dgate, want, 20 * H * want.abs())
