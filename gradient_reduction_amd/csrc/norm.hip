@@ -487,7 +487,9 @@ __global__ void __launch_bounds__(256) k_norm_join(NormJoin<T, G_> a) {
   }
 }
 
-// Gate rows that reach over runs: their parts in order.  (No tokens: zeros.)
+// Gate rows that reach over runs: their parts in order, in fp64, so that
+// thousands of them (narrow rows have runs of one or two) add no error that grows with
+// their number.  (No tokens: zeros.)
 template <class G_>
 __global__ void __launch_bounds__(256) k_gate_join(int64_t D, int64_t T_, int64_t rows, int64_t run, int64_t per_gate,
                                                    const float* partial, G_* dgate, int64_t ld, int32_t accumulate) {
@@ -496,13 +498,13 @@ __global__ void __launch_bounds__(256) k_gate_join(int64_t D, int64_t T_, int64_
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
     const int64_t g0 = row * per_gate, r0 = g0 / run, r1 = (g0 + per_gate - 1) / run;
     if (T_ && r0 == r1) continue;
-    float v = 0.f;
+    double v = 0;
     if (T_) {
 #pragma unroll 8
       for (int64_t r = r0; r <= r1; ++r) v += partial[(r * 2 + (r == r0 ? 1 : 0)) * D + j];
     }
     G_* to = dgate + row * ld + j;
-    *to = (G_)(accumulate ? (float)*to + v : v);
+    *to = (G_)(float)(accumulate ? (double)(float)*to + v : v);
   }
 }
 

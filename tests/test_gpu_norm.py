@@ -550,3 +550,27 @@ def test_subnormal_rows(kind, D):
         if gate is not None:
             want = host(ds) * n * host(wp)
             inside("dgate", dgate, want, 20 * H * want.abs())
+
+
+@pytest.mark.parametrize("size", [(16384, 64, 2), (16384, 64, 12), (4000, 74, 8), (4000, 300, 2), (9000, 1100, 3)],
+                         ids=str)
+@pytest.mark.parametrize("kind", DT)
+def test_gate_sums_do_not_drift(size, kind):
+    """Sums of many equal terms, whose roundings all fall to one side.  A part is
+    one run's: a fused add and a product's rounding for each of its few rows.
+    Parts are added in 64 bits, so that the bound does not grow with their
+    number: (2 run + 4) 2^-24 of the sum, and half a step of bf16's own values
+    nowhere, as these are exact.  Runs are as in the library: one workgroup of
+    512 threads a compute unit, 16, 64 or 256 threads to a row."""
+    T, D, gates = size
+    T = T // gates * gates
+    gen = torch.Generator().manual_seed(D)
+    ds = (0.3 + torch.rand(1, D, generator=gen)).to(DT[kind]).expand(T, D).contiguous().cuda()
+    h = (0.7 + torch.rand(1, D, generator=gen)).to(DT[kind]).expand(T, D).contiguous().cuda()
+    gate = torch.ones(gates, D, dtype=DT[kind], device="cuda")
+    dgate = norm.backward(None, ds, ds=ds, h=h, gate=gate)[4]
+    n = 16 if kind == "bf16" else 8
+    threads = 16 if D <= 16 * n else 64 if D <= 64 * n else 256
+    run = -(-T // (256 * 512 // threads))
+    want = (host(ds) * host(h))[:1] * (T // gates)
+    inside("dgate", dgate, want.expand(gates, D), (2 * run + 4) * H * want.abs())
