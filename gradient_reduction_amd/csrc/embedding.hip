@@ -358,13 +358,14 @@ __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
 
 // A row whose tokens reach over tiles: the wave of the tile in which it ends
 // adds up its partial sums, kJoin loads in flight; with more than a few of
-// them the workgroup's four waves take a run each.
+// them the workgroup's four waves take a run each.  In fp64: a token of half a
+// batch has thousands of parts, and in fp32 the error grew with their number.
 constexpr int kJoin = 8;
 
 template <class G>
 __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
   constexpr int V = 4;
-  __shared__ float part[4][64][V];
+  __shared__ double part[4][64][V];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t tiles = (a.n + a.tile - 1) / a.tile, base = (int64_t)blockIdx.x * kJoinTiles;
   // lane i looks at the tile base + i: whether a row that came in ends there
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
     const int64_t per = alone ? parts : (parts + 3) / 4, k0 = alone ? 0 : wave * per;
     const int64_t k1 = k0 + per < parts ? k0 + per : parts;
     G* to = static_cast<G*>(a.dtable) + (int64_t)key * a.ld + j;
-    float sum[V] = {}, y[V] = {};
+    double sum[V] = {};
+    float y[V] = {};
     if (a.accumulate && (alone || wave == 0)) load_columns<G, V>(to, left, y);
     for (int64_t k = k0; k < k1; k += kJoin) {
       float v[kJoin][V];
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(256) k_row_join(RowSums a) {
       for (int t = 0; t < V; ++t) sum[t] = (part[0][lane][t] + part[1][lane][t]) + (part[2][lane][t] + part[3][lane][t]);
     }
 #pragma unroll
-    for (int t = 0; t < V; ++t) y[t] = a.scale * sum[t] + y[t];
+    for (int t = 0; t < V; ++t) y[t] = (float)((double)a.scale * sum[t] + (double)y[t]);
     store_columns<G, V>(to, left, y);
   }
 }

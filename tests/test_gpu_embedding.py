@@ -274,3 +274,22 @@ def test_into_the_deferred_reduction():
         with pytest.raises(ValueError):
             red.accumulate_embedding(**a)
         assert torch.equal(red.acc.nan_to_num(), before.nan_to_num()) and not red.open
+
+
+@pytest.mark.parametrize("size", [(1 << 17, 9, 4), (1 << 20, 5, 6), (70000, 3, 257)], ids=str)
+@pytest.mark.parametrize("kind", DT)
+def test_sums_of_a_frequent_token_do_not_drift(size, kind):
+    """Many equal terms, whose roundings all fall to one side: at most 32 tokens
+    are added up in fp32, their sums in 64 bits, so that the bound does not grow
+    with the tokens: (32 + 4) 2^-24 of the sum."""
+    T, V, D = size
+    gen = torch.Generator().manual_seed(D)
+    one = (1.0 + torch.rand(1, D, generator=gen)).to(DT[kind])
+    dy = one.cuda().expand(T, D).contiguous()
+    ids = torch.full((T,), V - 1, device="cuda")
+    for acc in (False, True):
+        old = torch.zeros(V, D, device="cuda")
+        got = embedding.backward(dy, ids, dtable=old, accumulate=acc)
+        want = one.double() * T
+        inside(got[V - 1:], want, 36 * HALF * want.abs())
+        assert not got[:V - 1].any()
