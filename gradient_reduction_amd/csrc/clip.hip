@@ -204,7 +204,8 @@ __device__ __forceinline__ float factor(double squares, float max_norm, float ep
 // Every workgroup folds the partial sums by itself (16 KB from the caches) or
 // takes the given sum, then scales its units.  The list has the gradients in
 // reverse order, and each is gone through from its end.  `before`: units of
-// earlier launches.  A factor of 1 in place leaves nothing to do.
+// earlier launches.  A factor of 1 leaves nothing to do in place (in_place: the
+// whole list is).
 template <class List>
 __global__ void __launch_bounds__(256) k_clip(List l, int64_t before, const double* partial, int32_t parts,
                                               const double* squares, float max_norm, float eps, float* norm,
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(256) k_clip(List l, int64_t before, const doub
   for (int32_t u = blockIdx.x; u < units; u += gridDim.x) {
     while (l.begin[e + 1] <= u) ++e;
     const Unit t = unit_at(l, e, l.begin[e] + l.begin[e + 1] - 1 - u);
+    if (t.out == t.grad && c == 1.f) continue;
     u32x4 v[kVectors];
     load_unit(t, before + u > kCached, v);
     const int V = t.wide ? 4 : 8;

@@ -318,3 +318,18 @@ def test_after_the_deferred_reduce(rows):
         a = {**dict(out=out, ld_out=red.ld, max_norm=1.0, out_rows=rows), **bad}
         with pytest.raises(ValueError):
             red.clip(**a)
+
+
+def test_a_factor_of_one_leaves_what_is_in_place():
+    """Gradients in place beside others that are copied: the former keep every
+    bit, a NaN's own among them (the norm comes from elsewhere)."""
+    for kind, ints, nan in (("bf16", torch.int16, 0x7f85), ("f32", torch.int32, 0x7f800005)):
+        g = torch.randn(9001, device="cuda").to(DT[kind])
+        g.view(ints)[[0, 4500, 9000]] = nan
+        other = torch.randn(300, device="cuda")
+        bits, out = g.view(ints).clone(), torch.zeros(300, device="cuda")
+        squares = torch.ones(1, dtype=torch.float64, device="cuda")
+        for k, (gs, outs) in enumerate((([g, other], [g, out]), ([other, g], [out, g]))):
+            out.zero_()
+            assert clip.clip_grad_norm(gs, 3.0, out=outs, squares=squares).item() == 1.0
+            assert torch.equal(out, other) and torch.equal(g.view(ints), bits), k
