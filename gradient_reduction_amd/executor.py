@@ -544,7 +544,8 @@ class Zero1FlushExecutor:
             eb = 2 if self.dtype == dc.DC_BF16 else 4
             have = slab_out.untyped_storage().nbytes() - slab_out.storage_offset() * slab_out.element_size()
             end = int((recs["grad"] + recs["cols"].astype(np.uint64) * np.uint64(eb)).max()) if len(recs) else 0
-            if slab_out.element_size() != eb or slab_out.device != self.d_owner.device or end > have:
+            dtype = self.torch.bfloat16 if self.dtype == dc.DC_BF16 else self.torch.float32
+            if slab_out.dtype != dtype or slab_out.device != self.d_owner.device or end > have:
                 raise ValueError(f"slab_out {tuple(slab_out.shape)} of {slab_out.dtype} on {slab_out.device} "
                                  f"with ld_out={ld_out} does not hold every bucket")
         recs["grad"] += np.uint64(base)

@@ -333,3 +333,35 @@ def test_a_factor_of_one_leaves_what_is_in_place():
             out.zero_()
             assert clip.clip_grad_norm(gs, 3.0, out=outs, squares=squares).item() == 1.0
             assert torch.equal(out, other) and torch.equal(g.view(ints), bits), k
+
+
+@pytest.mark.parametrize("mode", ["owner", "all", "zero2"])
+def test_after_a_flush_in_bf16(mode):
+    """The slab that a flush leaves in bf16, with odd columns and sizes: every
+    reduced element counts once and every row that holds it is scaled."""
+    sizes = [901, 3, 1201, 0, 77, 2501, 641, 31, 1, 4001, 513, 87]
+    w = wl.custom_flush("clip16", 4, wl.DT_BF16, sizes, capacity=4003, pre_div=1)
+    ex = executor.from_workload(w, reduce_to_owner=mode == "owner", zero2=mode == "zero2")
+    ex.build_owner_map()
+    gen = torch.Generator().manual_seed(11)
+    slab = gradient(gen, (4, w.ld), "bf16")
+    out = torch.zeros(4, w.ld, dtype=torch.bfloat16, device="cuda")
+    for b in range(len(w.buckets)):
+        ex.flush(b, slab, w.ld, out, w.ld)
+    before = out.cpu()
+    squares = (before.double().abs().amax(0) ** 2).sum()
+    for part in (0.5, 0.25, 2.0):
+        want_norm = float(squares) ** 0.5
+        got = ex.clip_gradients(out, w.ld, part * want_norm)
+        assert abs(got.item() - want_norm) <= want_norm * 2 * HALF
+        c = min(1.0, float(np.float32(part * want_norm)) / (want_norm + float(np.float32(1e-6))))
+        want = before.double() * c
+        err = want.abs() * 3 * HALF
+        assert bool(((out.cpu().double() - want).abs() <= err + 2.0 ** -134 + (want.abs() + err) * 2.0 ** -8).all())
+        assert torch.equal(out.cpu() != 0, before != 0)
+        out.copy_(before)
+    for bad in (out.view(torch.float16), out.view(torch.int16), out.float()):
+        kept = bad.view(torch.uint8).clone()
+        with pytest.raises(ValueError):
+            ex.clip_gradients(bad, w.ld, 1.0)
+        assert torch.equal(bad.view(torch.uint8), kept)
