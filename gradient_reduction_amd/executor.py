@@ -71,7 +71,8 @@ class Zero1FlushExecutor:
         self.d_part_size = torch.empty(self.G, dtype=torch.int64, device=dev)
         self.d_pid_off = torch.empty(self.P + 1, dtype=torch.int32, device=dev)
         self.d_pids = torch.empty(max(self.pids_capacity, 1), dtype=torch.int32, device=dev)
-        self.d_owner = torch.empty(max(self.P, 1), dtype=torch.int32, device=dev)
+        # (no build leaves a -2: a map that was only recorded is told from one that was built)
+        self.d_owner = torch.full((max(self.P, 1),), -2, dtype=torch.int32, device=dev)
         self.d_counts = torch.empty(2 * self.G, dtype=torch.int32, device=dev)
         # one device task table for all buckets, bucket b at rows [t_begin[b], t_begin[b+1])
         self.h_tasks = [dc.tasks_array(b.tasks) for b in self.buckets]
@@ -525,14 +526,20 @@ class Zero1FlushExecutor:
         norm counts every reduced element once: on its owner's row (or its
         partition's), an AllReduced one on the first row that holds it, one of a
         sub-communicator once in each of its blocks, whose sums differ; every row
-        that holds one is scaled.  Comes after build_owner_map; the first call
-        for a row stride reads the map back and synchronizes."""
+        that holds one is scaled.  Comes after build_owner_map (or a replay of its
+        recording); the first call for a row stride reads the map back and
+        synchronizes.  What it finds is kept: the map depends on nothing but what
+        the executor was made with, and building it again changes nothing."""
         from . import clip
         if (self.reduce_to_owner or self.zero2) and not self.map_built:
             raise RuntimeError("clip_gradients() before build_owner_map()")
         if ld_out not in self.clip_recs:
-            if (self.reduce_to_owner or self.zero2) and self.h_owner is None:
-                self.fetch_metadata()
+            if self.reduce_to_owner or self.zero2:
+                if self.h_owner is None:
+                    self.fetch_metadata()
+                if self.P and self.h_owner.min() < -1:
+                    self.h_owner = self._h_psize = None      # read again when it is built
+                    raise RuntimeError("clip_gradients() before the recorded build_owner_map() has run")
             ends = [bk.col + bk.numel for bk in self.buckets]
             if ends and ld_out < max(ends):
                 raise ValueError(f"ld_out={ld_out} is less than a row with every bucket ({max(ends)})")

@@ -365,3 +365,28 @@ def test_after_a_flush_in_bf16(mode):
         with pytest.raises(ValueError):
             ex.clip_gradients(bad, w.ld, 1.0)
         assert torch.equal(bad.view(torch.uint8), kept)
+
+
+@pytest.mark.parametrize("mode", ["owner", "zero2"])
+def test_after_a_recorded_flush(mode):
+    """A step that is only recorded has built no owner map: refused; after its
+    replay the slab is clipped as after an eager flush."""
+    w = wl.custom_flush("clip", 4, wl.DT_F32, [900, 3, 1200, 77, 2500, 31], capacity=4000, pre_div=1)
+    gen = torch.Generator().manual_seed(12)
+    slab = gradient(gen, (4, w.ld), "f32")
+    outs, norms = [], []
+    for recorded in (False, True):
+        ex = executor.from_workload(w, reduce_to_owner=mode == "owner", zero2=mode == "zero2")
+        out = torch.zeros(4, w.ld, device="cuda")
+        if recorded:
+            graph = ex.capture_step(slab, w.ld, out, w.ld)
+            with pytest.raises(RuntimeError):
+                ex.clip_gradients(out, w.ld, 1.0)
+            graph.replay()
+        else:
+            ex.build_owner_map()
+            for b in range(len(w.buckets)):
+                ex.flush(b, slab, w.ld, out, w.ld)
+        norms.append(ex.clip_gradients(out, w.ld, 1.0))
+        outs.append(out)
+    assert torch.equal(norms[0], norms[1]) and norms[0].item() > 1 and torch.equal(outs[0], outs[1])
