@@ -103,6 +103,8 @@ class DeferredReducer:
         elements offset .. offset + rows D of the row; otherwise as
         accumulate_linear.  A table that is the output's too is given to both."""
         from . import embedding, linear
+        if dy.dim() < 1 or rows < 1:
+            raise ValueError(f"dy of shape {tuple(dy.shape)} for a table of {rows} rows")
         dtable = self._place(row, offset, rows * dy.shape[-1]).view(rows, dy.shape[-1])
         with linear.on(self.acc.device, stream):
             _, launch = embedding._backward(dy, ids, rows, scale, dtable, True, None)

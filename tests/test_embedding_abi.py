@@ -92,3 +92,16 @@ def test_refused_before_anything_is_launched(monkeypatch):
         assert not seen and bool((d.acc == 7).all()) and not d.open
     d.accumulate_embedding(0, 3, dy, ids, 6)
     assert len(seen) == 1 and d.open and not d.acc[0].any() and bool((d.acc[1] == 7).all())
+
+
+def test_a_gradient_without_columns_is_refused():
+    d = deferred.DeferredReducer(2, 100, device="cpu")
+    ids = torch.zeros((), dtype=torch.int64)
+    for rows in (6, 0, -1):
+        with pytest.raises(ValueError):
+            d.accumulate_embedding(0, 3, torch.zeros(()), ids, rows)
+    for rows in (0, -1):
+        with pytest.raises(ValueError):
+            d.accumulate_embedding(0, 3, torch.zeros(4, 5), torch.zeros(4, dtype=torch.int64), rows)
+        with pytest.raises(ValueError):
+            embedding.backward(torch.zeros(4, 5), torch.zeros(4, dtype=torch.int64), rows=rows)
