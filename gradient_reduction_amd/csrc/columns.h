@@ -41,9 +41,8 @@ __device__ __forceinline__ void load_columns(const T* p, int64_t left, float (&v
   for (int t = 0; t < V; ++t) v[t] = (float)x[t];
 }
 
-// V values rounded to T; columns past `left` are not written.  WHOLE: `left` is
-// never between 0 and V.
-template <class T, int V, bool WHOLE = false>
+// V values rounded to T; columns past `left` are not written.
+template <class T, int V>
 __device__ __forceinline__ void store_columns(T* p, int64_t left, const float (&v)[V]) {
   constexpr int B = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = B / sizeof(T);
   using A = typename Access<B>::type;
@@ -57,7 +56,7 @@ __device__ __forceinline__ void store_columns(T* p, int64_t left, const float (&
       __builtin_memcpy(&w, x + k * N, B);
       *reinterpret_cast<A*>(p + k * N) = w;
     }
-  } else if constexpr (!WHOLE) {
+  } else {
 #pragma unroll
     for (int t = 0; t < V; ++t)
       if (t < left) p[t] = x[t];
@@ -78,12 +77,10 @@ struct Pack {
   __device__ __forceinline__ void forget() {
     if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(w));
   }
-  // WHOLE: `left` is never between 0 and V.
-  template <bool WHOLE = false>
   __device__ __forceinline__ void load(const T* p, int64_t left) {
     w = u32x4{0, 0, 0, 0};
     if (left >= V) w = *reinterpret_cast<const u32x4_any*>(p);
-    if (WHOLE || left >= V) return;
+    if (left >= V) return;
 #pragma unroll
     for (int t = 0; t < V; ++t)
       if (t < left) {
