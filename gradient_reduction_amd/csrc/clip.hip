@@ -8,9 +8,9 @@
 // workgroups take units in turn and keep their place in the list.
 //
 // Bound by the bytes: 2 GiB of fp32 or bf16 are read at 5.9 TB/s; 100M bf16
-// take 34 us and, scaled from the cache, 66 more; 395M fp32 847 in all, 5.6
-// TB/s.  Units of 8 and 32 KB took 4% and 6% more on those.  113 vectors: 5.7
-// and 5.0 us.
+// take 34 us and 66 more to be scaled (6.1 TB/s read and written); 395M fp32
+// 840 in all, 5.6 TB/s.  Units of 8 and 32 KB took 4% and 6% more on those.
+// 113 vectors: 5.5 and 5.3 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -145,7 +145,9 @@ __device__ __forceinline__ int find_entry(const List& l, int32_t u) {
 // The squares are summed from the list's beginning to its end and the
 // gradients scaled from its end to its beginning: what was read last is then
 // still in the 256 MB cache.  Units further than kCached from the end are
-// streamed both times, past what is kept.
+// streamed both times, past what is kept: 100M bf16 118 to 103 us, 395M fp32 889
+// to 844.  (How much of the second read the cache serves was not measured; a
+// copy of as many bytes from HBM takes 59 of the 66 us.)
 constexpr int64_t kCached = ((int64_t)192 << 20) / kUnit;
 
 // partial[workgroup] (+)= the squares of its units.  `after`: units that later

@@ -8,9 +8,13 @@
 // row whose tokens reach over tiles leaves one partial sum in each, which a
 // second launch adds up in order; a frequent token is so spread over the chip.
 //
+// The sort is a least-significant-digit radix sort with ranks from ballots.
+//
 // 32768 tokens of a natural text's frequencies in a table of 151936 x 1024,
 // bf16 added to fp32: sort 22 us (two passes, each of a count and a pass),
-// rows 30 (167 MB, 5.6 TB/s), join 7.  Lookup of the same: 20, 4.6 TB/s.
+// rows 30 (167 MB, 5.6 TB/s), join 7.  Lookup of the same: 20, 4.6 TB/s.  With
+// half of the tokens one id of a 32000 x 1024 table, 84 in all where 64 are taken
+// without: the join of 512 tiles.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -67,7 +71,11 @@ constexpr int kMostBits = 10;                 // of a pass
 constexpr int kDigits = 1 << kMostBits;
 // (Workgroups of 1024, 2048 and 4096 tokens: 32768 take 69, 68 and 73 us with
 // all that follows.)
-constexpr int kSortSelf = 16;                 // tiles up to which every workgroup adds the counts up by itself
+// Tiles up to which every workgroup adds the counts up by itself; for more a
+// launch of its own does (that from 2 on, and 64 at once: 32768 tokens x 1024 68
+// and 67 us where 16 take 64; 65536 x 1024 99 and 98, 16 99; 131072 x 512 103 and 98,
+// 16 102).
+constexpr int kSortSelf = 16;
 
 template <class Id>
 __device__ __forceinline__ uint32_t key_of(Id id, uint32_t rows) {
@@ -237,8 +245,13 @@ __global__ void __launch_bounds__(1024) k_sort_tile(SortPasses s, const Id* ids)
 // ---------------------------------------------------------------------------
 // Sums of rows.
 // ---------------------------------------------------------------------------
-constexpr int kJoinTiles = 4;  // tiles that a workgroup of the join looks at
-constexpr int kFill = 8;   // rows of dE that a workgroup of the fill looks at
+// Tiles that a workgroup of the join looks at (2 and 16: 32768 tokens x 1024 65 and 68
+// us where 4 take 64; 1511 x 515 24 and 28, 4 24; half of the tokens one id 74 and
+// 76, 4 84).
+constexpr int kJoinTiles = 4;
+// Rows of dE that a workgroup of the fill looks at (2 and 32: 32000 x 4096
+// 132 and 135 us where 8 take 130).
+constexpr int kFill = 8;
 
 struct RowSums {
   int64_t n, rows, D;
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(256) k_row_sums(RowSums a) {
 // adds up its partial sums, kJoin loads in flight; with more than a few of
 // them the workgroup's four waves take a run each.  In fp64: a token of half a
 // batch has thousands of parts, and in fp32 the error grew with their number.
-constexpr int kJoin = 8;
+constexpr int kJoin = 8;  // (4 and 16: 64 and 67 us where 8 take 64; 65536 tokens 101 and 104, 8 99)
 
 template <class G>
 __global__ void __launch_bounds__(256) k_row_join(RowSums a) {

@@ -8,14 +8,16 @@
 //   dx = d,  du = scale gate d,  dgate (+)= sum_t scale d u
 //   m = h r1,  g = (offset + post) du:   dh = r1 (g - m mean(g m)),      dpost (+)= sum_t du m
 //
-// A row is held in the registers of G threads, 16 values each, so every input
-// is read once.  Sums over a row are fp64, so that squares of any fp32 value
+// A row is held in the registers of G threads, so every input is read once:
+// forward 16 values each, backward 32 bytes of each operand (64 of fp32 rows of
+// more than 8192).  Sums over a row are fp64, so that squares of any fp32 value
 // neither overflow nor vanish.
 //
 // 8192 rows of 4096 bf16: forward 39 us (268 MB, 6.9 TB/s, bound by HBM);
-// backward 75 to 79 and 5 for the join (403 MB, 5.1 to 5.4 TB/s), where the
-// arithmetic of some 750 instructions a wave and row (sums in fp64 among them)
-// takes as long as the bytes and two waves a SIMD do not hide all of it.
+// backward 74 to 79 and 5 for the join (403 MB, 5.1 to 5.4 TB/s), where the
+// arithmetic of some 1000 instructions a wave and row (190 in fp64 and 83
+// conversions to it) takes as long as the bytes and two waves a SIMD do not
+// hide all of it.
 // Tried: 8 values a thread instead of 16, twice the waves to a row, 111 to 119;
 // one sum over the lanes in place of two (three more fp64 products a value in
 // place of a second exchange), 95.
@@ -288,7 +290,8 @@ struct BackRow {
 
 // Every row group takes a run of neighbouring rows and keeps the column sums of
 // the parameters' gradients in registers; the next row's loads are under way
-// while a row is worked on (bf16; fp32 rows fill the registers).  GATES: the
+// while a row is worked on (not in workgroups of 1024: their threads have 128
+// registers, and spill without it already).  GATES: the
 // gate has several rows; its sums are handed out where a gate row ends.
 // Without, sum_t d m is kept, which gives dpost and dgate both (k_norm_join).
 template <class T, class G_, int G, int EACH, int THREADS, bool GATES, bool DIRECT>
@@ -508,9 +511,16 @@ __global__ void __launch_bounds__(256) k_gate_join(int64_t D, int64_t T_, int64_
   }
 }
 
-// Threads per row.  Backward a thread takes 32 bytes of a row of each operand
-// (64 for fp32 rows of more than 8192), and a workgroup 512 threads: two waves
-// a SIMD, whose 256 registers hold two rows' operands and the sums.
+// Threads per row: the fewest of a few steps that hold it.  Forward a thread
+// takes 16 values (with four times the threads 65536 rows of 256 bf16 took 53 us
+// for 29, 32768 of 1024 93 for 45, 8192 of 4096 143 for 44; fp32 59 for 45, 110
+// for 81, 167 for 80).  Between the steps lanes are left without columns: as
+// many bytes in rows of 2048 take 63 us, of 5120 118, of 8192 80, of 4096 45.
+// Backward a thread takes 32 bytes of a row of each operand (64 for fp32 rows of
+// more than 8192), and a workgroup 512 threads: two waves a SIMD, whose 256
+// registers hold two rows' operands and the sums (bf16 with the next step's
+// threads: 65536 x 256 95 us for 53, 32768 x 1024 205 for 85, 8192 x 4096 119 for
+// 80, 4096 x 8192 632 for 88).
 int row_threads(int64_t D) { return D <= 256 ? 16 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
 int back_row_threads(int32_t dtype, int64_t D) {
   const int64_t n = dtype == DC_BF16 ? 16 : 8;
@@ -519,7 +529,9 @@ int back_row_threads(int32_t dtype, int64_t D) {
 constexpr int back_threads(int g) { return g > 512 ? g : 512; }
 
 // Runs of the backward: about one workgroup a compute unit, each row group
-// with as few rows as that leaves.
+// with as few rows as that leaves (half and twice as many workgroups: 8192 x
+// 4096 bf16 119 and 86 us where 256 take 80, 65536 x 256 69 and 67 for 53, 4096 x
+// 4096 fp32 97 and 80 for 77).
 constexpr int64_t kBlocks = 256;
 struct Runs {
   int64_t rows, count, blocks;

@@ -983,7 +983,8 @@ dc_status dc_muon_update(int32_t dtype, int32_t weight_dtype, int32_t hold,
  * and
  *   c = n + eps <= max_norm ? 1 : max_norm / (n + eps),   out = c g
  * over all rows.  Squares and sums are fp64, in an order fixed by the list's sizes and
- * strides; c is rounded once to fp32, c g to fp32 and then to the dtype.  An infinity among the counted
+ * strides; c is rounded once to fp32 (under 2^-126 to the bits that are left
+ * there), c g to fp32 and then to the dtype.  An infinity among the counted
  * gradients gives c = 0 (and NaN where it stands), a NaN gives NaN throughout:
  * read *norm to pass such a step over.  Rules of the section above hold, with
  * 2^36 elements per gradient and 2^44 per row stride. */
@@ -1033,8 +1034,8 @@ dc_status dc_embedding_backward_workspace(int32_t dtype, int64_t T, int64_t rows
 
 /* The table's gradient:
  *   dE[v] = (accumulate ? dE[v] : 0) + scale sum over {t: ids[t] = v} of dy[t]
- * in fp32, every row's sum in the order of its tokens (in parts fixed by the
- * ids, added in order), rounded once.  With accumulate, rows that no id names are neither
+ * in fp32, every row's sum in the order of its tokens (in parts of up to 32
+ * tokens fixed by the ids, added in order in fp64), rounded once.  With accumulate, rows that no id names are neither
  * read nor written; without it they become zeros.  An id outside [0, rows)
  * gives nothing.  With accumulate and DC_F32, dE is a parameter's place in a
  * replica's accumulator row ([MT] What: micro-batch gradients add up locally).
@@ -1057,7 +1058,8 @@ dc_status dc_embedding_backward(int32_t dtype, int32_t id_bytes, int64_t T, int6
  *   s[t] = x[t] + scale gate[t / (T / gate_rows)] u[t]
  *   y[t] = (offset + gain) s[t] / sqrt(mean(s[t]^2) + eps)
  * in fp32 with the means' sums in fp64, s and y each rounded once (y from the
- * s before its rounding).  What is NULL falls away: without post_gain u = h, without gate it is 1,
+ * s before its rounding); with eps = 0 rows of subnormal values are normed like
+ * others, and a row of zeros gives NaN.  What is NULL falls away: without post_gain u = h, without gate it is 1,
  * without h s = x, without gain there is no y; h or gain is needed, and h for
  * post_gain and gate.
  *   x, ld_x          device [T, ld_x]: the residual stream
@@ -1087,7 +1089,8 @@ dc_status dc_norm_backward_workspace(int32_t dtype, int64_t T, int64_t D, int64_
  *   g = (offset + post_gain) v,  dh = r1 (g - m mean(g m))  (v without post_gain)
  *   dpost_gain (+)= sum_t v m
  * in fp32 with the means' sums in fp64, from s as it is stored; sums over
- * tokens are fp32 in an order fixed by the sizes; each output is rounded once,
+ * tokens are fp32 in an order fixed by the sizes (the parts that a gate row's
+ * sum may come in are added in fp64); each output is rounded once,
  * dx and dh from the same unrounded dx.
  *   dy, ld_dy        device [T, ld_dy]: y's gradient; read with gain
  *   ds, ld_ds        device [T, ld_ds] or NULL (0): what reaches s from later
